@@ -80,6 +80,17 @@ def load_library() -> ctypes.CDLL:
         for fn in (lib.attn_bwd, lib.attn_bwd_causal):
             fn.restype = i32
             fn.argtypes = [vp] * 9 + [i32, i32, i32, i32, i32, f32, i32, vp]
+        i64 = ctypes.c_int64
+        lib.attn_fwd_packed.restype = i32
+        lib.attn_fwd_packed.argtypes = [vp] * 7 + [i32] * 7 + [i64] * 3 + [f32, i32, i32, vp]
+        lib.attn_chunk_paged.restype = i32
+        lib.attn_chunk_paged.argtypes = [vp] * 8 + [i32] * 9 + [i64, f32, i32, i32, vp]
+        lib.attn_paged_plan.restype = i32
+        lib.attn_paged_plan.argtypes = [vp] * 9 + [i32] * 4 + [i64, vp]
+        lib.attn_paged_write.restype = i32
+        lib.attn_paged_write.argtypes = [vp] * 5 + [i64] + [i32] * 4 + [i64] * 2 + [i32, vp]
+        lib.attn_debug_packed_plan.restype = i32
+        lib.attn_debug_packed_plan.argtypes = [vp, vp] + [i32] * 8 + [vp]
         lib.attn_decode_splitkv_noalloc.restype = i32
         lib.attn_decode_splitkv_noalloc.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
                                                     f32, i32, i32, vp]
@@ -351,6 +362,206 @@ def attn_bwd(q, k, v, o, lse, dout, scale: float | None = None, dq=None, dk=None
     return dq, dk, dv
 
 
+def _rows(name, t, idx, dt):
+    """Token stride of packed rows [tokens, heads, d] whose heads lie side by
+    side (a tensor of their own, or a slice of wider rows)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, d]")
+    if t.dtype is not dt:
+        raise TypeError("q, k, v must share one dtype")
+    if t.get_device() != idx:
+        raise ValueError(f"{name} must be on q's device")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != d and h != 1) or (s0 < h * d and n != 1) or s0 % 8:
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: heads must lie d apart within a token's row, and rows a multiple of 8 apart")
+    # a lone row has no distance to the next
+    return s0 if n != 1 and s0 >= h * d else h * d
+
+
+def _int_array(name, t, shape, idx, dtype=torch.int32):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != idx \
+            or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor {list(shape)} on the same device")
+
+
+def _packed_q(q, cu_seqlens_q, out, lse):
+    """Sizes, dtype code, device index and token stride of packed query rows,
+    with their outputs."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
+        raise ValueError("q must be a CUDA tensor [total_q, h, d] (there is no CPU path)")
+    idx = q.get_device()
+    dt = q.dtype
+    code = _DTYPE_CODE.get(dt)
+    if code is None:
+        raise TypeError(f"exattn takes float16 or bfloat16 tensors, got {dt}")
+    t, h, d = q.shape
+    stride = _rows("q", q, idx, dt)
+    if not isinstance(cu_seqlens_q, torch.Tensor) or cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] < 2:
+        raise ValueError("cu_seqlens_q must be an int32 tensor [b + 1]")
+    b = cu_seqlens_q.shape[0] - 1
+    _int_array("cu_seqlens_q", cu_seqlens_q, (b + 1,), idx)
+    if out is None:
+        out = torch.empty((t, h, d), dtype=dt, device=q.device)
+    elif out.shape != q.shape or out.dtype is not dt or not out.is_contiguous() or out.get_device() != idx:
+        raise ValueError("out must be a contiguous tensor with q's shape and dtype")
+    if lse is None:
+        lse = torch.empty((h, t), dtype=torch.float32, device=q.device)
+    elif (lse.shape != (h, t) or lse.dtype is not torch.float32 or not lse.is_contiguous()
+          or lse.get_device() != idx):
+        raise ValueError("lse must be a contiguous float32 tensor [h, total_q]")
+    return b, t, h, d, code, idx, stride, out, lse
+
+
+def attn_fwd_packed(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int = 0,
+                    scale: float | None = None, out=None, lse=None, stream=None, causal: bool = False):
+    """Attention over sequences of different lengths packed one behind the
+    other, with grouped heads.
+
+    q: [total_q, h, d], k/v: [total_k, h_kv, d], fp16 or bf16 CUDA tensors, h
+    a multiple of h_kv; each may be a slice of wider rows (any token stride,
+    heads side by side). cu_seqlens_q, cu_seqlens_k: int32 [b + 1], sequence i
+    holds rows cu[i] .. cu[i + 1] - 1. max_seqlen_q: the most rows a sequence
+    has (0: not known; it only picks the kernel's form). ``causal``: the
+    bottom-right-aligned mask of each sequence's own lengths. Returns out
+    [total_q, h, d] and lse [h, total_q]; rows of no sequence are left as
+    they were."""
+    b, t, h, d, dt, idx, qs, out, lse = _packed_q(q, cu_seqlens_q, out, lse)
+    ks, vs = _rows("k", k, idx, q.dtype), _rows("v", v, idx, q.dtype)
+    tk, hk, dk = k.shape
+    if v.shape != k.shape or dk != d or hk < 1 or h % hk:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
+    _int_array("cu_seqlens_k", cu_seqlens_k, (b + 1,), idx)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    lib = _lib or load_library()
+    rc = _call(lib.attn_fwd_packed, idx, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+               cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), out.data_ptr(), lse.data_ptr(), b, t, tk,
+               int(max_seqlen_q), h, hk, d, qs, ks, vs, scale, 1 if causal else 0, dt)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_fwd_packed")
+    return out, lse
+
+
+def _pools(k_pages, v_pages, idx, dt):
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.get_device() != idx or t.dtype is not dt \
+                or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor [num_pages, page_size, h_kv, d] with the "
+                             "rows' dtype and device")
+    if k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must have the same shape")
+    return k_pages.shape
+
+
+def attn_chunk_paged(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q: int = 0,
+                     scale: float | None = None, out=None, lse=None, stream=None, causal: bool = False):
+    """Attention of each request's new tokens (one, or a chunk of a prompt)
+    over a paged KV cache that holds them already, with grouped heads.
+
+    q: [total_q, h, d], request i's rows cu_seqlens_q[i] .. cu_seqlens_q[i +
+    1] - 1 (int32 [b + 1]); k_pages, v_pages: [num_pages, page_size, h_kv, d]
+    (page_size a multiple of 16); block_table: int32 [b, max_pages];
+    seqlens_k: int32 [b] keys per request with the new ones. ``causal``: the
+    bottom-right-aligned mask against each request's own key count. Other
+    arguments and results as attn_fwd_packed."""
+    b, t, h, d, dt, idx, qs, out, lse = _packed_q(q, cu_seqlens_q, out, lse)
+    num_pages, page_size, hk, dk = _pools(k_pages, v_pages, idx, q.dtype)
+    if dk != d or hk < 1 or h % hk:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, pages {tuple(k_pages.shape)}")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be an int32 tensor [b, max_pages]")
+    max_pages = block_table.shape[1]
+    _int_array("block_table", block_table, (b, max_pages), idx)
+    _int_array("seqlens_k", seqlens_k, (b,), idx)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    lib = _lib or load_library()
+    rc = _call(lib.attn_chunk_paged, idx, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+               block_table.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), out.data_ptr(),
+               lse.data_ptr(), b, t, int(max_seqlen_q), h, hk, d, num_pages, page_size, max_pages, qs, scale,
+               1 if causal else 0, dt)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_chunk_paged")
+    return out, lse
+
+
+def attn_paged_plan(seqlens_k, new_lens, block_table, free_pages, free_count, page_size: int,
+                    max_tokens: int | None = None, cu_seqlens_q=None, seqlens_out=None, slot_map=None,
+                    free_left=None, stream=None):
+    """Block tables and slot maps of one step, built on the device.
+
+    seqlens_k: int32 [b] keys in the cache; new_lens: int32 [b] tokens each
+    request brings; block_table: int32 [b, max_pages], updated in place with
+    the pages taken; free_pages: int32 [num_free], a stack whose first
+    free_count (int32 [1]) entries are free. slot_map has max_tokens entries
+    (needed unless slot_map is given): a bound on the step's new tokens that
+    the host knows. Returns (cu_seqlens_q [b + 1], seqlens_out [b], slot_map
+    int64 [max_tokens], free_left [1]); a negative free_left says how many
+    pages were lacking. Inputs are left as they are: seqlens_out and
+    free_left are the next step's seqlens_k and free_count."""
+    if not isinstance(seqlens_k, torch.Tensor) or not seqlens_k.is_cuda or seqlens_k.dim() != 1:
+        raise ValueError("seqlens_k must be an int32 CUDA tensor [b] (there is no CPU path)")
+    b, idx, device = seqlens_k.shape[0], seqlens_k.get_device(), seqlens_k.device
+    _int_array("seqlens_k", seqlens_k, (b,), idx)
+    _int_array("new_lens", new_lens, (b,), idx)
+    for name, t, n in (("block_table", block_table, 2), ("free_pages", free_pages, 1)):
+        if not isinstance(t, torch.Tensor) or t.dim() != n:
+            raise ValueError(f"{name} must be an int32 tensor of {n} dimension(s)")
+    max_pages, num_free = block_table.shape[1], free_pages.shape[0]
+    _int_array("block_table", block_table, (b, max_pages), idx)
+    _int_array("free_pages", free_pages, (num_free,), idx)
+    _int_array("free_count", free_count, (1,), idx)
+    if cu_seqlens_q is None:
+        cu_seqlens_q = torch.empty(b + 1, dtype=torch.int32, device=device)
+    if seqlens_out is None:
+        seqlens_out = torch.empty(b, dtype=torch.int32, device=device)
+    if free_left is None:
+        free_left = torch.empty(1, dtype=torch.int32, device=device)
+    if slot_map is None:
+        if max_tokens is None:
+            raise ValueError("give max_tokens or slot_map")
+        slot_map = torch.empty(int(max_tokens), dtype=torch.int64, device=device)
+    elif max_tokens is not None and int(max_tokens) != slot_map.numel():
+        raise ValueError("slot_map must have max_tokens entries")
+    _int_array("cu_seqlens_q", cu_seqlens_q, (b + 1,), idx)
+    _int_array("seqlens_out", seqlens_out, (b,), idx)
+    _int_array("free_left", free_left, (1,), idx)
+    _int_array("slot_map", slot_map, (slot_map.numel(),), idx, torch.int64)
+    lib = _lib or load_library()
+    rc = _call(lib.attn_paged_plan, idx, stream, seqlens_k.data_ptr(), new_lens.data_ptr(),
+               block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), cu_seqlens_q.data_ptr(),
+               seqlens_out.data_ptr(), slot_map.data_ptr(), free_left.data_ptr(), b, max_pages, int(page_size),
+               num_free, slot_map.shape[0])
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_paged_plan")
+    return cu_seqlens_q, seqlens_out, slot_map, free_left
+
+
+def attn_paged_write(k, v, slot_map, k_pages, v_pages, stream=None):
+    """New K and V rows into the pages of a paged cache.
+
+    k, v: [tokens, h_kv, d] (each may be a slice of wider rows); slot_map:
+    int64 [tokens], the row of token t in the pools seen as [num_pages *
+    page_size, h_kv, d] (attn_paged_plan's; slots outside the pools, such as
+    -1, are skipped); k_pages, v_pages: [num_pages, page_size, h_kv, d],
+    written in place."""
+    if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dim() != 3:
+        raise ValueError("k must be a CUDA tensor [tokens, h_kv, d] (there is no CPU path)")
+    idx = k.get_device()
+    code = _dtype_code(k)
+    ks, vs = _rows("k", k, idx, k.dtype), _rows("v", v, idx, k.dtype)
+    num_pages, page_size, hk, d = _pools(k_pages, v_pages, idx, k.dtype)
+    t = k.shape[0]
+    if v.shape != k.shape or k.shape[1] != hk or k.shape[2] != d:
+        raise ValueError(f"shape mismatch: k {tuple(k.shape)}, v {tuple(v.shape)}, pages {tuple(k_pages.shape)}")
+    _int_array("slot_map", slot_map, (t,), idx, torch.int64)
+    lib = _lib or load_library()
+    rc = _call(lib.attn_paged_write, idx, stream, k.data_ptr(), v.data_ptr(), slot_map.data_ptr(),
+               k_pages.data_ptr(), v_pages.data_ptr(), t, hk, d, num_pages, page_size, ks, vs, code)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_paged_write")
+
+
 def attn_decode_splitkv_noalloc(q, k, v, out, lse, scale: float | None = None,
                                 num_splits: int = 0, stream=None):
     """attn_decode_splitkv for callers that cannot allocate device memory:
@@ -410,7 +621,8 @@ def attn_debug_set_flags(flags: int) -> None:
 
 __all__ = [
     "AttnError", "attn_fwd", "attn_fwd_host", "attn_bwd", "attn_decode_splitkv",
-    "attn_decode_paged", "attn_decode_splitkv_noalloc", "attn_get_noalloc_status",
+    "attn_decode_paged", "attn_fwd_packed", "attn_chunk_paged", "attn_paged_plan", "attn_paged_write",
+    "attn_decode_splitkv_noalloc", "attn_get_noalloc_status",
     "attn_decode_num_splits",
     "attn_decode_num_splits_for_sms", "attn_get_device_status", "attn_last_timeout_site",
     "attn_release_workspace", "attn_debug_set_flags", "attn_status_string", "load_library",

@@ -23,9 +23,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libexattn.so")
 
-SOURCES = ["api.cu", "fwd.cu", "fwd_short.cu", "bwd.cu", "bwd_short.cu", "decode.cu",
+SOURCES = ["api.cu", "api_packed.cu", "fwd.cu", "fwd_short.cu", "fwd_packed.cu", "chunk_paged.cu", "paged_tables.cu",
+           "bwd.cu", "bwd_short.cu", "decode.cu",
            "decode_noalloc.cu"]
-HEADERS = [os.path.join(CSRC, "internal.h"), os.path.join(CSRC, "ptx.cuh"),
+HEADERS = [os.path.join(CSRC, h) for h in ("internal.h", "ptx.cuh", "packed_sched.h", "packed_dev.cuh", "fwd_packed.cuh")] + [
            os.path.join(INCLUDE, "exattn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC]

@@ -69,6 +69,19 @@ bool encode_4d(CUtensorMap *map, const void *base, bool bf16, int d, int h, int 
     return r == CUDA_SUCCESS;
 }
 
+bool encode_dims(CUtensorMap *map, const void *base, bool bf16, const uint64_t (&dims)[4],
+                 const uint64_t (&strides)[3], const uint32_t (&box)[4], CUtensorMapSwizzle swizzle) {
+    cuuint64_t dm[4], st[3];
+    cuuint32_t bx[4];
+    for (int i = 0; i < 4; ++i) dm[i] = dims[i];
+    for (int i = 0; i < 3; ++i) st[i] = strides[i];
+    for (int i = 0; i < 4; ++i) bx[i] = box[i];
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return g_encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                    const_cast<void *>(base), dm, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace exattn
 
 namespace {
@@ -226,6 +239,10 @@ bool stream_workspace(DeviceState *ds, cudaStream_t stream, int64_t n, size_t pa
     return true;
 }
 
+}  // namespace
+
+namespace exattn {
+
 CUtensorMapSwizzle fwd_swizzle(int d) {
     switch (fwd_row_bytes(d)) {
         case 128: return CU_TENSOR_MAP_SWIZZLE_128B;
@@ -233,6 +250,25 @@ CUtensorMapSwizzle fwd_swizzle(int d) {
         default: return CU_TENSOR_MAP_SWIZZLE_32B;
     }
 }
+
+attn_status_t device_info(int *dev, uint32_t **status, int *num_sms) {
+    DeviceState *ds = nullptr;
+    const attn_status_t st = device_state(&ds);
+    if (st != ATTN_OK) return st;
+    *dev = static_cast<int>(ds - g_dev);
+    *status = ds->status;
+    *num_sms = ds->num_sms;
+    return ATTN_OK;
+}
+
+cudaStream_t device_side_stream(cudaStream_t stream) {
+    DeviceState *ds = nullptr;
+    return device_state(&ds) == ATTN_OK ? side_stream(ds, stream) : nullptr;
+}
+
+}  // namespace exattn
+
+namespace {
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -498,7 +534,7 @@ int dec_num_splits(int b, int sq, int sk, int h, int d, int num_sms) {
 
 extern "C" {
 
-int attn_version(void) { return 101; }
+int attn_version(void) { return 102; }
 
 const char *attn_status_string(attn_status_t s) {
     switch (s) {
@@ -976,6 +1012,7 @@ void attn_release_workspace(void) {
         }
         g_dev[dev].stream_ws.clear();
     }
+    packed_release(dev);
     cudaMemPool_t pool;
     if (cudaDeviceGetDefaultMemPool(&pool, dev) == cudaSuccess) cudaMemPoolTrimTo(pool, 0);
 }

@@ -1,0 +1,454 @@
+// C-ABI layer of the packed and paged operators with grouped heads: argument
+// checks, tensor maps, and the workspace of cut units. Declared in
+// include/exattn.h.
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+#include <vector>
+
+#include "exattn.h"
+#include "internal.h"
+
+using namespace exattn;
+
+namespace exattn {
+
+// Where the forward's work is cut (packed_sched.h). A unit's fixed cost (Q,
+// first S, epilogue) counts as one step of 128 keys; units are cut only
+// where each CTA's share is at least four steps, and two steps away from
+// their ends, as joining a cut unit costs about as much as two steps.
+LineShape pack_line(int heads, int tile_tokens, bool one_tile, bool causal) {
+    LineShape s;
+    s.heads = heads;
+    s.unit_len = one_tile ? tile_tokens : 2 * tile_tokens;
+    s.step_len = 128;
+    s.causal = causal ? 1 : 0;
+    s.by_key = 0;
+    s.unit_cost = 128;
+    s.min_steps = 2;
+    s.min_part = 4 * 128;
+    return s;
+}
+
+// The key-tile units of the backward: 128 keys against tiles of query tokens.
+LineShape bwd_key_line(int heads, int tile_tokens, bool causal) {
+    LineShape s;
+    s.heads = heads;
+    s.unit_len = 128;
+    s.step_len = tile_tokens;
+    s.causal = causal ? 1 : 0;
+    s.by_key = 1;
+    s.unit_cost = 2 * tile_tokens;
+    s.min_steps = 2;
+    s.min_part = 8 * static_cast<int64_t>(tile_tokens);
+    return s;
+}
+
+}  // namespace exattn
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kDevices = 64;
+constexpr int kMaxRows = 0x7fffff00;  // the ends of tiles stay below 2^31
+
+bool misaligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+// What the cut units of a call leave for one another, kept per stream: calls
+// on a stream are ordered, so each call reuses it. The lock is held until the
+// call is enqueued, so that another host thread cannot replace the buffers in
+// between.
+struct PackWs {
+    cudaStream_t stream;
+    uint32_t *arrivals = nullptr;
+    int n_arrivals = 0;
+    char *part = nullptr;
+    size_t part_bytes = 0;
+    uint32_t call = 0;
+};
+std::vector<PackWs> g_ws[kDevices];
+std::mutex g_ws_mu;
+
+struct Workspace {
+    std::unique_lock<std::mutex> lock;
+    uint32_t *arrivals = nullptr;
+    uint32_t call = 0;
+    char *part = nullptr;
+    void *owned = nullptr;  // a workspace of this call's own, to be freed stream-ordered
+};
+
+// n arrival counters and part_bytes of partial results. A stream that is
+// being captured (its replays are not ordered with the stream's other calls),
+// or the per-thread default stream (one handle, many streams), gets them from
+// the memory pool for this call alone.
+attn_status_t get_workspace(int dev, cudaStream_t stream, int n, size_t part_bytes, Workspace *w) {
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) {
+        cudaGetLastError();
+        return ATTN_ERR_CUDA;
+    }
+    const size_t count_bytes = (static_cast<size_t>(n) * sizeof(uint32_t) + 255) / 256 * 256;
+    if (cs != cudaStreamCaptureStatusNone || stream == cudaStreamPerThread) {
+        void *p = nullptr;
+        if (cudaMallocAsync(&p, count_bytes + part_bytes, stream) != cudaSuccess) {
+            cudaGetLastError();
+            return ATTN_ERR_NO_MEMORY;
+        }
+        if (cudaMemsetAsync(p, 0, count_bytes, stream) != cudaSuccess) {
+            cudaFreeAsync(p, stream);
+            return ATTN_ERR_CUDA;
+        }
+        w->owned = p;
+        w->arrivals = static_cast<uint32_t *>(p);
+        w->part = static_cast<char *>(p) + count_bytes;
+        w->call = 1;
+        return ATTN_OK;
+    }
+    w->lock = std::unique_lock<std::mutex>(g_ws_mu);
+    PackWs *e = nullptr;
+    for (auto &x : g_ws[dev])
+        if (x.stream == stream) e = &x;
+    if (e == nullptr) {
+        PackWs x;
+        x.stream = stream;
+        g_ws[dev].push_back(x);
+        e = &g_ws[dev].back();
+    }
+    if (e->n_arrivals < n) {
+        void *p = nullptr;
+        if (cudaMallocAsync(&p, count_bytes, stream) != cudaSuccess) {
+            cudaGetLastError();
+            return ATTN_ERR_NO_MEMORY;
+        }
+        if (cudaMemsetAsync(p, 0, count_bytes, stream) != cudaSuccess) {
+            cudaFreeAsync(p, stream);
+            return ATTN_ERR_CUDA;
+        }
+        if (e->arrivals) cudaFreeAsync(e->arrivals, stream);
+        e->arrivals = static_cast<uint32_t *>(p);
+        e->n_arrivals = n;
+    }
+    if (e->part_bytes < part_bytes) {
+        void *p = nullptr;
+        if (cudaMallocAsync(&p, part_bytes, stream) != cudaSuccess) {
+            cudaGetLastError();
+            return ATTN_ERR_NO_MEMORY;
+        }
+        if (e->part) cudaFreeAsync(e->part, stream);
+        e->part = static_cast<char *>(p);
+        e->part_bytes = part_bytes;
+    }
+    e->call = e->call >= 0xffffffu ? 1 : e->call + 1;
+    w->arrivals = e->arrivals;
+    w->part = e->part;
+    w->call = e->call;
+    return ATTN_OK;
+}
+
+// What every packed attention call checks. Strides are in elements, of the
+// token dimension of q, k and v.
+attn_status_t check_packed(int b, int total_q, int h, int h_kv, int d, float scale, int dtype) {
+    if (b < 1 || total_q < 1 || h < 1 || h_kv < 1) return ATTN_ERR_INVALID_ARG;
+    if (!std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+    if (dtype != ATTN_FP16 && dtype != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+    if (h % h_kv != 0) return ATTN_ERR_INVALID_ARG;
+    if (d != 16 && d != 32 && d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+    if (b > 65535 || h > 65535 || h / h_kv > 128) return ATTN_ERR_UNSUPPORTED;
+    if (total_q > kMaxRows) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+attn_status_t check_stride(int64_t stride, int64_t row) {
+    if (stride < row || stride % 8 != 0) return ATTN_ERR_INVALID_ARG;
+    if (stride * 2 >= (1ll << 40)) return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+// Rows [total, h, d] with a token stride, read in boxes of `tokens` tokens of
+// one K/V head's group of query heads: dims (d, group, h_kv, total).
+bool encode_rows(CUtensorMap *map, const void *base, bool bf16, int d, int h, int h_kv, int64_t total,
+                 int64_t stride, int tokens) {
+    const uint64_t g = h / h_kv, row = static_cast<uint64_t>(d) * 2;
+    const uint64_t dims[4] = {static_cast<uint64_t>(d), g, static_cast<uint64_t>(h_kv), static_cast<uint64_t>(total)};
+    const uint64_t strides[3] = {row, row * g, static_cast<uint64_t>(stride) * 2};
+    const uint32_t box[4] = {static_cast<uint32_t>(fwd_row_bytes(d) / 2), static_cast<uint32_t>(g), 1u,
+                             static_cast<uint32_t>(tokens)};
+    return encode_dims(map, base, bf16, dims, strides, box, fwd_swizzle(d));
+}
+
+// Rows [total, h_kv, d] with a token stride, read 128 at a time: dims (d,
+// h_kv, total, 1).
+bool encode_keys(CUtensorMap *map, const void *base, bool bf16, int d, int h_kv, int64_t total, int64_t stride) {
+    const uint64_t row = static_cast<uint64_t>(d) * 2, st = static_cast<uint64_t>(stride) * 2;
+    const uint64_t dims[4] = {static_cast<uint64_t>(d), static_cast<uint64_t>(h_kv), static_cast<uint64_t>(total), 1};
+    const uint64_t strides[3] = {row, st, st};
+    const uint32_t box[4] = {static_cast<uint32_t>(fwd_row_bytes(d) / 2), 1u, 128u, 1u};
+    return encode_dims(map, base, bf16, dims, strides, box, fwd_swizzle(d));
+}
+
+// Common part of the two forwards: everything but K and V.
+void fill_pack(PackArgs *a, void *o, float *lse, int b, int total_q, int max_seqlen_q, int h, int h_kv,
+               float scale, bool causal, uint32_t *status, int num_sms) {
+    a->o = o;
+    a->lse = lse;
+    a->h = h;
+    a->group = h / h_kv;
+    a->tile_tokens = pack_tile_tokens(a->group);
+    a->total_q = total_q;
+    a->causal = causal ? 1 : 0;
+    a->scale_log2 = scale * kLog2e;
+    a->status = status;
+    a->flags = debug_flags();
+    a->ctas = num_sms;
+    // Units of one query tile where no sequence is known to hold more.
+    const int longest = max_seqlen_q > 0 && max_seqlen_q < total_q ? max_seqlen_q : total_q;
+    a->one_tile = longest <= a->tile_tokens ? 1 : 0;
+    a->line = pack_line(h_kv, a->tile_tokens, a->one_tile != 0, causal);
+    a->seqs.b = b;
+    a->seqs.total_q = total_q;
+    a->block_table = nullptr;
+    a->page_size = a->max_pages = a->num_pages = a->box_rows = 0;
+}
+
+template <class Launch>
+attn_status_t run_pack(PackArgs *a, int dev, int d, cudaStream_t stream, Launch launch) {
+    const size_t rows = static_cast<size_t>(a->ctas) * 2 * (a->one_tile ? 1 : 2) * 128;
+    Workspace w;
+    const attn_status_t st =
+        get_workspace(dev, stream, 2 * a->ctas, rows * (static_cast<size_t>(d) + 1) * sizeof(float), &w);
+    if (st != ATTN_OK) return st;
+    a->arrivals = w.arrivals;
+    a->call = w.call;
+    a->o_part = reinterpret_cast<float *>(w.part);
+    a->lse_part = a->o_part + rows * d;
+    const cudaError_t e = launch();
+    const cudaError_t ef = w.owned ? cudaFreeAsync(w.owned, stream) : cudaSuccess;
+    return (e == cudaSuccess && ef == cudaSuccess) ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+bool overlap(const void *p, size_t np, const void *q, size_t nq) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + nq && b < a + np;
+}
+
+}  // namespace
+
+void exattn::packed_release(int dev) {
+    if (dev < 0 || dev >= kDevices) return;
+    std::lock_guard<std::mutex> lock(g_ws_mu);
+    for (auto &x : g_ws[dev]) {
+        if (x.arrivals) cudaFree(x.arrivals);
+        if (x.part) cudaFree(x.part);
+    }
+    g_ws[dev].clear();
+}
+
+extern "C" {
+
+int attn_debug_packed_plan(const int *seqlens_q, const int *seqlens_k, int b, int h, int h_kv, int one_tile,
+                           int causal, int by_key, int ctas, int max_ranges, int *out) {
+    if (!seqlens_q || !seqlens_k || !out || b < 1 || h < 1 || h_kv < 1 || h % h_kv != 0 || h / h_kv > 128 ||
+        ctas < 1 || max_ranges < 1)
+        return -1;
+    for (int i = 0; i < b; ++i)
+        if (seqlens_q[i] < 0 || seqlens_k[i] < 0) return -1;
+    const int tokens = pack_tile_tokens(h / h_kv);
+    const LineShape s = by_key ? bwd_key_line(h_kv, tokens, causal != 0)
+                               : pack_line(h_kv, tokens, one_tile != 0, causal != 0);
+    LineSum sum{0, 0, 0};
+    for (int i = 0; i < b; ++i) line_add(&sum, s, seqlens_q[i], seqlens_k[i]);
+    const LineDeal d = line_deal(s, sum, ctas);
+    auto find = [&](int64_t at, int64_t *before) {
+        *before = 0;
+        for (int i = 0; i < b; ++i) {
+            const int64_t cost = s.heads * deal_before(s, d, seqlens_q[i], seqlens_k[i],
+                                                       line_units(s, seqlens_q[i], seqlens_k[i]));
+            if (at < *before + cost) return place_in_seq(s, d, i, seqlens_q[i], seqlens_k[i], at - *before);
+            *before += cost;
+        }
+        return Place{b, 0, 0, 0};
+    };
+    int n = 0;
+    for (int c = 0; c < d.parts; ++c) {
+        int64_t x0 = 0, unused = 0;
+        const Place p = find(part_begin(d, c), &x0), e = find(part_begin(d, c + 1), &unused);
+        walk_part(s, d, b, c, p, e, x0, [&](int i) { return SeqLen{seqlens_q[i], seqlens_k[i]}; },
+                  [&](const UnitRange &r) {
+                      if (n >= max_ranges) return false;
+                      const int row[9] = {c, r.seq, r.head, r.unit, r.step0, r.nstep, r.slot, r.first_part, r.nparts};
+                      for (int i = 0; i < 9; ++i) out[9 * n + i] = row[i];
+                      ++n;
+                      return true;
+                  });
+    }
+    return n;
+}
+
+attn_status_t attn_fwd_packed(const void *q, const void *k, const void *v, const int32_t *cu_seqlens_q,
+                              const int32_t *cu_seqlens_k, void *o, float *lse, int b, int total_q, int total_k,
+                              int max_seqlen_q, int h, int h_kv, int d, int64_t q_stride, int64_t k_stride,
+                              int64_t v_stride, float scale, int causal, attn_dtype_t dtype, cudaStream_t stream) {
+    if (!q || !k || !v || !cu_seqlens_q || !cu_seqlens_k || !o || !lse) return ATTN_ERR_INVALID_ARG;
+    if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(o, 16) || misaligned(lse, 4) ||
+        misaligned(cu_seqlens_q, 4) || misaligned(cu_seqlens_k, 4))
+        return ATTN_ERR_INVALID_ARG;
+    if (total_k < 1) return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_packed(b, total_q, h, h_kv, d, scale, dtype);
+    if (st == ATTN_OK && total_k > kMaxRows) st = ATTN_ERR_UNSUPPORTED;
+    if (st == ATTN_OK) st = check_stride(q_stride, static_cast<int64_t>(h) * d);
+    if (st == ATTN_OK) st = check_stride(k_stride, static_cast<int64_t>(h_kv) * d);
+    if (st == ATTN_OK) st = check_stride(v_stride, static_cast<int64_t>(h_kv) * d);
+    if (st != ATTN_OK) return st;
+    int dev = 0, sms = 0;
+    uint32_t *status = nullptr;
+    if ((st = device_info(&dev, &status, &sms)) != ATTN_OK) return st;
+    const bool bf16 = dtype == ATTN_BF16;
+    PackArgs a;
+    fill_pack(&a, o, lse, b, total_q, max_seqlen_q, h, h_kv, scale, causal != 0, status, sms);
+    a.seqs.cu_q = cu_seqlens_q;
+    a.seqs.cu_k = cu_seqlens_k;
+    a.seqs.seqlens = nullptr;
+    a.seqs.max_k = total_k;
+    CUtensorMap tq, tk, tv;
+    if (!encode_rows(&tq, q, bf16, d, h, h_kv, total_q, q_stride, a.tile_tokens) ||
+        !encode_keys(&tk, k, bf16, d, h_kv, total_k, k_stride) ||
+        !encode_keys(&tv, v, bf16, d, h_kv, total_k, v_stride))
+        return ATTN_ERR_CUDA;
+    return run_pack(&a, dev, d, stream, [&] { return launch_fwd_packed(d, bf16, tq, tk, tv, a, stream); });
+}
+
+attn_status_t attn_chunk_paged(const void *q, const void *k_pages, const void *v_pages, const int32_t *block_table,
+                               const int32_t *cu_seqlens_q, const int32_t *seqlens_k, void *o, float *lse, int b,
+                               int total_q, int max_seqlen_q, int h, int h_kv, int d, int num_pages, int page_size,
+                               int max_pages_per_seq, int64_t q_stride, float scale, int causal,
+                               attn_dtype_t dtype, cudaStream_t stream) {
+    if (!q || !k_pages || !v_pages || !block_table || !cu_seqlens_q || !seqlens_k || !o || !lse)
+        return ATTN_ERR_INVALID_ARG;
+    if (misaligned(q, 16) || misaligned(k_pages, 16) || misaligned(v_pages, 16) || misaligned(o, 16) ||
+        misaligned(lse, 4) || misaligned(block_table, 4) || misaligned(cu_seqlens_q, 4) || misaligned(seqlens_k, 4))
+        return ATTN_ERR_INVALID_ARG;
+    if (num_pages < 1 || page_size < 1 || max_pages_per_seq < 1) return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_packed(b, total_q, h, h_kv, d, scale, dtype);
+    if (st == ATTN_OK) st = check_stride(q_stride, static_cast<int64_t>(h) * d);
+    if (st != ATTN_OK) return st;
+    // boxes of at most a page: page sizes are multiples of 16 keys
+    if (page_size % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+    const int64_t max_k = static_cast<int64_t>(max_pages_per_seq) * page_size;
+    if (max_k > kMaxRows) return ATTN_ERR_UNSUPPORTED;
+    int dev = 0, sms = 0;
+    uint32_t *status = nullptr;
+    if ((st = device_info(&dev, &status, &sms)) != ATTN_OK) return st;
+    const bool bf16 = dtype == ATTN_BF16;
+    PackArgs a;
+    fill_pack(&a, o, lse, b, total_q, max_seqlen_q, h, h_kv, scale, causal != 0, status, sms);
+    a.seqs.cu_q = cu_seqlens_q;
+    a.seqs.cu_k = nullptr;
+    a.seqs.seqlens = seqlens_k;
+    a.seqs.max_k = static_cast<int>(max_k);
+    a.block_table = block_table;
+    a.page_size = page_size;
+    a.max_pages = max_pages_per_seq;
+    a.num_pages = num_pages;
+    a.box_rows = 128;  // the largest power of two that divides the page and the step
+    while (page_size % a.box_rows != 0) a.box_rows /= 2;
+    const int box0 = fwd_row_bytes(d) / 2;
+    CUtensorMap tq, tk, tv;
+    if (!encode_rows(&tq, q, bf16, d, h, h_kv, total_q, q_stride, a.tile_tokens) ||
+        !encode_4d(&tk, k_pages, bf16, d, h_kv, page_size, num_pages, box0, a.box_rows, fwd_swizzle(d)) ||
+        !encode_4d(&tv, v_pages, bf16, d, h_kv, page_size, num_pages, box0, a.box_rows, fwd_swizzle(d)))
+        return ATTN_ERR_CUDA;
+    return run_pack(&a, dev, d, stream, [&] { return launch_chunk_paged(d, bf16, tq, tk, tv, a, stream); });
+}
+
+attn_status_t attn_paged_plan(const int32_t *seqlens_k, const int32_t *new_lens, int32_t *block_table,
+                              const int32_t *free_pages, const int32_t *free_count, int32_t *cu_seqlens_q,
+                              int32_t *seqlens_out, int64_t *slot_map, int32_t *free_left, int b,
+                              int max_pages_per_seq, int page_size, int num_free, int64_t max_tokens,
+                              cudaStream_t stream) {
+    if (!seqlens_k || !new_lens || !block_table || !free_pages || !free_count || !cu_seqlens_q || !seqlens_out ||
+        !slot_map || !free_left)
+        return ATTN_ERR_INVALID_ARG;
+    for (const void *p : {static_cast<const void *>(seqlens_k), static_cast<const void *>(new_lens),
+                          static_cast<const void *>(block_table), static_cast<const void *>(free_pages),
+                          static_cast<const void *>(free_count), static_cast<const void *>(cu_seqlens_q),
+                          static_cast<const void *>(seqlens_out), static_cast<const void *>(free_left)})
+        if (misaligned(p, 4)) return ATTN_ERR_INVALID_ARG;
+    if (misaligned(slot_map, 8)) return ATTN_ERR_INVALID_ARG;
+    if (b < 1 || max_pages_per_seq < 1 || page_size < 1 || num_free < 1 || max_tokens < 1)
+        return ATTN_ERR_INVALID_ARG;
+    if (b > 65535 || static_cast<int64_t>(max_pages_per_seq) * page_size > 0x7fffffffLL ||
+        max_tokens > 0x7fffffffLL)
+        return ATTN_ERR_UNSUPPORTED;
+    // every block reads all inputs while others write outputs
+    const size_t n4 = static_cast<size_t>(b) * 4;
+    const struct {
+        const void *p;
+        size_t n;
+    } in[4] = {{seqlens_k, n4}, {new_lens, n4}, {free_pages, static_cast<size_t>(num_free) * 4}, {free_count, 4}},
+      out[5] = {{block_table, n4 * max_pages_per_seq},
+                {cu_seqlens_q, n4 + 4},
+                {seqlens_out, n4},
+                {slot_map, static_cast<size_t>(max_tokens) * 8},
+                {free_left, 4}};
+    for (int i = 0; i < 5; ++i) {
+        for (const auto &x : in)
+            if (overlap(out[i].p, out[i].n, x.p, x.n)) return ATTN_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return ATTN_ERR_INVALID_ARG;
+    }
+    int dev = 0, sms = 0;
+    uint32_t *status = nullptr;
+    const attn_status_t st = device_info(&dev, &status, &sms);
+    if (st != ATTN_OK) return st;
+    PlanArgs a;
+    a.seqlens = seqlens_k;
+    a.new_lens = new_lens;
+    a.block_table = block_table;
+    a.free_pages = free_pages;
+    a.free_count = free_count;
+    a.cu_seqlens_q = cu_seqlens_q;
+    a.seqlens_out = seqlens_out;
+    a.slot_map = slot_map;
+    a.free_left = free_left;
+    a.b = b;
+    a.max_pages = max_pages_per_seq;
+    a.page_size = page_size;
+    a.num_free = num_free;
+    a.max_tokens = max_tokens;
+    return launch_paged_plan(a, sms, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+attn_status_t attn_paged_write(const void *k, const void *v, const int64_t *slot_map, void *k_pages, void *v_pages,
+                               int64_t tokens, int h_kv, int d, int num_pages, int page_size, int64_t k_stride,
+                               int64_t v_stride, attn_dtype_t dtype, cudaStream_t stream) {
+    if (!k || !v || !slot_map || !k_pages || !v_pages) return ATTN_ERR_INVALID_ARG;
+    if (misaligned(k, 16) || misaligned(v, 16) || misaligned(k_pages, 16) || misaligned(v_pages, 16) ||
+        misaligned(slot_map, 8))
+        return ATTN_ERR_INVALID_ARG;
+    if (tokens < 1 || h_kv < 1 || num_pages < 1 || page_size < 1) return ATTN_ERR_INVALID_ARG;
+    if (dtype != ATTN_FP16 && dtype != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+    if (d != 16 && d != 32 && d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+    if (h_kv > 65535 || tokens > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+    const int64_t row = static_cast<int64_t>(h_kv) * d;
+    attn_status_t st = check_stride(k_stride, row);
+    if (st == ATTN_OK) st = check_stride(v_stride, row);
+    if (st != ATTN_OK) return st;
+    int dev = 0, sms = 0;
+    uint32_t *status = nullptr;
+    if ((st = device_info(&dev, &status, &sms)) != ATTN_OK) return st;
+    WriteArgs a;
+    a.k = static_cast<const uint4 *>(k);
+    a.v = static_cast<const uint4 *>(v);
+    a.slot_map = slot_map;
+    a.k_pages = static_cast<uint4 *>(k_pages);
+    a.v_pages = static_cast<uint4 *>(v_pages);
+    a.tokens = tokens;
+    a.words = row / 8;
+    a.k_stride = k_stride / 8;
+    a.v_stride = v_stride / 8;
+    a.slots = static_cast<int64_t>(num_pages) * page_size;
+    if (a.tokens * a.words > (1ll << 40)) return ATTN_ERR_UNSUPPORTED;
+    return launch_paged_write(a, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // extern "C"

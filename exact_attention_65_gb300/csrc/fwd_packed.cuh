@@ -1,0 +1,888 @@
+// Forward attention over packed sequences with grouped heads, sm_103a: whole
+// prompts packed one behind the other (fwd_packed.cu), and the new tokens of
+// each request over a paged cache (chunk_paged.cu).
+//
+// The mathematics is the forward's (fwd.cu): S = scale Q K^T, an online
+// softmax with a running max and sum per row, O = P V, LSE = m + ln l.
+//
+// Grouped heads: the g = h / h_kv query heads of a K/V head see the same
+// keys, so a 128-row query tile holds floor(128 / g) tokens times those g
+// heads (row = token * g + head: one TMA box, as they lie side by side in
+// memory). Each K/V byte is read once for all heads of the group, a single
+// new token fills g rows instead of one, and the causal staircase of a tile
+// is g times flatter. Nothing is padded to a head count.
+//
+// Units and CTAs: a unit is two such tiles (one in the ONE form) of a
+// sequence and K/V head against its keys in steps of 128. Sequence lengths
+// live on the device, so every CTA works its part of the call out for itself
+// (packed_sched.h): equal shares of the total work, cut inside a unit where
+// that is needed. A cut unit's ranges leave normalised fp32 O_i and LSE_i
+// (log2) in the workspace; the range that finishes last joins them in the
+// order of the keys, so the result does not depend on who that is.
+//
+// Roles (384 threads, one CTA per SM): warp 0 TMA producer (a whole warp for
+// pages, one box per lane), warp 1 MMA issuer, warp 2 zeroes the V rows of a
+// unit's last tile that lie past the sequence (they belong to the next
+// sequence or are stale, P is 0 there, and 0 * NaN is NaN), warp 3 deals out
+// units, warps 4-7 and 8-11 softmax and epilogue of tile 0 and 1.
+//
+// What bounds it: long prompts, the tensor pipe and the exponentials; single
+// tokens, HBM (each SM keeps the ring, 160 to 192 KB at d = 128, in flight);
+// short calls, the chain launch, lengths, Q, K, S, P, O.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "packed_dev.cuh"
+#include "ptx.cuh"
+
+namespace exattn {
+namespace {
+
+// Bit 13 of a kind::f16 instruction descriptor: negate the A operand.
+constexpr uint32_t kNegateA = 1u << 13;
+
+template <int D, bool ONE>
+struct PackGeom {
+    static constexpr int BM = 128;  // rows of a query tile
+    static constexpr int BN = 128;  // keys of a step
+    static constexpr int QT = ONE ? 1 : 2;
+    static constexpr int ROW_BYTES = fwd_row_bytes(D);
+    static constexpr int PANELS = (D * 2) / ROW_BYTES;
+    static constexpr int PANEL_ELEMS = ROW_BYTES / 2;
+    static constexpr int PANEL_BYTES = BM * ROW_BYTES;
+    static constexpr int TILE_BYTES = BM * D * 2;
+    // K/V tiles in flight. The single-tile form is fed from HBM: its ring is
+    // as deep as shared memory allows, or holds 128 KB at small head dims.
+    static constexpr int SLOTS = ONE ? (D == 128 ? 6 : (D == 64 ? 10 : 16)) : (D == 128 ? 5 : 8);
+    static constexpr int QBUF = D <= 64 ? 2 : 1;
+    static constexpr int Q_BUF_BYTES = QT * TILE_BYTES;
+    static constexpr uint32_t LAYOUT =
+        ROW_BYTES == 128 ? kLayoutSw128 : (ROW_BYTES == 64 ? kLayoutSw64 : kLayoutSw32);
+    static constexpr uint32_t SBO = 8 * ROW_BYTES;
+    static constexpr int TMEM_COLS = 512;
+    static constexpr int TMEM_TILE_STRIDE = 256;
+    static constexpr int TMEM_O_OFF = 128;
+    static constexpr int OCH = D < 32 ? D : 32;
+
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_KV = OFF_Q + QBUF * Q_BUF_BYTES;
+    static constexpr int OFF_BAR = OFF_KV + SLOTS * TILE_BYTES;
+    static constexpr int BAR_QF = 0;              // [QBUF] Q landed
+    static constexpr int BAR_QE = BAR_QF + QBUF;  // [QBUF] Q read
+    static constexpr int BAR_KVF = BAR_QE + QBUF;
+    static constexpr int BAR_KVE = BAR_KVF + SLOTS;
+    static constexpr int BAR_SF = BAR_KVE + SLOTS;  // [2] S made (ONE: of even, odd steps)
+    static constexpr int BAR_PF = BAR_SF + 2;       // [2] P stored
+    static constexpr int BAR_OF = BAR_PF + 2;       // [2] O complete (ONE: [1] every P V done)
+    static constexpr int BAR_OE = BAR_OF + 2;       // [2] O read out
+    static constexpr int BAR_PVD = BAR_OF + 1;
+    static constexpr int BAR_DONE = BAR_OE + 2;
+    static constexpr int BAR_VLAND = BAR_DONE + 1;  // a last V tile landed (MMA -> zeroing)
+    static constexpr int BAR_VFIX = BAR_VLAND + 1;  // its rows past the sequence zeroed
+    static constexpr int BAR_MF = BAR_VFIX + 1;     // [kMsgSlots] unit message posted
+    static constexpr int BAR_ME = BAR_MF + kMsgSlots;
+    static constexpr int BAR_WG = BAR_ME + kMsgSlots;  // [2] a tile's softmax warps meet (cut units)
+    static constexpr int NUM_BARS = BAR_WG + 2;
+    static constexpr int OFF_MSG = (OFF_BAR + NUM_BARS * 8 + 15) & ~15;
+    static constexpr int OFF_SUM = OFF_MSG + kMsgSlots * 64;  // a LineSum per warp
+    static constexpr int OFF_MISC = OFF_SUM + 12 * 24;        // TMEM base, abort, joiner[2]
+    static constexpr int USED = OFF_MISC + 16;
+    static constexpr int MIN_SMEM = 120 * 1024;  // one CTA per SM: it owns all of TMEM
+    static constexpr int SMEM_BYTES = (USED > MIN_SMEM ? USED : MIN_SMEM) + 1024;
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+};
+
+constexpr int kPackThreads = 384;
+constexpr int kPackRegsLaunch = 168;
+constexpr int kPackRegsControl = 96;
+constexpr int kPackRegsSoftmax = 200;
+static_assert(4 * kPackRegsControl + 8 * kPackRegsSoftmax <= 12 * kPackRegsLaunch, "register split");
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2p(float lo, float hi) {
+    if constexpr (BF16)
+        return cvt_pack_bf16(lo, hi);
+    else
+        return cvt_pack_f16(lo, hi);
+}
+
+// Query tiles of a unit that hold tokens of the sequence.
+template <int QT>
+__device__ __forceinline__ int live_tiles(const volatile UnitMsg &x, const PackArgs &a) {
+    return x.sq - x.tok0 > a.tile_tokens ? QT : 1;
+}
+
+// A range's last V tile holds rows past the sequence.
+__device__ __forceinline__ bool v_tail(const UnitMsg &x) {
+    return x.nstep > 0 && (x.step0 + x.nstep) * 128 > x.sk;
+}
+
+template <int D, bool PAGED, bool ONE>
+__device__ __forceinline__ void pack_producer(const CUtensorMap *tq, const CUtensorMap *tk,
+                                              const CUtensorMap *tv, uint32_t sbase, const UnitMsg *msgs,
+                                              const PackArgs &a, const WaitGuard &g) {
+    using G = PackGeom<D, ONE>;
+    auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
+    const int lane = threadIdx.x & 31;
+    const uint32_t q_box = a.tile_tokens * a.group * G::ROW_BYTES;  // bytes of one panel of a Q tile
+    // K/V are read again by the sequence's other units, or once in all
+    const uint64_t keep = ONE ? policy_evict_first() : policy_evict_last();
+    const int nbox = PAGED ? G::BN / a.box_rows : 1;  // 1 .. 8 boxes, one per lane
+
+    int q_issued = 0, n_issued = 0;
+    bool ok = true;
+    UnitMsg x;
+    for (int n = 0; ok && take_unit<PAGED>(&x, n, msgs, bar(G::BAR_MF), bar(G::BAR_ME), g, 17); ++n) {
+        // this lane's page of step j, looked up a step ahead
+        auto page_of = [&](int j) {
+            int page = a.num_pages;  // past the pool: TMA fills with zeros
+            const int key = j * G::BN + lane * a.box_rows;
+            if (lane < nbox && j < x.step0 + x.nstep && key < x.sk)
+                page = min(max(__ldg(a.block_table + static_cast<int64_t>(x.seq) * a.max_pages + key / a.page_size),
+                               0),
+                           a.num_pages - 1);
+            return page;
+        };
+        int page = PAGED ? page_of(x.step0) : 0;
+        const int qb = q_issued % G::QBUF;
+        if (!PAGED || lane == 0) {
+            ok = mbar_wait(bar(G::BAR_QE + qb), ((q_issued / G::QBUF) & 1) ^ 1, g, 1);
+            if (ok) {
+                const int n_qt = live_tiles<G::QT>(x, a);
+                mbar_arrive_expect_tx(bar(G::BAR_QF + qb), n_qt * G::PANELS * q_box);
+                for (int t = 0; t < n_qt; ++t)
+                    for (int p = 0; p < G::PANELS; ++p)
+                        tma_load_4d(sbase + G::OFF_Q + qb * G::Q_BUF_BYTES + t * G::TILE_BYTES +
+                                        p * G::PANEL_BYTES,
+                                    tq, bar(G::BAR_QF + qb), p * G::PANEL_ELEMS, 0, x.head,
+                                    x.q0 + x.tok0 + t * a.tile_tokens);
+            }
+        }
+        if (PAGED) ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        ++q_issued;
+        for (int j = x.step0; ok && j < x.step0 + x.nstep; ++j) {
+            const int page_next = PAGED ? page_of(j + 1) : 0;
+            for (int kv = 0; kv < 2; ++kv) {
+                const int s = n_issued % G::SLOTS;
+                if (!PAGED || lane == 0) {
+                    ok = mbar_wait(bar(G::BAR_KVE + s), ((n_issued / G::SLOTS) & 1) ^ 1, g, 2);
+                    if (ok) mbar_arrive_expect_tx(bar(G::BAR_KVF + s), G::TILE_BYTES);
+                }
+                if (PAGED) ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                const CUtensorMap *map = kv ? tv : tk;
+                const uint32_t dst = sbase + G::OFF_KV + s * G::TILE_BYTES;
+                if constexpr (PAGED) {
+                    if (lane < nbox) {
+                        const int prow = (j * G::BN + lane * a.box_rows) % a.page_size;
+                        for (int p = 0; p < G::PANELS; ++p)
+                            tma_load_4d_hint(dst + lane * a.box_rows * G::ROW_BYTES + p * G::PANEL_BYTES, map,
+                                             bar(G::BAR_KVF + s), p * G::PANEL_ELEMS, x.head, prow, page, keep);
+                    }
+                    __syncwarp();
+                } else {
+                    for (int p = 0; p < G::PANELS; ++p)
+                        tma_load_4d_hint(dst + p * G::PANEL_BYTES, map, bar(G::BAR_KVF + s), p * G::PANEL_ELEMS,
+                                         x.head, x.k0 + j * G::BN, 0, keep);
+                }
+                ++n_issued;
+            }
+            page = page_next;
+        }
+    }
+    // Never leave the CTA with a copy still landing in shared memory.
+    if (!PAGED || lane == 0) {
+        WaitGuard drain = g;
+        uint32_t no_abort = 0;
+        drain.abort = &no_abort;
+        for (int n = (q_issued > G::QBUF ? q_issued - G::QBUF : 0); n < q_issued; ++n)
+            mbar_wait(bar(G::BAR_QF + n % G::QBUF), (n / G::QBUF) & 1, drain, 9);
+        for (int n = (n_issued > G::SLOTS ? n_issued - G::SLOTS : 0); n < n_issued; ++n)
+            mbar_wait(bar(G::BAR_KVF + n % G::SLOTS), (n / G::SLOTS) & 1, drain, 10);
+    }
+}
+
+// Warp 2: V rows past the sequence in a range's last tile become zeros. Of
+// those rows only the ones below the next multiple of 16 are read: the P V
+// product stops at the 16-key slice that holds the last key.
+template <int D, bool ONE>
+__device__ __forceinline__ void pack_fix_v(uint32_t sbase, const UnitMsg *msgs, const WaitGuard &g) {
+    using G = PackGeom<D, ONE>;
+    auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
+    const int lane = threadIdx.x & 31;
+    constexpr int CPR = G::ROW_BYTES / 16;  // 16-byte chunks per row and panel
+    int kv_base = 0, fix_cnt = 0;
+    UnitMsg x;
+    for (int n = 0; take_unit<true>(&x, n, msgs, bar(G::BAR_MF), bar(G::BAR_ME), g, 17); ++n) {
+        if (v_tail(x)) {
+            const int nv = 2 * (kv_base + x.nstep - 1) + 1;  // ring item of the last V tile
+            const int slot = nv % G::SLOTS;
+            // the issuer has seen the tile land and holds its slot until the
+            // hand-back, so the ring barrier's phase is this item's
+            bool ok = mbar_wait(bar(G::BAR_VLAND), fix_cnt & 1, g, 15);
+            ok = ok && mbar_wait(bar(G::BAR_KVF + slot), (nv / G::SLOTS) & 1, g, 16);
+            ++fix_cnt;
+            if (!__all_sync(0xffffffffu, ok)) return;
+            const int valid = x.sk - (x.step0 + x.nstep - 1) * G::BN;  // 1 .. 127
+            const int per_panel = (((valid + 15) & ~15) - valid) * CPR;
+            const uint32_t base = sbase + G::OFF_KV + slot * G::TILE_BYTES + valid * G::ROW_BYTES;
+            for (int c = lane; c < per_panel * G::PANELS; c += 32) {
+                const int p = c / per_panel;
+                st_shared_zero16(base + p * G::PANEL_BYTES + (c - p * per_panel) * 16);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(G::BAR_VFIX));
+        }
+        kv_base += x.nstep;
+    }
+}
+
+template <int D, bool BF16, bool ONE>
+__device__ __forceinline__ void pack_mma(uint32_t sbase, uint32_t tmem, const UnitMsg *msgs, const PackArgs &a,
+                                         const WaitGuard &g) {
+    using G = PackGeom<D, ONE>;
+    auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
+    // with a negative scale the S MMAs negate Q, so that the softmax always
+    // works with a scale >= 0
+    const uint32_t idesc_s =
+        mma_idesc_f16(G::BM, G::BN, BF16, false, false) | (a.scale_log2 < 0.f ? kNegateA : 0u);
+    constexpr uint32_t idesc_o = mma_idesc_f16(G::BM, D, BF16, false, true);
+    const uint64_t dq = smem_desc(sbase + G::OFF_Q, 16, G::SBO, G::LAYOUT);                 // K-major
+    const uint64_t dk = smem_desc(sbase + G::OFF_KV, 16, G::SBO, G::LAYOUT);                // K-major
+    const uint64_t dv = smem_desc(sbase + G::OFF_KV, G::PANEL_BYTES, G::SBO, G::LAYOUT);    // MN-major
+
+    // S = Q_t K^T, 16 head-dim elements per instruction
+    auto issue_s = [&](uint32_t tS, uint64_t qdesc, uint64_t kdesc) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const int p = (kk * 16) / G::PANEL_ELEMS;
+            const int off = ((kk * 16) % G::PANEL_ELEMS) * 2;
+            const uint32_t o16 = (p * G::PANEL_BYTES + off) >> 4;
+            mma_ss(tS, qdesc + o16, kdesc + o16, idesc_s, kk > 0 ? 1u : 0u);
+        }
+    };
+    // O (+)= P V over the first `keys` keys of the tile, 16 per instruction
+    auto issue_pv = [&](uint32_t tO, uint32_t tP, uint64_t vdesc, int keys, bool first) {
+#pragma unroll
+        for (int kk = 0; kk < G::BN / 16; ++kk)
+            if (kk * 16 < keys)
+                mma_ts(tO, tP + kk * 8, vdesc + ((kk * 16 * G::ROW_BYTES) >> 4), idesc_o,
+                       (!first || kk > 0) ? 1u : 0u);
+    };
+
+    int it_u = 0;     // units taken
+    int kv_base = 0;  // steps consumed before the current unit
+    int p_cnt[2] = {}, o_cnt[2] = {};
+    int fix_cnt = 0;
+    bool ok = true;
+    UnitMsg x;
+    for (; ok && take_unit<false>(&x, it_u, msgs, bar(G::BAR_MF), bar(G::BAR_ME), g, 17); ++it_u) {
+        const int qbuf = it_u % G::QBUF;
+        if (!mbar_wait(bar(G::BAR_QF + qbuf), (it_u / G::QBUF) & 1, g, 4)) break;
+        const uint64_t qdesc = dq + ((qbuf * G::Q_BUF_BYTES) >> 4);
+        const int nkv = x.nstep;
+        const int last_keys = min(G::BN, x.sk - (x.step0 + nkv - 1) * G::BN);  // of the last step
+        if constexpr (ONE) {
+            // S of step j goes to the S columns of tile (j & 1), so S_{j+1}
+            // is made while the softmax works on S_j; S_{j+2} goes out right
+            // after P_j V_j, which has read the columns it overwrites.
+            const uint32_t tO = tmem + G::TMEM_O_OFF;
+            auto next_s = [&](int j) {
+                const int nk = 2 * (kv_base + j), ks = nk % G::SLOTS;
+                if (!mbar_wait(bar(G::BAR_KVF + ks), (nk / G::SLOTS) & 1, g, 5)) return false;
+                tc_fence_after();
+                issue_s(tmem + (j & 1) * G::TMEM_TILE_STRIDE, qdesc, dk + ((ks * G::TILE_BYTES) >> 4));
+                mma_commit(bar(G::BAR_SF + (j & 1)));
+                mma_commit(bar(G::BAR_KVE + ks));
+                if (j == nkv - 1) mma_commit(bar(G::BAR_QE + qbuf));
+                return true;
+            };
+            if (nkv > 0) ok = next_s(0);
+            if (ok && nkv > 1) ok = next_s(1);
+            for (int j = 0; ok && j < nkv; ++j) {
+                const int nv = 2 * (kv_base + j) + 1, vs = nv % G::SLOTS;
+                if (!mbar_wait(bar(G::BAR_KVF + vs), (nv / G::SLOTS) & 1, g, 6)) {
+                    ok = false;
+                    break;
+                }
+                if (j == nkv - 1 && v_tail(x)) {
+                    mbar_arrive(bar(G::BAR_VLAND));
+                    if (!mbar_wait(bar(G::BAR_VFIX), fix_cnt & 1, g, 11)) {
+                        ok = false;
+                        break;
+                    }
+                    ++fix_cnt;
+                }
+                // the first P V overwrites O: the last unit's must have been read out
+                if (j == 0 && !mbar_wait(bar(G::BAR_OE), (o_cnt[0] & 1) ^ 1, g, 7)) {
+                    ok = false;
+                    break;
+                }
+                if (!mbar_wait(bar(G::BAR_PF + (j & 1)), p_cnt[j & 1] & 1, g, 8)) {
+                    ok = false;
+                    break;
+                }
+                ++p_cnt[j & 1];
+                tc_fence_after();
+                issue_pv(tO, tmem + (j & 1) * G::TMEM_TILE_STRIDE, dv + ((vs * G::TILE_BYTES) >> 4),
+                         j == nkv - 1 ? last_keys : G::BN, j == 0);
+                mma_commit(bar(G::BAR_KVE + vs));
+                mma_commit(bar(G::BAR_PVD));
+                if (j == nkv - 1) mma_commit(bar(G::BAR_OF));
+                if (j + 2 < nkv) ok = next_s(j + 2);
+            }
+            if (!ok) break;
+            if (nkv == 0) {
+                // no key to see: O counts as made, once the last unit's has
+                // been read out (its barrier must not run two phases ahead)
+                if (!mbar_wait(bar(G::BAR_OE), (o_cnt[0] & 1) ^ 1, g, 7)) break;
+                mma_commit(bar(G::BAR_QE + qbuf));
+                mma_commit(bar(G::BAR_OF));
+            }
+            ++o_cnt[0];
+        } else {
+            const int n_qt = live_tiles<G::QT>(x, a);
+            // every wait or commit sits right after a group of MMAs, while
+            // those are queued, never in a clump between two groups
+            for (int j = 0; ok && j <= nkv; ++j) {
+                const int nk = 2 * (kv_base + j), nv = nk - 1;  // ring items K_j, V_{j-1}
+                const int ks = nk % G::SLOTS, vs = nv % G::SLOTS;
+                if (j == nkv && v_tail(x)) {
+                    if (!mbar_wait(bar(G::BAR_VFIX), fix_cnt & 1, g, 11)) {
+                        ok = false;
+                        break;
+                    }
+                    ++fix_cnt;
+                }
+                for (int t = 0; t < n_qt; ++t) {
+                    const uint32_t tS = tmem + t * G::TMEM_TILE_STRIDE;
+                    if (j > 0) {
+                        if (j == 1 && !mbar_wait(bar(G::BAR_OE + t), (o_cnt[t] & 1) ^ 1, g, 7)) {
+                            ok = false;
+                            break;
+                        }
+                        if (!mbar_wait(bar(G::BAR_PF + t), p_cnt[t] & 1, g, 8)) {
+                            ok = false;
+                            break;
+                        }
+                        ++p_cnt[t];
+                        tc_fence_after();
+                        issue_pv(tS + G::TMEM_O_OFF, tS, dv + ((vs * G::TILE_BYTES) >> 4),
+                                 j == nkv ? last_keys : G::BN, j == 1);
+                        if (t == n_qt - 1) mma_commit(bar(G::BAR_KVE + vs));
+                    }
+                    if (j < nkv) {
+                        if (t == 0 && !mbar_wait(bar(G::BAR_KVF + ks), (nk / G::SLOTS) & 1, g, 5)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        issue_s(tS, qdesc + ((t * G::TILE_BYTES) >> 4), dk + ((ks * G::TILE_BYTES) >> 4));
+                        mma_commit(bar(G::BAR_SF + t));
+                        if (t == n_qt - 1) {
+                            mma_commit(bar(G::BAR_KVE + ks));
+                            if (j == nkv - 1) mma_commit(bar(G::BAR_QE + qbuf));
+                        }
+                    } else {
+                        // (no key to see: as above)
+                        if (nkv == 0 && !mbar_wait(bar(G::BAR_OE + t), (o_cnt[t] & 1) ^ 1, g, 7)) {
+                            ok = false;
+                            break;
+                        }
+                        mma_commit(bar(G::BAR_OF + t));
+                    }
+                }
+                if (!ok) break;
+                if (j < nkv &&
+                    !mbar_wait(bar(G::BAR_KVF + (nk + 1) % G::SLOTS), ((nk + 1) / G::SLOTS) & 1, g, 6)) {
+                    ok = false;
+                    break;
+                }
+                if (j == nkv - 1 && v_tail(x)) mbar_arrive(bar(G::BAR_VLAND));
+            }
+            if (nkv == 0) mma_commit(bar(G::BAR_QE + qbuf));
+            for (int t = 0; t < n_qt; ++t) ++o_cnt[t];
+        }
+        kv_base += nkv;
+    }
+    // No MMA may still be running when TMEM is released.
+    mma_commit(bar(G::BAR_DONE));
+    WaitGuard drain = g;
+    uint32_t no_abort = 0;
+    drain.abort = &no_abort;
+    mbar_wait(bar(G::BAR_DONE), 0, drain, 12);
+}
+
+// The four warps of a tile meet: a barrier whose wait is bounded, as a warp
+// that gave up elsewhere never comes.
+__device__ __forceinline__ bool meet(uint32_t bar, int &phase, const WaitGuard &g) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+    const bool ok = mbar_wait(bar, phase & 1, g, 19);
+    ++phase;
+    return __all_sync(0xffffffffu, ok);
+}
+
+// Joins a cut unit's partial results of one query tile: with M the largest
+// LSE_i, l = sum_i 2^(LSE_i - M), O = sum_i 2^(LSE_i - M) O_i / l, LSE = M +
+// log2 l. Run by the tile's 128 threads; a row's columns lie over D / 4 lanes
+// (16-byte loads), a warp takes 4 row slots at a time so that several loads
+// are in flight per thread. Ranges are taken in order with a running maximum.
+template <int D, bool BF16>
+__device__ __forceinline__ void pack_join(int first_part, int nparts, int t, int tiles, int64_t tok0, int head0,
+                                          int rows, const PackArgs &a) {
+    constexpr int LPR = D / 4, RPW = 32 / LPR, R = 4;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
+    const int sub = lane % LPR;
+    for (int r0 = 0; r0 < rows; r0 += 4 * RPW * R) {
+        float m[R], l[R];
+        float4 acc[R];
+        int row[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            row[i] = r0 + (i * 4 + w) * RPW + lane / LPR;
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+            acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll 2
+        for (int p = 0; p < nparts; ++p) {
+            const int64_t part = (static_cast<int64_t>(2 * (first_part + p) + (p == 0 ? 1 : 0)) * tiles + t) * 128;
+            float lp[R];
+            float4 op[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                lp[i] = -INFINITY;
+                op[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (row[i] < rows) {
+                    lp[i] = __ldcg(a.lse_part + part + row[i]);
+                    op[i] = __ldcg(reinterpret_cast<const float4 *>(a.o_part + (part + row[i]) * D) + sub);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float mn = fmaxf(m[i], lp[i]);
+                const float f = m[i] == -INFINITY ? 0.f : fast_exp2(m[i] - mn);
+                const float e = lp[i] == -INFINITY ? 0.f : fast_exp2(lp[i] - mn);
+                m[i] = mn;
+                l[i] = l[i] * f + e;
+                acc[i].x = acc[i].x * f + op[i].x * e;
+                acc[i].y = acc[i].y * f + op[i].y * e;
+                acc[i].z = acc[i].z * f + op[i].z * e;
+                acc[i].w = acc[i].w * f + op[i].w * e;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (row[i] >= rows) continue;
+            const int64_t tok = tok0 + row[i] / a.group;
+            const int head = head0 + row[i] % a.group;
+            const float inv = l[i] == 0.f ? 0.f : 1.0f / l[i];
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + (tok * a.h + head) * D + 4 * sub) =
+                make_uint2(pack2p<BF16>(acc[i].x * inv, acc[i].y * inv),
+                           pack2p<BF16>(acc[i].z * inv, acc[i].w * inv));
+            if (sub == 0)
+                a.lse[static_cast<int64_t>(head) * a.total_q + tok] =
+                    l[i] == 0.f ? -INFINITY : (m[i] + __log2f(l[i])) * 0.69314718055994530942f;
+        }
+    }
+}
+
+template <int D, bool BF16, bool ONE>
+__device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint32_t tmem, const UnitMsg *msgs,
+                                             int t, int q4, const PackArgs &a, const WaitGuard &g) {
+    using G = PackGeom<D, ONE>;
+    auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
+    const uint32_t lane = threadIdx.x & 31;
+    const int row = q4 * 32 + lane;
+    const int row_tok = row / a.group, row_head = row - row_tok * a.group;
+    const bool row_used = row_tok < a.tile_tokens;
+    const uint32_t tS0 = tmem + t * G::TMEM_TILE_STRIDE + (static_cast<uint32_t>(q4 * 32) << 16);
+    const uint32_t tO = tS0 + G::TMEM_O_OFF;
+    const float c = fabsf(a.scale_log2);
+    int s_cnt = 0, s2_cnt = 0, o_cnt = 0;
+    int pv_done = 0;  // ONE: P V products issued before this unit
+    int met = 0;      // meetings of the tile's warps
+    volatile int *joiner = reinterpret_cast<volatile int *>(smem + G::OFF_MISC + 8);
+
+    for (int n = 0;; ++n) {
+        const volatile UnitMsg *x = wait_unit(n, msgs, bar(G::BAR_MF), g, 17);
+        if (x == nullptr) return;
+        if (t >= live_tiles<G::QT>(*x, a)) {
+            free_unit(n, bar(G::BAR_ME));
+            continue;
+        }
+        const int tok = x->tok0 + t * a.tile_tokens + row_tok;  // this row's token in the sequence
+        const bool row_out = row_used && tok < x->sq;
+        // A warp without a row of the sequence skips the math but keeps the
+        // barrier protocol.
+        const bool warp_live = __any_sync(0xffffffffu, row_out);
+        // keys of the range this row sees (0 or less: none)
+        const int sees = (a.causal ? min(x->sk, tok + x->sk - x->sq + 1) : x->sk) - x->step0 * G::BN;
+        const int nstep = x->nstep;
+
+        float m_ref = -INFINITY;  // reference max, log2 units
+        float l = 0.f;            // running sum of 2^(s*c - m_ref)
+        bool alive = true;
+        for (int j = 0; j < nstep; ++j) {
+            const bool alt = ONE && (j & 1);  // ONE: odd steps use the second tile's S columns
+            const uint32_t tS = alt ? tS0 + G::TMEM_TILE_STRIDE : tS0;
+            const bool ok = mbar_wait(bar(alt ? G::BAR_SF + 1 : G::BAR_SF + t), (alt ? s2_cnt : s_cnt) & 1, g, 13);
+            if (alt)
+                ++s2_cnt;
+            else
+                ++s_cnt;
+            if (!__all_sync(0xffffffffu, ok)) {
+                alive = false;
+                break;
+            }
+            tc_fence_after();
+            if (warp_live) {
+                const int valid = sees - j * G::BN;
+                const int vmax = __reduce_max_sync(0xffffffffu, valid);
+                const bool ragged = __any_sync(0xffffffffu, valid < G::BN);
+                uint32_t sr[G::BN];
+                const float *s = reinterpret_cast<const float *>(sr);
+                float mx[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mx[i] = -INFINITY;
+                if (!ragged) {
+                    // the max of the first 64 scores runs while the rest load
+                    tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+                    tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+                    tmem_wait_ld();
+                    tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
+                    tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+                        if (part == 1) tmem_wait_ld();
+#pragma unroll
+                        for (int i = part * G::BN / 4; i < (part + 1) * G::BN / 4; ++i)
+                            mx[i & 3] = max3f(mx[i & 3], s[2 * i], s[2 * i + 1]);
+                    }
+                } else {
+                    // whole 32-key chunks that no row of the warp sees are skipped
+#pragma unroll
+                    for (int c0 = 0; c0 < G::BN; c0 += 32) {
+                        if (c0 < vmax) tmem_ld32(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(&sr[c0]));
+                    }
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c0 = 0; c0 < G::BN; c0 += 32) {
+                        if (c0 < vmax) {
+#pragma unroll
+                            for (int i = c0; i < c0 + 32; ++i) {
+                                if (i < valid) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+                            }
+                        }
+                    }
+                }
+                const float mraw = fmaxf(max3f(mx[0], mx[1], mx[2]), mx[3]);
+                // (a scale of 0 makes every score 0: 0 * -inf must not be NaN)
+                const float m_tile = mraw == -INFINITY ? -INFINITY : mraw * c;
+
+                // the reference max moves only when a tile exceeds it by more
+                // than 8: P stays at most 2^8, exact in 16 bits as below 1
+                const bool need = m_tile > m_ref + 8.0f;
+                const float m_new = need ? m_tile : m_ref;
+                // a row that has seen no key yet keeps m = -inf and alpha 1
+                const float alpha = m_new == -INFINITY ? 1.0f : fast_exp2(m_ref - m_new);
+                m_ref = m_new;
+                const bool rescale = j > 0 && __any_sync(0xffffffffu, need);
+
+                // P = 2^(s*c - m_ref), rounded to 16 bits for the P V product
+                // (the row sum takes the unrounded values), 64 keys at a time;
+                // keys the row does not see get exactly 0
+                const float neg_m = -m_ref;
+                const uint64_t c2 = f2_make(c, c), nm2 = f2_make(neg_m, neg_m);
+                uint64_t acc2[2] = {0ull, 0ull};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t pk[G::BN / 4];
+                    if (!ragged) {
+#pragma unroll
+                        for (int i = 0; i < G::BN / 4; ++i) {
+                            const int k0 = half * (G::BN / 2) + 2 * i;
+                            float x0, x1;
+                            f2_split(f2_fma(f2_make(s[k0], s[k0 + 1]), c2, nm2), x0, x1);
+                            const float p0 = fast_exp2(x0);
+                            const float p1 = fast_exp2(x1);
+                            acc2[i & 1] = f2_add(acc2[i & 1], f2_make(p0, p1));
+                            pk[i] = pack2p<BF16>(p0, p1);
+                        }
+                    } else {
+#pragma unroll
+                        for (int ch = 0; ch < 2; ++ch) {
+                            if (half * (G::BN / 2) + ch * 32 < vmax) {
+#pragma unroll
+                                for (int i = ch * 16; i < ch * 16 + 16; ++i) {
+                                    const int k0 = half * (G::BN / 2) + 2 * i;
+                                    float x0, x1;
+                                    f2_split(f2_fma(f2_make(s[k0], s[k0 + 1]), c2, nm2), x0, x1);
+                                    x0 = (k0 < valid) ? x0 : -INFINITY;
+                                    x1 = (k0 + 1 < valid) ? x1 : -INFINITY;
+                                    const float p0 = fast_exp2(x0);
+                                    const float p1 = fast_exp2(x1);
+                                    acc2[i & 1] = f2_add(acc2[i & 1], f2_make(p0, p1));
+                                    pk[i] = pack2p<BF16>(p0, p1);
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = ch * 16; i < ch * 16 + 16; ++i) pk[i] = 0u;
+                            }
+                        }
+                    }
+                    tmem_st32(tS + half * (G::BN / 4), pk);
+                }
+                if (rescale) {
+                    // O row *= alpha once P_{j-1} V_{j-1} is done: S_j's
+                    // commit covers it where S_j was issued after it; ONE
+                    // issues S_j earlier and waits for that product's own barrier
+                    if (ONE) {
+                        const bool okv = mbar_wait(bar(G::BAR_PVD), (pv_done + j - 1) & 1, g, 15);
+                        if (!__all_sync(0xffffffffu, okv)) {
+                            alive = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 16) {
+                        uint32_t ov[16];
+                        tmem_ld16(tO + c0, ov);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                        tmem_st16(tO + c0, ov);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(alt ? G::BAR_PF + 1 : G::BAR_PF + t));
+                float a0, a1, a2, a3;
+                f2_split(acc2[0], a0, a1);
+                f2_split(acc2[1], a2, a3);
+                l = l * alpha + ((a0 + a1) + (a2 + a3));
+            } else {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(alt ? G::BAR_PF + 1 : G::BAR_PF + t));
+            }
+        }
+        if (!alive) return;
+        if (ONE) pv_done += nstep;
+
+        // ---------------------------------------------------- epilogue
+        // A row that saw no key of the range: O = 0, LSE = -inf. (Not told by
+        // l > 0: a NaN among the row's inputs has to come out as NaN.)
+        const bool empty_row = nstep == 0 || sees <= 0;
+        const float inv_l = empty_row ? 0.0f : 1.0f / l;
+        const int slot = x->slot;
+        const bool part = slot >= 0;
+        const int64_t grow = x->q0 + (row_out ? tok : 0);
+        const int head = x->head * a.group + row_head;
+        uint16_t *dst = static_cast<uint16_t *>(a.o) + (grow * a.h + (row_out ? head : 0)) * D;
+        const int64_t prow =
+            (static_cast<int64_t>(2 * static_cast<int>(blockIdx.x) + max(slot, 0)) * G::QT + t) * 128 + row;
+        const bool o_al32 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
+        const bool ok = mbar_wait(bar(G::BAR_OF + t), o_cnt & 1, g, 14);
+        ++o_cnt;
+        if (!__all_sync(0xffffffffu, ok)) return;
+        tc_fence_after();
+        if (warp_live) {
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += G::OCH) {
+                uint32_t ov[G::OCH];
+                if constexpr (G::OCH == 32)
+                    tmem_ld32(tO + c0, *reinterpret_cast<uint32_t(*)[32]>(ov));
+                else
+                    tmem_ld16(tO + c0, *reinterpret_cast<uint32_t(*)[16]>(ov));
+                tmem_wait_ld();
+                if (!row_out) continue;
+                if (part) {
+#pragma unroll
+                    for (int i = 0; i < G::OCH; ++i)
+                        ov[i] = empty_row ? 0u : __float_as_uint(__uint_as_float(ov[i]) * inv_l);
+#pragma unroll
+                    for (int i = 0; i < G::OCH / 8; ++i)
+                        st_global_v8(a.o_part + prow * D + c0 + 8 * i,
+                                     *reinterpret_cast<const uint32_t(*)[8]>(&ov[8 * i]));
+                } else {
+                    uint32_t pk[G::OCH / 2];
+#pragma unroll
+                    for (int i = 0; i < G::OCH / 2; ++i)
+                        pk[i] = empty_row ? 0u
+                                          : pack2p<BF16>(__uint_as_float(ov[2 * i]) * inv_l,
+                                                         __uint_as_float(ov[2 * i + 1]) * inv_l);
+                    if (o_al32) {
+#pragma unroll
+                        for (int i = 0; i < G::OCH / 16; ++i)
+                            st_global_v8(dst + c0 + 16 * i, *reinterpret_cast<const uint32_t(*)[8]>(&pk[8 * i]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < G::OCH / 8; ++i)
+                            reinterpret_cast<uint4 *>(dst + c0)[i] =
+                                make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                    }
+                }
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(G::BAR_OE + t));
+        const float lse2 = empty_row ? -INFINITY : m_ref + __log2f(l);
+        if (!part) {
+            if (row_out) a.lse[static_cast<int64_t>(head) * a.total_q + grow] = lse2 * 0.69314718055994530942f;
+            free_unit(n, bar(G::BAR_ME));
+            continue;
+        }
+        // A cut unit: count this range's arrival; the last one joins them all.
+        if (row_out) a.lse_part[prow] = lse2;
+        __threadfence();
+        if (!meet(bar(G::BAR_WG + t), met, g)) return;
+        if (row == 0) {
+            // the counter holds (call << 8 | arrivals): one left over by a
+            // call that gave up counts as zero
+            uint32_t *cnt = a.arrivals + x->first_part * G::QT + t;
+            uint32_t old = *reinterpret_cast<volatile uint32_t *>(cnt), seen;
+            do {
+                seen = old;
+                const uint32_t base = (seen >> 8) == a.call ? seen : a.call << 8;
+                old = atomicCAS(cnt, seen, base + 1);
+            } while (old != seen);
+            const uint32_t before = (seen >> 8) == a.call ? (seen & 0xffu) : 0u;
+            const bool last = before + 1 == static_cast<uint32_t>(x->nparts);
+            if (last) atomicExch(cnt, 0u);
+            joiner[t] = last;
+            __threadfence();
+        }
+        if (!meet(bar(G::BAR_WG + t), met, g)) return;
+        if (joiner[t]) {
+            __threadfence();
+            const int tile_tok = x->tok0 + t * a.tile_tokens;
+            const int toks = min(a.tile_tokens, x->sq - tile_tok);
+            pack_join<D, BF16>(x->first_part, x->nparts, t, G::QT, static_cast<int64_t>(x->q0) + tile_tok,
+                               x->head * a.group, toks * a.group, a);
+        }
+        free_unit(n, bar(G::BAR_ME));
+    }
+}
+
+template <int D, bool BF16, bool PAGED, bool ONE>
+__global__ void __launch_bounds__(kPackThreads, 1)
+    pack_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                const __grid_constant__ CUtensorMap tv, const PackArgs a) {
+    using G = PackGeom<D, ONE>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (sbase - raw);
+    auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
+
+    const int warp = threadIdx.x >> 5;
+    const uint32_t lane = threadIdx.x & 31;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + G::OFF_MISC);
+    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + G::OFF_MISC + 4);
+    UnitMsg *msgs = reinterpret_cast<UnitMsg *>(smem + G::OFF_MSG);
+    LineSum *sums = reinterpret_cast<LineSum *>(smem + G::OFF_SUM);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < G::NUM_BARS; ++i) {
+            uint32_t count = 1;
+            if ((i >= G::BAR_PF && i < G::BAR_PF + 2) || (i >= G::BAR_OE && i < G::BAR_OE + 2))
+                count = 4;  // the tile's softmax warps
+            if (i >= G::BAR_WG) count = 4;
+            if (i >= G::BAR_ME && i < G::BAR_WG) count = 3 + 4 * G::QT;  // producer, issuer, zeroing, softmax warps
+            mbar_init(bar(i), count);
+        }
+        *abort_flag = 0u;
+        fence_mbar_init();
+        tma_prefetch_desc(&tq);
+        tma_prefetch_desc(&tk);
+        tma_prefetch_desc(&tv);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), G::TMEM_COLS);
+        tmem_relinquish();
+    }
+    line_sum_warps(a.seqs, a.line, sums);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitGuard g{abort_flag, a.status, kKernFwd};
+
+    if (warp < 4) {
+        reg_dealloc<kPackRegsControl>();
+        if (warp == 0) {
+            if ((PAGED || lane == 0) && !(a.flags & kFlagSkipLoads))
+                pack_producer<D, PAGED, ONE>(&tq, &tk, &tv, sbase, msgs, a, g);
+        } else if (warp == 1) {
+            if (lane == 0) pack_mma<D, BF16, ONE>(sbase, tmem, msgs, a, g);
+        } else if (warp == 2) {
+            pack_fix_v<D, ONE>(sbase, msgs, g);
+        } else {
+            post_units(a.seqs, a.line, line_total(sums, kPackThreads / 32), msgs, bar(G::BAR_MF), bar(G::BAR_ME),
+                       g, 18);
+        }
+    } else {
+        reg_alloc<kPackRegsSoftmax>();
+        if (warp < 4 + 4 * G::QT)
+            pack_softmax<D, BF16, ONE>(smem, sbase, tmem, msgs, (warp - 4) >> 2, warp & 3, a, g);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, G::TMEM_COLS);
+}
+
+template <int D, bool BF16, bool PAGED, bool ONE>
+cudaError_t launch_pack_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const PackArgs &a,
+                          cudaStream_t stream) {
+    using G = PackGeom<D, ONE>;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && !attr_set[dev]) {
+        e = cudaFuncSetAttribute(pack_kernel<D, BF16, PAGED, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 G::SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+        attr_set[dev] = true;
+    }
+    pack_kernel<D, BF16, PAGED, ONE><<<a.ctas, kPackThreads, G::SMEM_BYTES, stream>>>(tq, tk, tv, a);
+    return cudaGetLastError();
+}
+
+template <int D, bool PAGED>
+cudaError_t launch_pack_d(bool bf16, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                          const PackArgs &a, cudaStream_t stream) {
+    if (a.one_tile)
+        return bf16 ? launch_pack_t<D, true, PAGED, true>(tq, tk, tv, a, stream)
+                    : launch_pack_t<D, false, PAGED, true>(tq, tk, tv, a, stream);
+    return bf16 ? launch_pack_t<D, true, PAGED, false>(tq, tk, tv, a, stream)
+                : launch_pack_t<D, false, PAGED, false>(tq, tk, tv, a, stream);
+}
+
+template <bool PAGED>
+cudaError_t launch_pack(int d, bool bf16, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                        const PackArgs &a, cudaStream_t stream) {
+    switch (d) {
+        case 16: return launch_pack_d<16, PAGED>(bf16, tq, tk, tv, a, stream);
+        case 32: return launch_pack_d<32, PAGED>(bf16, tq, tk, tv, a, stream);
+        case 64: return launch_pack_d<64, PAGED>(bf16, tq, tk, tv, a, stream);
+        case 128: return launch_pack_d<128, PAGED>(bf16, tq, tk, tv, a, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+}  // namespace exattn

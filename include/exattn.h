@@ -236,6 +236,120 @@ attn_status_t attn_decode_paged(const void *q, const void *k_pages, const void *
                                 attn_dtype_t dtype, cudaStream_t stream);
 
 /*
+ * ---------------------------------------------------------------------
+ * Packed batches and grouped heads
+ *
+ * Sequences of different lengths lie one behind the other in one tensor of
+ * rows: sequence i holds rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1 (int32
+ * [b + 1], on the device, ascending; a sequence may be empty). Rows that
+ * belong to no sequence are neither used nor written. Starts that are out of
+ * order or past the tensor are clamped: the results then mean nothing, but
+ * no other memory is touched.
+ *
+ * Grouped heads: h query heads share h_kv K/V heads, h a multiple of h_kv
+ * and at most 128 h_kv (ATTN_ERR_UNSUPPORTED above); query head x uses K/V
+ * head x / (h / h_kv). h_kv == h gives every head its own.
+ *
+ * q, k and v may be slices of wider rows: q_stride, k_stride and v_stride
+ * are the distances in elements from one token's row to the next, at least
+ * h * d (h_kv * d) and multiples of 8; within a row, heads are d apart. o,
+ * dout and the page pools are contiguous. lse is fp32 [h, total_q].
+ * Values of another sequence, of rows behind the last sequence, and stale
+ * values in a page never reach a result, whatever they are; a row's own keys
+ * are taken to be finite.
+ */
+
+/*
+ * Forward over packed sequences: for each sequence, O and LSE of attn_fwd
+ * (causal != 0: attn_fwd_causal, aligned to the sequence's own lengths) over
+ * its own rows.
+ *   q, o    [total_q, h, d]    k, v  [total_k, h_kv, d]
+ *   max_seqlen_q  the most rows a sequence has, or 0 if not known. It only
+ *                 picks the kernel's form (results are right whatever it
+ *                 is): units of one 128-row tile where every sequence fits
+ *                 one, else of two.
+ * A row that sees no key gets O = 0 and LSE = -inf. total_q, total_k >= 1.
+ * How the work is dealt out is decided on the device from the lengths; ranges
+ * of a row tile's keys that went to several SMs are joined in a fixed order,
+ * so the same call gives the same bits. Workspace (fp32 partial results, at
+ * most 80 MB) and arrival counters are kept per stream and freed by
+ * attn_release_workspace(); while the stream is being captured into a graph
+ * (and on cudaStreamPerThread) they are taken from the device's memory pool
+ * for the call alone. Errors as attn_fwd.
+ */
+attn_status_t attn_fwd_packed(const void *q, const void *k, const void *v, const int32_t *cu_seqlens_q,
+                              const int32_t *cu_seqlens_k, void *o, float *lse, int b, int total_q,
+                              int total_k, int max_seqlen_q, int h, int h_kv, int d, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, float scale, int causal,
+                              attn_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * The new tokens of each request (one, a few, or a chunk of a prompt) over a
+ * paged cache: attn_decode_paged_ex for grouped heads and requests with
+ * different numbers of new tokens.
+ *   q, o         [total_q, h, d]: request i's rows are cu_seqlens_q[i] ..
+ *                cu_seqlens_q[i + 1] - 1
+ *   k_pages, v_pages  [num_pages, page_size, h_kv, d], page_size a multiple of
+ *                16 (ATTN_ERR_UNSUPPORTED otherwise)
+ *   block_table  int32 [b, max_pages_per_seq]; seqlens_k int32 [b]: keys of
+ *                request i, the new tokens' own included (they are in the
+ *                cache already: attn_paged_write); clamped as in
+ *                attn_decode_paged_ex
+ *   causal       the bottom-right-aligned mask: row r of request i sees key j
+ *                only if j <= r + seqlens_k[i] - (request i's rows)
+ *   max_seqlen_q as in attn_fwd_packed
+ * A long cache is spread over as many SMs as the batch leaves it. Rows
+ * without a key, workspace and errors as attn_fwd_packed.
+ */
+attn_status_t attn_chunk_paged(const void *q, const void *k_pages, const void *v_pages,
+                               const int32_t *block_table, const int32_t *cu_seqlens_q,
+                               const int32_t *seqlens_k, void *o, float *lse, int b, int total_q,
+                               int max_seqlen_q, int h, int h_kv, int d, int num_pages, int page_size,
+                               int max_pages_per_seq, int64_t q_stride, float scale, int causal,
+                               attn_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * Block tables and slot maps of one step, built on the device from request
+ * lengths (nothing is read back to the host).
+ *   seqlens_k    int32 [b] keys each request has in the cache; new_lens int32
+ *                [b] tokens it brings now (0 is fine; negative values count
+ *                as 0)
+ *   free_pages   int32 [num_free]: the free pages as a stack, of which the
+ *                first free_count[0] (int32 [1], clamped to 0 .. num_free) are
+ *                free; pages are taken from its top, in request order
+ *   block_table  int32 [b, max_pages_per_seq], updated in place: the entries of the
+ *                pages a request takes are written, the others left alone
+ *   cu_seqlens_q int32 [b + 1] out: first of each request's new tokens
+ *   seqlens_out  int32 [b] out: keys with the new tokens, at most
+ *                max_pages_per_seq * page_size
+ *   slot_map     int64 [max_tokens] out: new token t's row in the pools seen
+ *                as [num_pages * page_size, h_kv, d]; -1 where it has none, and
+ *                behind the last token
+ *   free_left    int32 [1] out: free pages left. Negative: that many were
+ *                lacking; the entries concerned are -1 in the table and in
+ *                slot_map, and the step must not be run as it is
+ * Outputs may not overlap inputs or each other (the inputs stay as they are,
+ * so a call can be repeated). Errors as attn_fwd.
+ */
+attn_status_t attn_paged_plan(const int32_t *seqlens_k, const int32_t *new_lens, int32_t *block_table,
+                              const int32_t *free_pages, const int32_t *free_count, int32_t *cu_seqlens_q,
+                              int32_t *seqlens_out, int64_t *slot_map, int32_t *free_left, int b,
+                              int max_pages_per_seq, int page_size, int num_free, int64_t max_tokens,
+                              cudaStream_t stream);
+
+/*
+ * New K and V rows into the pages: row t of k and v (token strides k_stride
+ * and v_stride, as above) goes to row slot_map[t] of the pools seen as
+ * [num_pages * page_size, h_kv, d]. Slots outside the pools (-1: a padding
+ * token) are skipped. The same slot twice leaves each 16 bytes of it from one
+ * of the two rows. tokens >= 1; errors as attn_fwd.
+ */
+attn_status_t attn_paged_write(const void *k, const void *v, const int64_t *slot_map, void *k_pages,
+                               void *v_pages, int64_t tokens, int h_kv, int d, int num_pages,
+                               int page_size, int64_t k_stride, int64_t v_stride, attn_dtype_t dtype,
+                               cudaStream_t stream);
+
+/*
  * Split-KV decode that allocates no device memory. The pages have no
  * counterpart: this is a library convenience, not part of the method.
  *
@@ -358,7 +472,20 @@ void attn_debug_set_flags(unsigned int flags);
  */
 int attn_debug_short_plan(int sq, int sk, int h, int d, int grouped_ok, int *out);
 
-/* Library ABI version (major * 100 + minor): 101. */
+/*
+ * Test hook, host-side only: how a packed call of h query heads on h_kv K/V
+ * heads would deal b sequences (host arrays of lengths) to ctas CTAs.
+ * one_tile: units of one 128-row query tile instead of two; by_key != 0: the
+ * key-tile units of the backward. Writes up to max_ranges rows of 9 ints:
+ *   CTA, sequence, K/V head, unit, first step, steps, slot (-1: the unit is
+ *   not cut; 0 / 1: a range that does not / does begin it), and of a cut unit
+ *   the first CTA that shares it and how many do
+ * and returns their number, or -1 on invalid arguments.
+ */
+int attn_debug_packed_plan(const int *seqlens_q, const int *seqlens_k, int b, int h, int h_kv,
+                           int one_tile, int causal, int by_key, int ctas, int max_ranges, int *out);
+
+/* Library ABI version (major * 100 + minor): 102. */
 int attn_version(void);
 
 #ifdef __cplusplus

@@ -274,3 +274,78 @@ def attention_backward(q, k, v, do, scale: float, causal=False):
             dk[bb, :, hh] = scale * (dS.T @ Qh)
             dv[bb, :, hh] = P.T @ dOh
     return dq, dk, dv
+
+
+def _group(x, group):
+    """[1, s, h_kv, d] -> [1, s, h_kv * group, d]: each K/V head repeated for
+    the query heads that share it."""
+    return np.repeat(_f64(x)[None], group, axis=2)
+
+
+def packed_attention(q, k, v, cu_q, cu_k, scale: float, causal=False):
+    """Exact attention of sequences packed one behind the other, with grouped
+    heads (not on the pages; the common reading): sequence i holds query rows
+    cu_q[i] .. cu_q[i + 1] - 1 and key rows cu_k[i] .. cu_k[i + 1] - 1, and
+    query head x uses K/V head x // (h / h_kv).
+
+    q: [total_q, h, d]; k, v: [total_k, h_kv, d]. Returns (o [total_q, h, d],
+    lse [h, total_q]) fp64; rows that see no key, and rows of no sequence,
+    hold O = 0 and LSE = -inf."""
+    t, h, d = q.shape
+    group = h // k.shape[1]
+    o = np.zeros((t, h, d))
+    lse = np.full((h, t), -np.inf)
+    for i in range(len(cu_q) - 1):
+        a, z, ka, kz = int(cu_q[i]), int(cu_q[i + 1]), int(cu_k[i]), int(cu_k[i + 1])
+        if z == a or kz == ka:
+            continue
+        o_i, l_i = attention(_f64(q[a:z])[None], _group(k[ka:kz], group), _group(v[ka:kz], group), scale,
+                             causal=causal)
+        o[a:z], lse[:, a:z] = o_i[0], l_i[0]
+    return o, lse
+
+
+def packed_attention_backward(q, k, v, do, cu_q, cu_k, scale: float, causal=False):
+    """Gradients of ``packed_attention`` by ``attention_backward``; dK and dV of
+    a K/V head are the sums over the query heads that share it. Returns (dq,
+    dk, dv) fp64; rows of no sequence hold 0."""
+    Q, K, V, G = (_f64(x) for x in (q, k, v, do))
+    t, h, d = Q.shape
+    h_kv = K.shape[1]
+    group = h // h_kv
+    dq, dk, dv = np.zeros_like(Q), np.zeros_like(K), np.zeros_like(V)
+    for i in range(len(cu_q) - 1):
+        a, z, ka, kz = int(cu_q[i]), int(cu_q[i + 1]), int(cu_k[i]), int(cu_k[i + 1])
+        if z == a or kz == ka:
+            continue
+        g = attention_backward(Q[a:z][None], _group(K[ka:kz], group), _group(V[ka:kz], group), G[a:z][None],
+                               scale, causal=causal)
+        dq[a:z] = g[0][0]
+        for out, x in ((dk, g[1]), (dv, g[2])):
+            out[ka:kz] = x[0].reshape(kz - ka, h_kv, group, d).sum(axis=2)
+    return dq, dk, dv
+
+
+def paged_plan(seqlens, new_lens, block_table, free_pages, free_count, page_size: int, max_tokens: int):
+    """One step's upkeep of a paged cache, request by request and token by
+    token: pages are taken from the top of the free stack in request order;
+    token j of request i goes to row pos % page_size of page block_table[i, pos
+    // page_size], pos = seqlens[i] + j. Returns (block_table, cu_seqlens_q,
+    seqlens_out, slot_map, free_left) as numpy arrays; entries without a page
+    are -1, and free_left below 0 says how many pages were lacking."""
+    table = np.array(block_table, dtype=np.int64)
+    width = table.shape[1]
+    left = min(max(int(free_count), 0), len(free_pages))
+    slots = np.full(max_tokens, -1, dtype=np.int64)
+    cu, lens = [0], []
+    for i, (old, new) in enumerate(zip(np.maximum(seqlens, 0).tolist(), np.maximum(new_lens, 0).tolist())):
+        for p in range(-(-old // page_size), min(-(-(old + new) // page_size), width)):
+            left -= 1
+            table[i, p] = int(free_pages[left]) if left >= 0 else -1
+        for j in range(new):
+            pos, t = old + j, cu[-1] + j
+            if t < max_tokens and pos < width * page_size and table[i, pos // page_size] >= 0:
+                slots[t] = table[i, pos // page_size] * page_size + pos % page_size
+        cu.append(cu[-1] + new)
+        lens.append(min(old + new, width * page_size))
+    return table, np.array(cu), np.array(lens), slots, left
