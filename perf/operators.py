@@ -290,7 +290,7 @@ def _own(s, c, op):
         return o, lse
     dq, dk, dv = s["grads"]
     ea.attn_bwd_packed(s["q"], s["k"], s["v"], o, lse, s["dout"], s["cu_q"], s["cu_q"],
-                       max_seqlen_q=s["max_q"], dq=dq, dk=dk, dv=dv, causal=c["causal"])
+                       dq=dq, dk=dk, dv=dv, causal=c["causal"])
     return o, lse, dq, dk, dv
 
 
