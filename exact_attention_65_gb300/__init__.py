@@ -83,6 +83,8 @@ def load_library() -> ctypes.CDLL:
         i64 = ctypes.c_int64
         lib.attn_fwd_packed.restype = i32
         lib.attn_fwd_packed.argtypes = [vp] * 7 + [i32] * 7 + [i64] * 3 + [f32, i32, i32, vp]
+        lib.attn_bwd_packed.restype = i32
+        lib.attn_bwd_packed.argtypes = [vp] * 11 + [i32] * 6 + [i64] * 6 + [f32, i32, i32, vp]
         lib.attn_chunk_paged.restype = i32
         lib.attn_chunk_paged.argtypes = [vp] * 8 + [i32] * 9 + [i64, f32, i32, i32, vp]
         lib.attn_paged_plan.restype = i32
@@ -443,6 +445,43 @@ def attn_fwd_packed(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int = 0,
     return out, lse
 
 
+def attn_bwd_packed(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, scale: float | None = None,
+                    dq=None, dk=None, dv=None, stream=None, causal: bool = False):
+    """Backward pass of attn_fwd_packed: returns (dq, dk, dv).
+
+    q, k, v, cu_seqlens_q, cu_seqlens_k, ``causal``: as in the forward; o,
+    lse: its results; dout: [total_q, h, d], contiguous. dq, dk, dv may be
+    slices of wider rows, as q, k, v may (tensors of their own where they are
+    not given); rows of no sequence are left as they were."""
+    if not isinstance(dout, torch.Tensor) or not dout.is_contiguous():
+        raise ValueError("dout must be a contiguous tensor like o")
+    b, t, h, d, dt, idx, qs, o, lse = _packed_q(q, cu_seqlens_q, o, lse)
+    ks, vs = _rows("k", k, idx, q.dtype), _rows("v", v, idx, q.dtype)
+    tk, hk, dk_ = k.shape
+    if v.shape != k.shape or dk_ != d or hk < 1 or h % hk:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
+    if dout.shape != q.shape or dout.dtype is not q.dtype or dout.get_device() != idx:
+        raise ValueError("dout must be a contiguous tensor with q's shape and dtype")
+    _int_array("cu_seqlens_k", cu_seqlens_k, (b + 1,), idx)
+    grads, strides = [], []
+    for name, x, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if x is None:
+            x = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        strides.append(_rows(name, x, idx, q.dtype))
+        if x.shape != like.shape:
+            raise ValueError(f"{name} must have {name[1]}'s shape")
+        grads.append(x)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    lib = _lib or load_library()
+    rc = _call(lib.attn_bwd_packed, idx, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+               lse.data_ptr(), dout.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(),
+               grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(), b, t, tk, h, hk, d, qs, ks, vs,
+               *strides, scale, 1 if causal else 0, dt)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_bwd_packed")
+    return tuple(grads)
+
+
 def _pools(k_pages, v_pages, idx, dt):
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
         if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.get_device() != idx or t.dtype is not dt \
@@ -621,7 +660,7 @@ def attn_debug_set_flags(flags: int) -> None:
 
 __all__ = [
     "AttnError", "attn_fwd", "attn_fwd_host", "attn_bwd", "attn_decode_splitkv",
-    "attn_decode_paged", "attn_fwd_packed", "attn_chunk_paged", "attn_paged_plan", "attn_paged_write",
+    "attn_decode_paged", "attn_fwd_packed", "attn_bwd_packed", "attn_chunk_paged", "attn_paged_plan", "attn_paged_write",
     "attn_decode_splitkv_noalloc", "attn_get_noalloc_status",
     "attn_decode_num_splits",
     "attn_decode_num_splits_for_sms", "attn_get_device_status", "attn_last_timeout_site",

@@ -23,11 +23,11 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libexattn.so")
 
-SOURCES = ["api.cu", "api_packed.cu", "fwd.cu", "fwd_short.cu", "fwd_packed.cu", "chunk_paged.cu", "paged_tables.cu",
-           "bwd.cu", "bwd_short.cu", "decode.cu",
+SOURCES = ["fwd.cu", "fwd_packed.cu", "chunk_paged.cu", "bwd.cu", "fwd_short.cu", "bwd_packed.cu",
+           "bwd_short.cu", "decode.cu", "api.cu", "api_packed.cu", "paged_tables.cu",
            "decode_noalloc.cu"]
-HEADERS = [os.path.join(CSRC, h) for h in ("internal.h", "ptx.cuh", "packed_sched.h", "packed_dev.cuh", "fwd_packed.cuh")] + [
-           os.path.join(INCLUDE, "exattn.h")]
+HEADERS = [os.path.join(CSRC, h) for h in ("internal.h", "ptx.cuh", "packed_sched.h", "packed_dev.cuh",
+                                           "fwd_packed.cuh")] + [os.path.join(INCLUDE, "exattn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC]
 

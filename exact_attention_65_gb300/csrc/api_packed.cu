@@ -30,7 +30,12 @@ LineShape pack_line(int heads, int tile_tokens, bool one_tile, bool causal) {
     return s;
 }
 
-// The key-tile units of the backward: 128 keys against tiles of query tokens.
+// The backward's query-tile units: one tile against steps of 128 keys.
+LineShape bwd_query_line(int heads, int tile_tokens, bool causal) {
+    return pack_line(heads, tile_tokens, true, causal);
+}
+
+// Its key-tile units: 128 keys against tiles of query tokens.
 LineShape bwd_key_line(int heads, int tile_tokens, bool causal) {
     LineShape s;
     s.heads = heads;
@@ -358,6 +363,84 @@ attn_status_t attn_chunk_paged(const void *q, const void *k_pages, const void *v
         !encode_4d(&tv, v_pages, bf16, d, h_kv, page_size, num_pages, box0, a.box_rows, fwd_swizzle(d)))
         return ATTN_ERR_CUDA;
     return run_pack(&a, dev, d, stream, [&] { return launch_chunk_paged(d, bf16, tq, tk, tv, a, stream); });
+}
+
+attn_status_t attn_bwd_packed(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                              const void *dout, const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, void *dq,
+                              void *dk, void *dv, int b, int total_q, int total_k, int h, int h_kv, int d,
+                              int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t dq_stride,
+                              int64_t dk_stride, int64_t dv_stride, float scale, int causal, attn_dtype_t dtype,
+                              cudaStream_t stream) {
+    for (const void *p : {q, k, v, o, dout, static_cast<const void *>(dq), static_cast<const void *>(dk),
+                          static_cast<const void *>(dv)})
+        if (!p || misaligned(p, 16)) return ATTN_ERR_INVALID_ARG;
+    for (const void *p : {static_cast<const void *>(lse), static_cast<const void *>(cu_seqlens_q),
+                          static_cast<const void *>(cu_seqlens_k)})
+        if (!p || misaligned(p, 4)) return ATTN_ERR_INVALID_ARG;
+    if (total_k < 1) return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_packed(b, total_q, h, h_kv, d, scale, dtype);
+    if (st == ATTN_OK && total_k > kMaxRows) st = ATTN_ERR_UNSUPPORTED;
+    const int64_t qrow = static_cast<int64_t>(h) * d, krow = static_cast<int64_t>(h_kv) * d;
+    for (int64_t s : {q_stride, dq_stride})
+        if (st == ATTN_OK) st = check_stride(s, qrow);
+    for (int64_t s : {k_stride, v_stride, dk_stride, dv_stride})
+        if (st == ATTN_OK) st = check_stride(s, krow);
+    if (st != ATTN_OK) return st;
+    int dev = 0, sms = 0;
+    uint32_t *status = nullptr;
+    if ((st = device_info(&dev, &status, &sms)) != ATTN_OK) return st;
+    if (sms < 2) return ATTN_ERR_UNSUPPORTED;
+    const bool bf16 = dtype == ATTN_BF16;
+    PackBwdArgs a;
+    a.seqs.cu_q = cu_seqlens_q;
+    a.seqs.cu_k = cu_seqlens_k;
+    a.seqs.seqlens = nullptr;
+    a.seqs.b = b;
+    a.seqs.total_q = total_q;
+    a.seqs.max_k = total_k;
+    a.o = o;
+    a.dout = dout;
+    a.lse = lse;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.dq_stride = dq_stride;
+    a.dk_stride = dk_stride;
+    a.dv_stride = dv_stride;
+    a.h = h;
+    a.group = h / h_kv;
+    a.tile_tokens = pack_tile_tokens(a.group);
+    a.total_q = total_q;
+    a.causal = causal ? 1 : 0;
+    a.scale = scale;
+    a.scale_log2 = scale * kLog2e;
+    a.status = status;
+    a.flags = debug_flags();
+    a.line[0] = bwd_query_line(h_kv, a.tile_tokens, causal != 0);
+    a.line[1] = bwd_key_line(h_kv, a.tile_tokens, causal != 0);
+    // Both kinds visit the same pairs of tiles; a key-tile step costs about
+    // 1.1 times a query-tile step (four products against three).
+    a.ctas_kv = (sms * 11 + 10) / 21;
+    a.ctas_q = sms - a.ctas_kv;
+    CUtensorMap tq, tk, tv, tdo;
+    if (!encode_rows(&tq, q, bf16, d, h, h_kv, total_q, q_stride, a.tile_tokens) ||
+        !encode_rows(&tdo, dout, bf16, d, h, h_kv, total_q, qrow, a.tile_tokens) ||
+        !encode_keys(&tk, k, bf16, d, h_kv, total_k, k_stride) ||
+        !encode_keys(&tv, v, bf16, d, h_kv, total_k, v_stride))
+        return ATTN_ERR_CUDA;
+    const size_t tile = 128 * static_cast<size_t>(d) * sizeof(float);
+    const size_t part_q = 2 * a.ctas_q * tile, part_kv = 4 * a.ctas_kv * tile;
+    const size_t ld = static_cast<size_t>(total_q) * h * sizeof(float2);
+    Workspace w;
+    if ((st = get_workspace(dev, stream, 2 * sms, part_q + part_kv + ld, &w)) != ATTN_OK) return st;
+    a.arrivals = w.arrivals;
+    a.call = w.call;
+    a.part[0] = reinterpret_cast<float *>(w.part);
+    a.part[1] = reinterpret_cast<float *>(w.part + part_q);
+    a.ld = reinterpret_cast<float2 *>(w.part + part_q + part_kv);
+    const cudaError_t e = launch_bwd_packed(d, bf16, tq, tk, tv, tdo, a, stream);
+    const cudaError_t ef = w.owned ? cudaFreeAsync(w.owned, stream) : cudaSuccess;
+    return (e == cudaSuccess && ef == cudaSuccess) ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 attn_status_t attn_paged_plan(const int32_t *seqlens_k, const int32_t *new_lens, int32_t *block_table,

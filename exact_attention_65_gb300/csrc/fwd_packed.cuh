@@ -418,16 +418,6 @@ __device__ __forceinline__ void pack_mma(uint32_t sbase, uint32_t tmem, const Un
     mbar_wait(bar(G::BAR_DONE), 0, drain, 12);
 }
 
-// The four warps of a tile meet: a barrier whose wait is bounded, as a warp
-// that gave up elsewhere never comes.
-__device__ __forceinline__ bool meet(uint32_t bar, int &phase, const WaitGuard &g) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-    const bool ok = mbar_wait(bar, phase & 1, g, 19);
-    ++phase;
-    return __all_sync(0xffffffffu, ok);
-}
-
 // Joins a cut unit's partial results of one query tile: with M the largest
 // LSE_i, l = sum_i 2^(LSE_i - M), O = sum_i 2^(LSE_i - M) O_i / l, LSE = M +
 // log2 l. Run by the tile's 128 threads; a row's columns lie over D / 4 lanes
@@ -748,19 +738,7 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
         __threadfence();
         if (!meet(bar(G::BAR_WG + t), met, g)) return;
         if (row == 0) {
-            // the counter holds (call << 8 | arrivals): one left over by a
-            // call that gave up counts as zero
-            uint32_t *cnt = a.arrivals + x->first_part * G::QT + t;
-            uint32_t old = *reinterpret_cast<volatile uint32_t *>(cnt), seen;
-            do {
-                seen = old;
-                const uint32_t base = (seen >> 8) == a.call ? seen : a.call << 8;
-                old = atomicCAS(cnt, seen, base + 1);
-            } while (old != seen);
-            const uint32_t before = (seen >> 8) == a.call ? (seen & 0xffu) : 0u;
-            const bool last = before + 1 == static_cast<uint32_t>(x->nparts);
-            if (last) atomicExch(cnt, 0u);
-            joiner[t] = last;
+            joiner[t] = arrive_last(a.arrivals + x->first_part * G::QT + t, a.call, x->nparts);
             __threadfence();
         }
         if (!meet(bar(G::BAR_WG + t), met, g)) return;
@@ -830,7 +808,7 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             pack_fix_v<D, ONE>(sbase, msgs, g);
         } else {
             post_units(a.seqs, a.line, line_total(sums, kPackThreads / 32), msgs, bar(G::BAR_MF), bar(G::BAR_ME),
-                       g, 18);
+                       g, 18, blockIdx.x, gridDim.x);
         }
     } else {
         reg_alloc<kPackRegsSoftmax>();

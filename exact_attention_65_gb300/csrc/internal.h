@@ -240,6 +240,32 @@ cudaError_t launch_fwd_packed(int d, bool bf16, const CUtensorMap &tq, const CUt
 cudaError_t launch_chunk_paged(int d, bool bf16, const CUtensorMap &tq, const CUtensorMap &tk,
                                const CUtensorMap &tv, const PackArgs &a, cudaStream_t stream);
 
+// Backward of the packed forward (bwd_packed.cu). Index 0: query-tile units
+// (dQ), 1: key-tile units (dK, dV).
+struct PackBwdArgs {
+    SeqArrays seqs;
+    LineShape line[2];
+    const void *o, *dout;  // [total_q, h, d]
+    const float *lse;      // [h, total_q]
+    float2 *ld;            // workspace [h_kv, total_q, group]: (LSE log2 e, D)
+    void *dq, *dk, *dv;
+    int64_t dq_stride, dk_stride, dv_stride;  // elements from one token's row to the next
+    int h, group, tile_tokens, total_q, causal;
+    float scale, scale_log2;
+    uint32_t *status;
+    uint32_t flags;
+    int ctas_q, ctas_kv;
+    // cut units: fp32 sums [ctas, 2, accumulators, 128, d], and a counter per
+    // CTA (key-tile CTAs first), valid for call number `call`
+    float *part[2];
+    uint32_t *arrivals;
+    uint32_t call;
+};
+LineShape bwd_query_line(int heads, int tile_tokens, bool causal);
+cudaError_t launch_bwd_packed(int d, bool bf16, const CUtensorMap &tq, const CUtensorMap &tk,
+                              const CUtensorMap &tv, const CUtensorMap &tdo, const PackBwdArgs &a,
+                              cudaStream_t stream);
+
 // ------------------------------------------------------------ paged cache upkeep
 struct PlanArgs {
     const int32_t *seqlens, *new_lens;  // [b]

@@ -75,15 +75,15 @@ __device__ __forceinline__ LineSum line_total(const LineSum *sums, int warps) {
     return t;
 }
 
-// Run by one warp: finds this CTA's part of the line and posts its units.
+// Run by one warp: finds part `part` of the line dealt to `ctas` CTAs and
+// posts its units.
 // `full` / `empty`: kMsgSlots barriers each; `site`: where a timeout of the
 // wait for a free message slot is recorded.
 __device__ __forceinline__ void post_units(const SeqArrays &seqs, const LineShape &shape, const LineSum &total,
                                            UnitMsg *msgs, uint32_t full, uint32_t empty, const WaitGuard &g,
-                                           uint32_t site) {
+                                           uint32_t site, int part, int ctas) {
     const int lane = threadIdx.x & 31;
-    const LineDeal deal = line_deal(shape, total, gridDim.x);
-    const int part = blockIdx.x;
+    const LineDeal deal = line_deal(shape, total, ctas);
     Place p{seqs.b, 0, 0, 0}, e = p;
     int64_t seq_x0 = 0;  // the line before sequence p.seq
     if (part < deal.parts) {
@@ -185,6 +185,30 @@ __device__ __forceinline__ bool take_unit(UnitMsg *m, int n, const UnitMsg *msgs
     if (WARP) __syncwarp();
     if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(empty + 8u * s);
     return m->live != 0;
+}
+
+// Warps meet (as many as the barrier counts): a bounded wait, as a warp that
+// gave up elsewhere never comes.
+__device__ __forceinline__ bool meet(uint32_t bar, int &phase, const WaitGuard &g) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+    const bool ok = mbar_wait(bar, phase & 1, g, 19);
+    ++phase;
+    return __all_sync(0xffffffffu, ok);
+}
+
+// Counts an arrival of call number `call` (24 bits) and tells whether it is
+// the last of n. The counter holds (call << 8 | arrivals): what a call that
+// gave up left there counts as none; the last arrival clears it.
+__device__ __forceinline__ bool arrive_last(uint32_t *counter, uint32_t call, int n) {
+    uint32_t old = *reinterpret_cast<volatile uint32_t *>(counter), seen;
+    do {
+        seen = old;
+        old = atomicCAS(counter, seen, ((seen >> 8) == call ? seen : call << 8) + 1);
+    } while (old != seen);
+    const bool last = ((seen >> 8) == call ? seen & 0xffu : 0u) + 1 == static_cast<uint32_t>(n);
+    if (last) atomicExch(counter, 0u);
+    return last;
 }
 
 // The two halves of take_unit() for warps that are short of registers: wait

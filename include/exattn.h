@@ -284,6 +284,27 @@ attn_status_t attn_fwd_packed(const void *q, const void *k, const void *v, const
                               attn_dtype_t dtype, cudaStream_t stream);
 
 /*
+ * Backward pass of attn_fwd_packed with the same sequences, heads and mask:
+ * attn_bwd's chain rule, where dk and dv of a K/V head are the sums over the
+ * query heads that share it.
+ *   o, dout  [total_q, h, d], lse [h, total_q] as attn_fwd_packed wrote them
+ *   dq       [total_q, h, d], dk, dv [total_k, h_kv, d]; they too may be slices of
+ *            wider rows (dq_stride, dk_stride, dv_stride)
+ * Rows of sequences are written in full (a row without a key gets dq = 0, a
+ * key that no row sees dk = dv = 0), rows of no sequence not at all. No
+ * atomics add into the results: the same call gives the same bits.
+ * Workspace (8 h total_q bytes, and fp32 partial sums of at most 32 MB) as
+ * attn_fwd_packed's. Errors as attn_fwd.
+ */
+attn_status_t attn_bwd_packed(const void *q, const void *k, const void *v, const void *o,
+                              const float *lse, const void *dout, const int32_t *cu_seqlens_q,
+                              const int32_t *cu_seqlens_k, void *dq, void *dk, void *dv, int b,
+                              int total_q, int total_k, int h, int h_kv, int d, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, int64_t dq_stride, int64_t dk_stride,
+                              int64_t dv_stride, float scale, int causal, attn_dtype_t dtype,
+                              cudaStream_t stream);
+
+/*
  * The new tokens of each request (one, a few, or a chunk of a prompt) over a
  * paged cache: attn_decode_paged_ex for grouped heads and requests with
  * different numbers of new tokens.

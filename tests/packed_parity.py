@@ -60,3 +60,46 @@ def check_forward(o, lse, o_ref, lse_ref, a_ref, dtype, slack, rows):
 
 def default_scale(d):
     return 1.0 / math.sqrt(d)
+
+
+def check_backward(grads, q, k, v, o, dout, cq, ck, scale, causal, refs, dtype, slack):
+    """(dq, dk, dv) (device) against the oracle's. Per sequence and head, with P
+    the weights and u, f as above:
+      P and dS are rounded once before the products that add them up, D is
+      the row sum of dO times the rounded O, and each result is rounded:
+        |ddV| <= (u + f) P^T |dO| + u |dV|
+        |ddS| <= (u + f) |dS| + P (e + 2 f |dO| |V|^T),  e = (u + f) rowsum(|dO| (A + |O|))
+        |ddQ| <= scale |ddS| |K| + u |dQ|,  |ddK| <= scale |ddS|^T |Q| + u |dK|."""
+    u, f = unit_roundoff(dtype), slack
+    got = [x.double().cpu().numpy() for x in grads]
+    Q, K, V, O, G = (x.double().cpu().numpy() for x in (q, k, v, o, dout))
+    h, group = Q.shape[1], Q.shape[1] // K.shape[1]
+    bounds = [u * np.abs(r) + 2.0 ** -24 for r in refs]
+    for i in range(len(cq) - 1):
+        a, z, ka, kz = (int(x) for x in (cq[i], cq[i + 1], ck[i], ck[i + 1]))
+        if z == a or kz == ka:
+            continue
+        hidden = np.arange(kz - ka)[None] > np.arange(z - a)[:, None] + (kz - ka) - (z - a)
+        for x in range(h):
+            y = x // group
+            qx, gx, kx, vx = Q[a:z, x], G[a:z, x], K[ka:kz, y], V[ka:kz, y]
+            s = scale * (qx @ kx.T)
+            if causal:
+                s = np.where(hidden, -np.inf, s)
+            m = s.max(axis=1, keepdims=True)
+            p = np.exp(s - np.where(np.isfinite(m), m, 0.0))
+            total = p.sum(axis=1, keepdims=True)
+            p = p / np.where(total > 0, total, 1.0)
+            dp = gx @ vx.T
+            ds = np.abs(p * (dp - (p * dp).sum(axis=1, keepdims=True)))
+            e = (u + f) * (np.abs(gx) * (p @ np.abs(vx) + np.abs(O[a:z, x]))).sum(axis=1, keepdims=True)
+            eds = (u + f) * ds + p * (e + 2 * f * (np.abs(gx) @ np.abs(vx).T))
+            bounds[0][a:z, x] += abs(scale) * (eds @ np.abs(kx))
+            bounds[1][ka:kz, y] += abs(scale) * (eds.T @ np.abs(qx))
+            bounds[2][ka:kz, y] += (u + f) * (p.T @ np.abs(gx))
+    for name, x, ref, bound in zip(("dq", "dk", "dv"), got, refs, bounds):
+        rows = int(cq[-1] if name == "dq" else ck[-1])
+        x, ref, bound = x[:rows], ref[:rows], bound[:rows]
+        assert np.all(np.isfinite(x)), f"{name} is not finite"
+        over = (np.abs(x - ref) - bound).max(initial=-1.0)
+        assert over <= 0, f"{name} off by {np.abs(x - ref).max():.3e}, {over:.3e} over its bound"
