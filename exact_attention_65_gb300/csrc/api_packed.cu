@@ -13,39 +13,64 @@ using namespace exattn;
 
 namespace exattn {
 
+namespace {
+
+// Costs count 2^k steps each where the line would not fit 31 bits.
+void fit_line(LineShape *s, const LineBound &x) {
+    // units, and steps of a unit, at most
+    const double units = (static_cast<double>(s->by_key ? x.total_k : x.total_q) / s->unit_len + x.b) * s->heads;
+    const double steps = static_cast<double>(s->by_key ? x.total_q : x.max_k) * s->weight / (1 << s->shift);
+    fast_division(s->unit_len, &s->unit_mul, &s->unit_div);
+    fast_division(s->step_len, &s->step_mul, &s->step_div);
+    for (double w = units * (steps + s->unit_cost + 1); w > 1.0e9; w /= 2) {
+        ++s->shift;
+        s->unit_cost = s->unit_cost > 1 ? s->unit_cost / 2 : 1;
+        s->min_part = s->min_part > 1 ? s->min_part / 2 : 1;
+    }
+}
+
+}  // namespace
+
 // Where the forward's work is cut (packed_sched.h). A unit's fixed cost (Q,
 // first S, epilogue) counts as one step of 128 keys; units are cut only
 // where each CTA's share is at least four steps, and two steps away from
 // their ends, as joining a cut unit costs about as much as two steps.
-LineShape pack_line(int heads, int tile_tokens, bool one_tile, bool causal) {
+LineShape pack_line(int heads, int group, bool one_tile, bool causal, const LineBound &bound) {
     LineShape s;
     s.heads = heads;
-    s.unit_len = one_tile ? tile_tokens : 2 * tile_tokens;
+    s.unit_len = pack_tile_tokens(group) * (one_tile ? 1 : 2);
     s.step_len = 128;
     s.causal = causal ? 1 : 0;
     s.by_key = 0;
-    s.unit_cost = 128;
+    s.weight = 1;
+    s.shift = 7;
+    s.unit_cost = 1;
     s.min_steps = 2;
-    s.min_part = 4 * 128;
+    s.min_part = 4;
+    fit_line(&s, bound);
     return s;
 }
 
 // The backward's query-tile units: one tile against steps of 128 keys.
-LineShape bwd_query_line(int heads, int tile_tokens, bool causal) {
-    return pack_line(heads, tile_tokens, true, causal);
+LineShape bwd_query_line(int heads, int group, bool causal, const LineBound &bound) {
+    return pack_line(heads, group, true, causal, bound);
 }
 
-// Its key-tile units: 128 keys against tiles of query tokens.
-LineShape bwd_key_line(int heads, int tile_tokens, bool causal) {
+// Its key-tile units: 128 keys against tiles of query tokens, whose heads
+// make rows of them.
+LineShape bwd_key_line(int heads, int group, bool causal, const LineBound &bound) {
     LineShape s;
     s.heads = heads;
     s.unit_len = 128;
-    s.step_len = tile_tokens;
+    s.step_len = pack_tile_tokens(group);
     s.causal = causal ? 1 : 0;
     s.by_key = 1;
-    s.unit_cost = 2 * tile_tokens;
+    s.weight = group;
+    s.shift = 7;
+    s.unit_cost = 2;
     s.min_steps = 2;
-    s.min_part = 8 * static_cast<int64_t>(tile_tokens);
+    s.min_part = 8;
+    fit_line(&s, bound);
     return s;
 }
 
@@ -193,7 +218,7 @@ bool encode_keys(CUtensorMap *map, const void *base, bool bf16, int d, int h_kv,
 
 // Common part of the two forwards: everything but K and V.
 void fill_pack(PackArgs *a, void *o, float *lse, int b, int total_q, int max_seqlen_q, int h, int h_kv,
-               float scale, bool causal, uint32_t *status, int num_sms) {
+               int64_t max_k, float scale, bool causal, uint32_t *status, int num_sms) {
     a->o = o;
     a->lse = lse;
     a->h = h;
@@ -208,7 +233,8 @@ void fill_pack(PackArgs *a, void *o, float *lse, int b, int total_q, int max_seq
     // Units of one query tile where no sequence is known to hold more.
     const int longest = max_seqlen_q > 0 && max_seqlen_q < total_q ? max_seqlen_q : total_q;
     a->one_tile = longest <= a->tile_tokens ? 1 : 0;
-    a->line = pack_line(h_kv, a->tile_tokens, a->one_tile != 0, causal);
+    a->group_inv = pack_group_inv(a->group);
+    a->line = pack_line(h_kv, a->group, a->one_tile != 0, causal, LineBound{b, total_q, max_k, max_k});
     a->seqs.b = b;
     a->seqs.total_q = total_q;
     a->block_table = nullptr;
@@ -257,30 +283,41 @@ int attn_debug_packed_plan(const int *seqlens_q, const int *seqlens_k, int b, in
         return -1;
     for (int i = 0; i < b; ++i)
         if (seqlens_q[i] < 0 || seqlens_k[i] < 0) return -1;
-    const int tokens = pack_tile_tokens(h / h_kv);
-    const LineShape s = by_key ? bwd_key_line(h_kv, tokens, causal != 0)
-                               : pack_line(h_kv, tokens, one_tile != 0, causal != 0);
+    LineBound bound{b, 0, 0, 0};
+    for (int i = 0; i < b; ++i) {
+        bound.total_q += seqlens_q[i];
+        bound.total_k += seqlens_k[i];
+    }
+    bound.max_k = bound.total_k;
+    LineShape s = by_key ? bwd_key_line(h_kv, h / h_kv, causal != 0, bound)
+                         : pack_line(h_kv, h / h_kv, one_tile != 0, causal != 0, bound);
     LineSum sum{0, 0, 0};
     for (int i = 0; i < b; ++i) line_add(&sum, s, seqlens_q[i], seqlens_k[i]);
-    const LineDeal d = line_deal(s, sum, ctas);
-    auto find = [&](int64_t at, int64_t *before) {
+    const LineDeal d = line_deal(&s, sum, ctas);
+    auto find = [&](int at, int *before) {
         *before = 0;
         for (int i = 0; i < b; ++i) {
-            const int64_t cost = s.heads * deal_before(s, d, seqlens_q[i], seqlens_k[i],
-                                                       line_units(s, seqlens_q[i], seqlens_k[i]));
-            if (at < *before + cost) return place_in_seq(s, d, i, seqlens_q[i], seqlens_k[i], at - *before);
+            const int cost =
+                s.heads * line_before(s, seqlens_q[i], seqlens_k[i], line_units(s, seqlens_q[i], seqlens_k[i]));
+            if (at < *before + cost) return place_in_seq(s, i, seqlens_q[i], seqlens_k[i], at - *before);
             *before += cost;
         }
         return Place{b, 0, 0, 0};
     };
     int n = 0;
     for (int c = 0; c < d.parts; ++c) {
-        int64_t x0 = 0, unused = 0;
+        int x0 = 0, unused = 0;
         const Place p = find(part_begin(d, c), &x0), e = find(part_begin(d, c + 1), &unused);
-        walk_part(s, d, b, c, p, e, x0, [&](int i) { return SeqLen{seqlens_q[i], seqlens_k[i]}; },
+        if (p.seq >= b) continue;
+        walk_part(s, b, p, e, SeqLen{seqlens_q[p.seq], seqlens_k[p.seq]},
+                  line_units(s, seqlens_q[p.seq], seqlens_k[p.seq]), x0,
+                  [&](int i) { return SeqLen{seqlens_q[i], seqlens_k[i]}; },
                   [&](const UnitRange &r) {
                       if (n >= max_ranges) return false;
-                      const int row[9] = {c, r.seq, r.head, r.unit, r.step0, r.nstep, r.slot, r.first_part, r.nparts};
+                      int first = c, cuts = 0;
+                      for (int o = 0; r.slot >= 0 && o < d.parts; ++o)
+                          if (part_cuts(s, d, o, r.x0, r.cost, r.steps) && cuts++ == 0) first = o - 1;
+                      const int row[9] = {c, r.seq, r.head, r.unit, r.step0, r.nstep, r.slot, first, cuts + 1};
                       for (int i = 0; i < 9; ++i) out[9 * n + i] = row[i];
                       ++n;
                       return true;
@@ -309,7 +346,7 @@ attn_status_t attn_fwd_packed(const void *q, const void *k, const void *v, const
     if ((st = device_info(&dev, &status, &sms)) != ATTN_OK) return st;
     const bool bf16 = dtype == ATTN_BF16;
     PackArgs a;
-    fill_pack(&a, o, lse, b, total_q, max_seqlen_q, h, h_kv, scale, causal != 0, status, sms);
+    fill_pack(&a, o, lse, b, total_q, max_seqlen_q, h, h_kv, total_k, scale, causal != 0, status, sms);
     a.seqs.cu_q = cu_seqlens_q;
     a.seqs.cu_k = cu_seqlens_k;
     a.seqs.seqlens = nullptr;
@@ -345,7 +382,7 @@ attn_status_t attn_chunk_paged(const void *q, const void *k_pages, const void *v
     if ((st = device_info(&dev, &status, &sms)) != ATTN_OK) return st;
     const bool bf16 = dtype == ATTN_BF16;
     PackArgs a;
-    fill_pack(&a, o, lse, b, total_q, max_seqlen_q, h, h_kv, scale, causal != 0, status, sms);
+    fill_pack(&a, o, lse, b, total_q, max_seqlen_q, h, h_kv, max_k, scale, causal != 0, status, sms);
     a.seqs.cu_q = cu_seqlens_q;
     a.seqs.cu_k = nullptr;
     a.seqs.seqlens = seqlens_k;
@@ -416,8 +453,10 @@ attn_status_t attn_bwd_packed(const void *q, const void *k, const void *v, const
     a.scale_log2 = scale * kLog2e;
     a.status = status;
     a.flags = debug_flags();
-    a.line[0] = bwd_query_line(h_kv, a.tile_tokens, causal != 0);
-    a.line[1] = bwd_key_line(h_kv, a.tile_tokens, causal != 0);
+    a.group_inv = pack_group_inv(a.group);
+    const LineBound bound{b, total_q, total_k, total_k};
+    a.line[0] = bwd_query_line(h_kv, a.group, causal != 0, bound);
+    a.line[1] = bwd_key_line(h_kv, a.group, causal != 0, bound);
     // Both kinds visit the same pairs of tiles; a key-tile step costs about
     // 1.1 times a query-tile step (four products against three).
     a.ctas_kv = (sms * 11 + 10) / 21;

@@ -70,7 +70,7 @@ struct PBwdGeom {
     static constexpr int OFF_LD = OFF_RING + SLOTS * TILE_BYTES;  // [kStages][2][128] LSE, then D
     static constexpr int OFF_MSG = OFF_LD + kStages * 2 * BT * 4;
     static constexpr int OFF_SUM = OFF_MSG + kMsgSlots * 64;
-    static constexpr int OFF_BAR = OFF_SUM + 12 * 24;
+    static constexpr int OFF_BAR = (OFF_SUM + 12 * 12 + 15) & ~15;
     static constexpr int BAR_FF = 0, BAR_FE = 1;
     static constexpr int BAR_RF = 2;
     static constexpr int BAR_RE = BAR_RF + SLOTS;
@@ -86,7 +86,8 @@ struct PBwdGeom {
     static constexpr int BAR_WG = BAR_DONE + 1;  // the elementwise warps meet (cut units)
     static constexpr int BAR_MF = BAR_WG + 1;
     static constexpr int BAR_ME = BAR_MF + kMsgSlots;
-    static constexpr int NUM_BARS = BAR_ME + kMsgSlots;
+    static constexpr int BAR_MS = BAR_ME + kMsgSlots;  // who shares a cut unit
+    static constexpr int NUM_BARS = BAR_MS + kMsgSlots;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;  // TMEM base, abort, joiner
     static constexpr int USED = OFF_MISC + 16;
     static constexpr int MIN_SMEM = 120 * 1024;  // one CTA per SM: it owns all of TMEM
@@ -175,7 +176,7 @@ __device__ __forceinline__ void pbwd_producer(const CUtensorMap *tq, const CUten
     bool ok = true;
     UnitMsg x;
     for (; ok && take_unit<false>(&x, it_u, msgs, bar(G::BAR_MF), bar(G::BAR_ME), g, 17); ++it_u) {
-        if (!mbar_wait(bar(G::BAR_FE), (it_u & 1) ^ 1, g, 1)) break;
+        if (!await(bar(G::BAR_FE), (it_u & 1) ^ 1, g, 1)) break;
         mbar_arrive_expect_tx(bar(G::BAR_FF), 2 * (MODE == kModeDQ ? q_bytes : G::TILE_BYTES));
         const uint32_t fix = sbase + G::OFF_FIX;
         for (int p = 0; p < G::PANELS; ++p) {
@@ -189,7 +190,7 @@ __device__ __forceinline__ void pbwd_producer(const CUtensorMap *tq, const CUten
         }
         for (int i = 0; i < 2 * x.nstep; ++i) {  // step j: K then V, or Q then dO
             const int s = n_issued % G::SLOTS;
-            if (!mbar_wait(bar(G::BAR_RE + s), ((n_issued / G::SLOTS) & 1) ^ 1, g, 2)) {
+            if (!await(bar(G::BAR_RE + s), ((n_issued / G::SLOTS) & 1) ^ 1, g, 2)) {
                 ok = false;
                 break;
             }
@@ -209,9 +210,9 @@ __device__ __forceinline__ void pbwd_producer(const CUtensorMap *tq, const CUten
     WaitGuard drain = g;
     uint32_t no_abort = 0;
     drain.abort = &no_abort;
-    if (it_u > 0) mbar_wait(bar(G::BAR_FF), (it_u - 1) & 1, drain, 9);
+    if (it_u > 0) await(bar(G::BAR_FF), (it_u - 1) & 1, drain, 9);
     for (int n = (n_issued > G::SLOTS ? n_issued - G::SLOTS : 0); n < n_issued; ++n)
-        mbar_wait(bar(G::BAR_RF + n % G::SLOTS), (n / G::SLOTS) & 1, drain, 10);
+        await(bar(G::BAR_RF + n % G::SLOTS), (n / G::SLOTS) & 1, drain, 10);
 }
 
 // Warp 2. Key-tile units: each step's (LSE, D) into shared memory, steps
@@ -240,7 +241,7 @@ __device__ __forceinline__ void pbwd_stage(uint8_t *smem, uint32_t sbase, const 
                     v[i] = r < live ? __ldg(rows + static_cast<int64_t>(tok) * a.group + r)
                                     : make_float2(INFINITY, 0.f);
                 }
-                bool ok = mbar_wait(bar(G::BAR_LDE + s), (((step + j) / kStages) & 1) ^ 1, g, 20);
+                bool ok = await(bar(G::BAR_LDE + s), (((step + j) / kStages) & 1) ^ 1, g, 20);
                 if (!__all_sync(0xffffffffu, ok)) return;
                 float *buf = reinterpret_cast<float *>(smem + G::OFF_LD) + s * 2 * G::BT;
 #pragma unroll
@@ -255,14 +256,14 @@ __device__ __forceinline__ void pbwd_stage(uint8_t *smem, uint32_t sbase, const 
         if (x.nstep > 0) {
             const int rows = tail_rows<MODE>(x, a);
             if (tail_zeroed<MODE>(rows, a)) {
-                const bool ok = mbar_wait(bar(G::BAR_LAND), zeroed & 1, g, 15);
+                const bool ok = await(bar(G::BAR_LAND), zeroed & 1, g, 15);
                 ++zeroed;
                 if (!__all_sync(0xffffffffu, ok)) return;
                 const int per_panel = (((rows + 15) & ~15) - rows) * CPR;
                 for (int w = 0; w < (MODE == kModeDQ ? 1 : 2); ++w) {
                     const int item = 2 * (step + x.nstep - 1) + w, slot = item % G::SLOTS;
                     // (the issuer has seen it land and holds the slot)
-                    const bool okl = mbar_wait(bar(G::BAR_RF + slot), (item / G::SLOTS) & 1, g, 16);
+                    const bool okl = await(bar(G::BAR_RF + slot), (item / G::SLOTS) & 1, g, 16);
                     if (!__all_sync(0xffffffffu, okl)) return;
                     const uint32_t base = sbase + G::OFF_RING + slot * G::TILE_BYTES + rows * G::ROW_BYTES;
                     for (int c = lane; c < per_panel * G::PANELS; c += 32) {
@@ -327,18 +328,18 @@ __device__ __forceinline__ void pbwd_mma(uint32_t sbase, uint32_t tmem, const Un
         const int na = 2 * gs, nb = na + 1;
         sa = na % G::SLOTS;
         sb = nb % G::SLOTS;
-        return mbar_wait(bar(G::BAR_RF + sa), (na / G::SLOTS) & 1, g, 5) &&
-               mbar_wait(bar(G::BAR_RF + sb), (nb / G::SLOTS) & 1, g, 6);
+        return await(bar(G::BAR_RF + sa), (na / G::SLOTS) & 1, g, 5) &&
+               await(bar(G::BAR_RF + sb), (nb / G::SLOTS) & 1, g, 6);
     };
 
     int it_u = 0, base = 0, zeroed = 0;
     bool ok = true;
     UnitMsg x;
     for (; ok && take_unit<false>(&x, it_u, msgs, bar(G::BAR_MF), bar(G::BAR_ME), g, 17); ++it_u) {
-        if (!mbar_wait(bar(G::BAR_FF), it_u & 1, g, 4)) break;
+        if (!await(bar(G::BAR_FF), it_u & 1, g, 4)) break;
         const int count = x.nstep;
         if (count == 0) {  // nothing to add: the accumulators count as made
-            if (!mbar_wait(bar(G::BAR_AE), (it_u & 1) ^ 1, g, 7)) break;
+            if (!await(bar(G::BAR_AE), (it_u & 1) ^ 1, g, 7)) break;
             mma_commit(bar(G::BAR_FE));
             mma_commit(bar(G::BAR_AF));
             continue;
@@ -370,7 +371,7 @@ __device__ __forceinline__ void pbwd_mma(uint32_t sbase, uint32_t tmem, const Un
             const bool last = j == count - 1;
             if (last && zero_tail) {
                 mbar_arrive(bar(G::BAR_LAND));
-                if (!mbar_wait(bar(G::BAR_ZERO), zeroed & 1, g, 11)) {
+                if (!await(bar(G::BAR_ZERO), zeroed & 1, g, 11)) {
                     ok = false;
                     break;
                 }
@@ -378,11 +379,11 @@ __device__ __forceinline__ void pbwd_mma(uint32_t sbase, uint32_t tmem, const Un
             }
             const int rows = last ? rows_tail : rows_full;
             for (int h = 0; h < 2; ++h) {
-                if (!mbar_wait(bar(G::BAR_PF + h), gs & 1, g, 8)) {
+                if (!await(bar(G::BAR_PF + h), gs & 1, g, 8)) {
                     ok = false;
                     break;
                 }
-                if (j == 0 && h == 0 && !mbar_wait(bar(G::BAR_AE), (it_u & 1) ^ 1, g, 7)) {
+                if (j == 0 && h == 0 && !await(bar(G::BAR_AE), (it_u & 1) ^ 1, g, 7)) {
                     ok = false;
                     break;
                 }
@@ -419,7 +420,7 @@ __device__ __forceinline__ void pbwd_mma(uint32_t sbase, uint32_t tmem, const Un
     WaitGuard drain = g;
     uint32_t no_abort = 0;
     drain.abort = &no_abort;
-    mbar_wait(bar(G::BAR_DONE), 0, drain, 12);
+    await(bar(G::BAR_DONE), 0, drain, 12);
 }
 
 // COLS columns of one fp32 TMEM row, scaled, as 16-bit values at dst, or as
@@ -427,7 +428,7 @@ __device__ __forceinline__ void pbwd_mma(uint32_t sbase, uint32_t tmem, const Un
 template <int COLS, bool BF16>
 __device__ __forceinline__ void store_acc(uint32_t taddr, float mul, uint16_t *dst, float *part, bool out,
                                           bool zero) {
-#pragma unroll
+#pragma unroll 1
     for (int c0 = 0; c0 < COLS; c0 += 16) {
         uint32_t v[16];
         tmem_ld16(taddr + c0, v);
@@ -456,6 +457,7 @@ __device__ __forceinline__ void join_sums(int nparts, int rows, float mul, Part 
     constexpr int LPR = D / 4, RPW = 32 / LPR, R = 4;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 4;  // elementwise warp
     const int sub = lane % LPR;
+#pragma unroll 1
     for (int r0 = 0; r0 < rows; r0 += kPBwdWarps * RPW * R) {
         int row[R];
         float4 acc[R];
@@ -464,7 +466,7 @@ __device__ __forceinline__ void join_sums(int nparts, int rows, float mul, Part 
             row[i] = r0 + (i * kPBwdWarps + w) * RPW + lane / LPR;
             acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-#pragma unroll 2
+#pragma unroll 1
         for (int p = 0; p < nparts; ++p) {
             const float *base = part(p);
 #pragma unroll
@@ -495,7 +497,7 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
     const int row = q4 * 32 + lane;  // TMEM lane = row of the unit's tile
     const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
     const float c = a.scale_log2;
-    const int row_tok = row / a.group, row_head = row - row_tok * a.group;
+    const int row_tok = (row * a.group_inv) >> 16, row_head = row - row_tok * a.group;
     volatile int *joiner = reinterpret_cast<volatile int *>(smem + G::OFF_MISC + 8);
     int step = 0, met = 0;
     for (int it_u = 0;; ++it_u) {
@@ -525,7 +527,7 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
             const float *ldbuf = nullptr;
             int cmin = 0, cmax = G::BT;  // (DKV) the step's columns [cmin, cmax) see this key
             if constexpr (MODE == kModeDKV) {
-                const bool okl = mbar_wait(bar(G::BAR_LDF + step % kStages), (step / kStages) & 1, g, 21);
+                const bool okl = await(bar(G::BAR_LDF + step % kStages), (step / kStages) & 1, g, 21);
                 if (!__all_sync(0xffffffffu, okl)) return;
                 ldbuf = reinterpret_cast<const float *>(smem + G::OFF_LD) + (step % kStages) * 2 * G::BT;
                 cmin = min(max(from - j * a.tile_tokens, 0), a.tile_tokens) * a.group;
@@ -534,7 +536,7 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
                 cmax = sees - j * G::BT;
             }
             const bool masked = __any_sync(0xffffffffu, cmin > 0 || cmax < G::BT);
-            const bool ok = mbar_wait(bar(G::BAR_SF), step & 1, g, 13);
+            const bool ok = await(bar(G::BAR_SF), step & 1, g, 13);
             if (!__all_sync(0xffffffffu, ok)) return;
             tc_fence_after();
 #pragma unroll 1
@@ -597,7 +599,7 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
         }
 
         // ---------------------------------------------------- epilogue
-        const bool ok = mbar_wait(bar(G::BAR_AF), it_u & 1, g, 14);
+        const bool ok = await(bar(G::BAR_AF), it_u & 1, g, 14);
         if (!__all_sync(0xffffffffu, ok)) return;
         tc_fence_after();
         // each group stores half of the columns (d = 16: group 0 all of them)
@@ -629,6 +631,8 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
         if (lane == 0) mbar_arrive(bar(G::BAR_AE));
         if (slot >= 0) {
             // a cut unit: count this range's arrival; the last one adds them
+            const bool ok = await(bar(G::BAR_MS + it_u % kMsgSlots), (it_u / kMsgSlots) & 1, g, 23);
+            if (!__all_sync(0xffffffffu, ok)) return;
             __threadfence();
             if (!meet(bar(G::BAR_WG), met, g)) return;
             if (threadIdx.x == 128) {
@@ -650,7 +654,7 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
                     const int64_t q0 = x->q0 + t0;
                     join_sums<D, BF16>(n, min(a.tile_tokens, x->sq - t0) * a.group, a.scale, part_of(0),
                                        [&](int r) {
-                                           const int tok = r / a.group;
+                                           const int tok = (r * a.group_inv) >> 16;
                                            return static_cast<uint16_t *>(a.dq) + (q0 + tok) * a.dq_stride +
                                                   (head * a.group + r - tok * a.group) * D;
                                        });
@@ -686,9 +690,11 @@ __device__ __forceinline__ void pbwd_run(const CUtensorMap *tq, const CUtensorMa
     } else if (warp == 2) {
         pbwd_stage<D, MODE>(smem, sbase, msgs, a, g);
     } else if (warp == 3) {
-        post_units(a.seqs, a.line[MODE],
-                   line_total(reinterpret_cast<const LineSum *>(smem + G::OFF_SUM), kPBwdThreads / 32),
-                   reinterpret_cast<UnitMsg *>(smem + G::OFF_MSG), bar(G::BAR_MF), bar(G::BAR_ME), g, 18, cta, ctas);
+        const LineSum *sums = reinterpret_cast<const LineSum *>(smem + G::OFF_SUM);
+        post_units<MODE == kModeDKV>(
+            a.seqs, a.line[MODE], [&] { return line_total(sums, kPBwdThreads / 32); },
+            reinterpret_cast<UnitMsg *>(smem + G::OFF_MSG), bar(G::BAR_MF), bar(G::BAR_ME), bar(G::BAR_MS), g, 18, cta,
+            ctas);
     } else {
         pbwd_compute<D, MODE, BF16>(smem, sbase, tmem, msgs, warp & 3, (warp - 4) >> 2, cta, a, g);
     }
@@ -716,7 +722,7 @@ __global__ void __launch_bounds__(kPBwdThreads, 1)
             if ((i >= G::BAR_PF && i < G::BAR_PF + 2) || i == G::BAR_AE || i == G::BAR_WG ||
                 (i >= G::BAR_LDE && i < G::BAR_LDE + kStages))
                 count = kPBwdWarps;
-            if (i >= G::BAR_ME) count = 3 + kPBwdWarps;  // producer, issuer, staging, elementwise warps
+            if (i >= G::BAR_ME && i < G::BAR_MS) count = 3 + kPBwdWarps;  // producer, issuer, staging, elementwise warps
             mbar_init(bar(i), count);
         }
         *abort_flag = 0u;
@@ -742,7 +748,11 @@ __global__ void __launch_bounds__(kPBwdThreads, 1)
         }
         fence_proxy_async_smem();
     }
-    line_sum_warps(a.seqs, a.line[keys ? kModeDKV : kModeDQ], reinterpret_cast<LineSum *>(smem + G::OFF_SUM));
+    LineSum *sums = reinterpret_cast<LineSum *>(smem + G::OFF_SUM);
+    if (keys)
+        line_sum_warps<1>(a.seqs, a.line[kModeDKV], sums);
+    else
+        line_sum_warps<0>(a.seqs, a.line[kModeDQ], sums);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -21,10 +21,15 @@
 // order of the keys, so the result does not depend on who that is.
 //
 // Roles (384 threads, one CTA per SM): warp 0 TMA producer (a whole warp for
-// pages, one box per lane), warp 1 MMA issuer, warp 2 zeroes the V rows of a
-// unit's last tile that lie past the sequence (they belong to the next
-// sequence or are stale, P is 0 there, and 0 * NaN is NaN), warp 3 deals out
-// units, warps 4-7 and 8-11 softmax and epilogue of tile 0 and 1.
+// pages, one box per lane), warps 1 and 2 issue the MMAs of tile 0 and 1, warp
+// 3 deals out units, warps 4-7 and 8-11 softmax and epilogue of tile 0 and 1.
+// An issuer waits, counts and issues for about 1,300 cycles per step, the
+// tensor pipe's own time for its tile; with one thread for both tiles the pipe
+// stood still a third of the time (b1 s8192 h32 d128: 888 us, now XXX).
+//
+// V rows of a unit's last tile that lie past the sequence belong to the next
+// sequence or are stale; P is 0 there, and 0 * NaN is NaN: the issuers zero
+// those below the next multiple of 16, where the P V product stops.
 //
 // What bounds it: long prompts, the tensor pipe and the exponentials; single
 // tokens, HBM (each SM keeps the ring, 160 to 192 KB at d = 128, in flight);
@@ -80,15 +85,15 @@ struct PackGeom {
     static constexpr int BAR_OE = BAR_OF + 2;       // [2] O read out
     static constexpr int BAR_PVD = BAR_OF + 1;
     static constexpr int BAR_DONE = BAR_OE + 2;
-    static constexpr int BAR_VLAND = BAR_DONE + 1;  // a last V tile landed (MMA -> zeroing)
-    static constexpr int BAR_VFIX = BAR_VLAND + 1;  // its rows past the sequence zeroed
-    static constexpr int BAR_MF = BAR_VFIX + 1;     // [kMsgSlots] unit message posted
+    static constexpr int BAR_TURN = BAR_DONE + 2;  // [2] the tile's issuer may issue
+    static constexpr int BAR_MF = BAR_TURN + 2;    // [kMsgSlots] unit message posted
     static constexpr int BAR_ME = BAR_MF + kMsgSlots;
-    static constexpr int BAR_WG = BAR_ME + kMsgSlots;  // [2] a tile's softmax warps meet (cut units)
+    static constexpr int BAR_MS = BAR_ME + kMsgSlots;  // [kMsgSlots] who shares a cut unit
+    static constexpr int BAR_WG = BAR_MS + kMsgSlots;  // [2] a tile's softmax warps meet (cut units)
     static constexpr int NUM_BARS = BAR_WG + 2;
     static constexpr int OFF_MSG = (OFF_BAR + NUM_BARS * 8 + 15) & ~15;
     static constexpr int OFF_SUM = OFF_MSG + kMsgSlots * 64;  // a LineSum per warp
-    static constexpr int OFF_MISC = OFF_SUM + 12 * 24;        // TMEM base, abort, joiner[2]
+    static constexpr int OFF_MISC = OFF_SUM + 12 * 12;        // TMEM base, abort, joiner[2]
     static constexpr int USED = OFF_MISC + 16;
     static constexpr int MIN_SMEM = 120 * 1024;  // one CTA per SM: it owns all of TMEM
     static constexpr int SMEM_BYTES = (USED > MIN_SMEM ? USED : MIN_SMEM) + 1024;
@@ -115,12 +120,25 @@ __device__ __forceinline__ int live_tiles(const volatile UnitMsg &x, const PackA
     return x.sq - x.tok0 > a.tile_tokens ? QT : 1;
 }
 
-// A range's last V tile holds rows past the sequence.
-__device__ __forceinline__ bool v_tail(const UnitMsg &x) {
-    return x.nstep > 0 && (x.step0 + x.nstep) * 128 > x.sk;
-}
+// The ring of K and V tiles as a warp walks it: K_0, V_0, K_1, V_1, ...
+template <int SLOTS>
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == SLOTS) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
 
-template <int D, bool PAGED, bool ONE>
+// The TMA producer: Q and the K and V tiles, through one ring in the order K_0,
+// V_0, K_1, V_1, ... A thread issues a box every 100 cycles or so, and a tile
+// of 16-key pages is 16 boxes at d = 128, more than a step from HBM takes; so
+// the paged one-tile form has two producer warps, one for Q and K and one for
+// V (WHICH 0 and 1; 2: both).
+template <int D, bool PAGED, bool ONE, int WHICH>
 __device__ __forceinline__ void pack_producer(const CUtensorMap *tq, const CUtensorMap *tk,
                                               const CUtensorMap *tv, uint32_t sbase, const UnitMsg *msgs,
                                               const PackArgs &a, const WaitGuard &g) {
@@ -132,44 +150,60 @@ __device__ __forceinline__ void pack_producer(const CUtensorMap *tq, const CUten
     const uint64_t keep = ONE ? policy_evict_first() : policy_evict_last();
     const int nbox = PAGED ? G::BN / a.box_rows : 1;  // 1 .. 8 boxes, one per lane
 
-    int q_issued = 0, n_issued = 0;
+    int qb = 0;
+    uint32_t q_phase = 1;
+    Ring<G::SLOTS> ring;
+    ring.phase = 1;
+    int q_issued = 0, n_issued = 0;  // items that this warp has issued
     bool ok = true;
     UnitMsg x;
+#pragma unroll 1
     for (int n = 0; ok && take_unit<PAGED>(&x, n, msgs, bar(G::BAR_MF), bar(G::BAR_ME), g, 17); ++n) {
+        const int end = x.step0 + x.nstep;
         // this lane's page of step j, looked up a step ahead
         auto page_of = [&](int j) {
             int page = a.num_pages;  // past the pool: TMA fills with zeros
             const int key = j * G::BN + lane * a.box_rows;
-            if (lane < nbox && j < x.step0 + x.nstep && key < x.sk)
+            if (lane < nbox && j < end && key < x.sk)
                 page = min(max(__ldg(a.block_table + static_cast<int64_t>(x.seq) * a.max_pages + key / a.page_size),
                                0),
                            a.num_pages - 1);
             return page;
         };
         int page = PAGED ? page_of(x.step0) : 0;
-        const int qb = q_issued % G::QBUF;
-        if (!PAGED || lane == 0) {
-            ok = mbar_wait(bar(G::BAR_QE + qb), ((q_issued / G::QBUF) & 1) ^ 1, g, 1);
-            if (ok) {
-                const int n_qt = live_tiles<G::QT>(x, a);
-                mbar_arrive_expect_tx(bar(G::BAR_QF + qb), n_qt * G::PANELS * q_box);
-                for (int t = 0; t < n_qt; ++t)
-                    for (int p = 0; p < G::PANELS; ++p)
-                        tma_load_4d(sbase + G::OFF_Q + qb * G::Q_BUF_BYTES + t * G::TILE_BYTES +
-                                        p * G::PANEL_BYTES,
-                                    tq, bar(G::BAR_QF + qb), p * G::PANEL_ELEMS, 0, x.head,
-                                    x.q0 + x.tok0 + t * a.tile_tokens);
+        if (WHICH != 1) {
+            if (!PAGED || lane == 0) {
+                ok = await(bar(G::BAR_QE + qb), q_phase, g, 1);
+                if (ok) {
+                    const int n_qt = live_tiles<G::QT>(x, a);
+                    mbar_arrive_expect_tx(bar(G::BAR_QF + qb), n_qt * G::PANELS * q_box);
+#pragma unroll 1
+                    for (int t = 0; t < n_qt; ++t)
+#pragma unroll
+                        for (int p = 0; p < G::PANELS; ++p)
+                            tma_load_4d(sbase + G::OFF_Q + qb * G::Q_BUF_BYTES + t * G::TILE_BYTES +
+                                            p * G::PANEL_BYTES,
+                                        tq, bar(G::BAR_QF + qb), p * G::PANEL_ELEMS, 0, x.head,
+                                        x.q0 + x.tok0 + t * a.tile_tokens);
+                }
+            }
+            if (PAGED) ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            ++q_issued;
+            if (++qb == G::QBUF) {
+                qb = 0;
+                q_phase ^= 1u;
             }
         }
-        if (PAGED) ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        ++q_issued;
-        for (int j = x.step0; ok && j < x.step0 + x.nstep; ++j) {
+#pragma unroll 1
+        for (int j = x.step0; ok && j < end; ++j) {
             const int page_next = PAGED ? page_of(j + 1) : 0;
-            for (int kv = 0; kv < 2; ++kv) {
-                const int s = n_issued % G::SLOTS;
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv, ring.next()) {
+                if (WHICH != 2 && kv != WHICH) continue;
+                const int s = ring.slot;
                 if (!PAGED || lane == 0) {
-                    ok = mbar_wait(bar(G::BAR_KVE + s), ((n_issued / G::SLOTS) & 1) ^ 1, g, 2);
+                    ok = await(bar(G::BAR_KVE + s), ring.phase, g, 2);
                     if (ok) mbar_arrive_expect_tx(bar(G::BAR_KVF + s), G::TILE_BYTES);
                 }
                 if (PAGED) ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -179,12 +213,14 @@ __device__ __forceinline__ void pack_producer(const CUtensorMap *tq, const CUten
                 if constexpr (PAGED) {
                     if (lane < nbox) {
                         const int prow = (j * G::BN + lane * a.box_rows) % a.page_size;
+#pragma unroll
                         for (int p = 0; p < G::PANELS; ++p)
                             tma_load_4d_hint(dst + lane * a.box_rows * G::ROW_BYTES + p * G::PANEL_BYTES, map,
                                              bar(G::BAR_KVF + s), p * G::PANEL_ELEMS, x.head, prow, page, keep);
                     }
                     __syncwarp();
                 } else {
+#pragma unroll
                     for (int p = 0; p < G::PANELS; ++p)
                         tma_load_4d_hint(dst + p * G::PANEL_BYTES, map, bar(G::BAR_KVF + s), p * G::PANEL_ELEMS,
                                          x.head, x.k0 + j * G::BN, 0, keep);
@@ -194,67 +230,43 @@ __device__ __forceinline__ void pack_producer(const CUtensorMap *tq, const CUten
             page = page_next;
         }
     }
-    // Never leave the CTA with a copy still landing in shared memory.
+    // Never leave the CTA with a copy still landing in shared memory: wait for
+    // the last items of this warp (an item that was not issued leaves its
+    // barrier alone, so its wait would run out: only issued ones are waited for).
     if (!PAGED || lane == 0) {
         WaitGuard drain = g;
         uint32_t no_abort = 0;
         drain.abort = &no_abort;
-        for (int n = (q_issued > G::QBUF ? q_issued - G::QBUF : 0); n < q_issued; ++n)
-            mbar_wait(bar(G::BAR_QF + n % G::QBUF), (n / G::QBUF) & 1, drain, 9);
-        for (int n = (n_issued > G::SLOTS ? n_issued - G::SLOTS : 0); n < n_issued; ++n)
-            mbar_wait(bar(G::BAR_KVF + n % G::SLOTS), (n / G::SLOTS) & 1, drain, 10);
+#pragma unroll 1
+        for (int i = (q_issued > G::QBUF ? q_issued - G::QBUF : 0); i < q_issued; ++i)
+            await(bar(G::BAR_QF + i % G::QBUF), (i / G::QBUF) & 1, drain, 9);
+        constexpr int EACH = WHICH == 2 ? 1 : 2;  // this warp's items are every EACH-th
+        static_assert(WHICH == 2 || G::SLOTS % 2 == 0, "a slot belongs to one of the two");
+#pragma unroll 1
+        for (int i = (n_issued > G::SLOTS / EACH ? n_issued - G::SLOTS / EACH : 0); i < n_issued; ++i) {
+            const int item = i * EACH + (WHICH == 1 ? 1 : 0);
+            await(bar(G::BAR_KVF + item % G::SLOTS), (item / G::SLOTS) & 1, drain, 10);
+        }
     }
 }
 
-// Warp 2: V rows past the sequence in a range's last tile become zeros. Of
-// those rows only the ones below the next multiple of 16 are read: the P V
-// product stops at the 16-key slice that holds the last key.
-template <int D, bool ONE>
-__device__ __forceinline__ void pack_fix_v(uint32_t sbase, const UnitMsg *msgs, const WaitGuard &g) {
+// The MMAs of tile t (ONE: of the only tile). A whole warp: lane 0 issues, all
+// lanes zero the V tail.
+template <int D, bool BF16, bool ONE>
+__device__ __forceinline__ void pack_issue(uint32_t sbase, uint32_t tmem, const UnitMsg *msgs, int t,
+                                           const PackArgs &a, const WaitGuard &g) {
     using G = PackGeom<D, ONE>;
     auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
     const int lane = threadIdx.x & 31;
-    constexpr int CPR = G::ROW_BYTES / 16;  // 16-byte chunks per row and panel
-    int kv_base = 0, fix_cnt = 0;
-    UnitMsg x;
-    for (int n = 0; take_unit<true>(&x, n, msgs, bar(G::BAR_MF), bar(G::BAR_ME), g, 17); ++n) {
-        if (v_tail(x)) {
-            const int nv = 2 * (kv_base + x.nstep - 1) + 1;  // ring item of the last V tile
-            const int slot = nv % G::SLOTS;
-            // the issuer has seen the tile land and holds its slot until the
-            // hand-back, so the ring barrier's phase is this item's
-            bool ok = mbar_wait(bar(G::BAR_VLAND), fix_cnt & 1, g, 15);
-            ok = ok && mbar_wait(bar(G::BAR_KVF + slot), (nv / G::SLOTS) & 1, g, 16);
-            ++fix_cnt;
-            if (!__all_sync(0xffffffffu, ok)) return;
-            const int valid = x.sk - (x.step0 + x.nstep - 1) * G::BN;  // 1 .. 127
-            const int per_panel = (((valid + 15) & ~15) - valid) * CPR;
-            const uint32_t base = sbase + G::OFF_KV + slot * G::TILE_BYTES + valid * G::ROW_BYTES;
-            for (int c = lane; c < per_panel * G::PANELS; c += 32) {
-                const int p = c / per_panel;
-                st_shared_zero16(base + p * G::PANEL_BYTES + (c - p * per_panel) * 16);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(G::BAR_VFIX));
-        }
-        kv_base += x.nstep;
-    }
-}
-
-template <int D, bool BF16, bool ONE>
-__device__ __forceinline__ void pack_mma(uint32_t sbase, uint32_t tmem, const UnitMsg *msgs, const PackArgs &a,
-                                         const WaitGuard &g) {
-    using G = PackGeom<D, ONE>;
-    auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
     // with a negative scale the S MMAs negate Q, so that the softmax always
     // works with a scale >= 0
     const uint32_t idesc_s =
         mma_idesc_f16(G::BM, G::BN, BF16, false, false) | (a.scale_log2 < 0.f ? kNegateA : 0u);
     constexpr uint32_t idesc_o = mma_idesc_f16(G::BM, D, BF16, false, true);
-    const uint64_t dq = smem_desc(sbase + G::OFF_Q, 16, G::SBO, G::LAYOUT);                 // K-major
-    const uint64_t dk = smem_desc(sbase + G::OFF_KV, 16, G::SBO, G::LAYOUT);                // K-major
-    const uint64_t dv = smem_desc(sbase + G::OFF_KV, G::PANEL_BYTES, G::SBO, G::LAYOUT);    // MN-major
+    const uint64_t dq = smem_desc(sbase + G::OFF_Q + t * G::TILE_BYTES, 16, G::SBO, G::LAYOUT);  // K-major
+    const uint64_t dk = smem_desc(sbase + G::OFF_KV, 16, G::SBO, G::LAYOUT);                     // K-major
+    const uint64_t dv = smem_desc(sbase + G::OFF_KV, G::PANEL_BYTES, G::SBO, G::LAYOUT);         // MN-major
+    constexpr uint32_t tile16 = G::TILE_BYTES >> 4;
 
     // S = Q_t K^T, 16 head-dim elements per instruction
     auto issue_s = [&](uint32_t tS, uint64_t qdesc, uint64_t kdesc) {
@@ -263,6 +275,8 @@ __device__ __forceinline__ void pack_mma(uint32_t sbase, uint32_t tmem, const Un
             const int p = (kk * 16) / G::PANEL_ELEMS;
             const int off = ((kk * 16) % G::PANEL_ELEMS) * 2;
             const uint32_t o16 = (p * G::PANEL_BYTES + off) >> 4;
+            // the turn passes while the last quarter is still to be queued
+            if (!ONE && kk == D / 16 * 3 / 4) mbar_arrive(bar(G::BAR_TURN + (t ^ 1)));
             mma_ss(tS, qdesc + o16, kdesc + o16, idesc_s, kk > 0 ? 1u : 0u);
         }
     };
@@ -274,161 +288,184 @@ __device__ __forceinline__ void pack_mma(uint32_t sbase, uint32_t tmem, const Un
                 mma_ts(tO, tP + kk * 8, vdesc + ((kk * 16 * G::ROW_BYTES) >> 4), idesc_o,
                        (!first || kk > 0) ? 1u : 0u);
     };
+    // zeros into the rows of a landed V tile from `keys` up to a multiple of 16
+    auto zero_tail = [&](int slot, int keys) {
+        constexpr int CPR = G::ROW_BYTES / 16;
+        const int per_panel = (((keys + 15) & ~15) - keys) * CPR;
+        const uint32_t base = sbase + G::OFF_KV + slot * G::TILE_BYTES + keys * G::ROW_BYTES;
+#pragma unroll 1
+        for (int c = lane; c < per_panel * G::PANELS; c += 32) {
+            const int p = c >= per_panel ? 1 : 0;
+            st_shared_zero16(base + p * G::PANEL_BYTES + (c - p * per_panel) * 16);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+    };
+    static_assert(G::PANELS <= 2, "panels of a tile");
 
-    int it_u = 0;     // units taken
-    int kv_base = 0;  // steps consumed before the current unit
-    int p_cnt[2] = {}, o_cnt[2] = {};
-    int fix_cnt = 0;
+    Ring<G::SLOTS> ring;
+    int qbuf = 0;
+    uint32_t q_phase = 0;         // of the Q buffers
+    uint32_t p_phase = 0;         // P stored; ONE: bit 0 and 1, of even and odd steps
+    uint32_t o_phase = 0;         // O handed back
+    uint32_t turn = t ^ 1u;       // tile 0 goes first
     bool ok = true;
     UnitMsg x;
-    for (; ok && take_unit<false>(&x, it_u, msgs, bar(G::BAR_MF), bar(G::BAR_ME), g, 17); ++it_u) {
-        const int qbuf = it_u % G::QBUF;
-        if (!mbar_wait(bar(G::BAR_QF + qbuf), (it_u / G::QBUF) & 1, g, 4)) break;
-        const uint64_t qdesc = dq + ((qbuf * G::Q_BUF_BYTES) >> 4);
+#pragma unroll 1
+    for (int n = 0; ok && take_unit<true>(&x, n, msgs, bar(G::BAR_MF), bar(G::BAR_ME), g, 17); ++n) {
         const int nkv = x.nstep;
+        ok = await(bar(G::BAR_QF + qbuf), q_phase, g, 4);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const uint32_t qe = bar(G::BAR_QE + qbuf);
+        const uint64_t qdesc = dq + ((qbuf * G::Q_BUF_BYTES) >> 4);
+        if (++qbuf == G::QBUF) {
+            qbuf = 0;
+            q_phase ^= 1u;
+        }
         const int last_keys = min(G::BN, x.sk - (x.step0 + nkv - 1) * G::BN);  // of the last step
         if constexpr (ONE) {
             // S of step j goes to the S columns of tile (j & 1), so S_{j+1}
             // is made while the softmax works on S_j; S_{j+2} goes out right
-            // after P_j V_j, which has read the columns it overwrites.
+            // after P_j V_j, which has read the columns it overwrites. So K is
+            // taken two steps ahead of V: K_0 K_1 V_0 K_2 V_1 ...
             const uint32_t tO = tmem + G::TMEM_O_OFF;
+            Ring<G::SLOTS> kr = ring;
             auto next_s = [&](int j) {
-                const int nk = 2 * (kv_base + j), ks = nk % G::SLOTS;
-                if (!mbar_wait(bar(G::BAR_KVF + ks), (nk / G::SLOTS) & 1, g, 5)) return false;
+                ok = await(bar(G::BAR_KVF + kr.slot), kr.phase, g, 5);
+                if (!__all_sync(0xffffffffu, ok)) return;
                 tc_fence_after();
-                issue_s(tmem + (j & 1) * G::TMEM_TILE_STRIDE, qdesc, dk + ((ks * G::TILE_BYTES) >> 4));
-                mma_commit(bar(G::BAR_SF + (j & 1)));
-                mma_commit(bar(G::BAR_KVE + ks));
-                if (j == nkv - 1) mma_commit(bar(G::BAR_QE + qbuf));
-                return true;
+                if (lane == 0) {
+                    issue_s(tmem + (j & 1) * G::TMEM_TILE_STRIDE, qdesc, dk + kr.slot * tile16);
+                    mma_commit(bar(G::BAR_SF + (j & 1)));
+                    mma_commit(bar(G::BAR_KVE + kr.slot));
+                    if (j == nkv - 1) mma_commit(qe);
+                }
+                kr.next();
+                kr.next();
             };
-            if (nkv > 0) ok = next_s(0);
-            if (ok && nkv > 1) ok = next_s(1);
-            for (int j = 0; ok && j < nkv; ++j) {
-                const int nv = 2 * (kv_base + j) + 1, vs = nv % G::SLOTS;
-                if (!mbar_wait(bar(G::BAR_KVF + vs), (nv / G::SLOTS) & 1, g, 6)) {
-                    ok = false;
-                    break;
-                }
-                if (j == nkv - 1 && v_tail(x)) {
-                    mbar_arrive(bar(G::BAR_VLAND));
-                    if (!mbar_wait(bar(G::BAR_VFIX), fix_cnt & 1, g, 11)) {
-                        ok = false;
-                        break;
+#pragma unroll 1
+            for (int j = -2; ok && j < nkv; ++j) {
+                if (j >= 0) {
+                    ring.next();  // past K_j
+                    ok = await(bar(G::BAR_KVF + ring.slot), ring.phase, g, 6);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    const int keys = j == nkv - 1 ? last_keys : G::BN;
+                    if (keys & 15) zero_tail(ring.slot, keys);
+                    // the first P V overwrites O: the last unit's must have been read out
+                    if (j == 0) ok = await(bar(G::BAR_OE), o_phase ^ 1u, g, 7);
+                    ok = ok && await(bar(G::BAR_PF + (j & 1)), p_phase >> (j & 1) & 1u, g, 8);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    p_phase ^= 1u << (j & 1);
+                    tc_fence_after();
+                    if (lane == 0) {
+                        issue_pv(tO, tmem + (j & 1) * G::TMEM_TILE_STRIDE, dv + ring.slot * tile16, keys, j == 0);
+                        mma_commit(bar(G::BAR_KVE + ring.slot));
+                        mma_commit(bar(G::BAR_PVD));
+                        if (j == nkv - 1) mma_commit(bar(G::BAR_OF));
                     }
-                    ++fix_cnt;
+                    ring.next();
                 }
-                // the first P V overwrites O: the last unit's must have been read out
-                if (j == 0 && !mbar_wait(bar(G::BAR_OE), (o_cnt[0] & 1) ^ 1, g, 7)) {
-                    ok = false;
-                    break;
-                }
-                if (!mbar_wait(bar(G::BAR_PF + (j & 1)), p_cnt[j & 1] & 1, g, 8)) {
-                    ok = false;
-                    break;
-                }
-                ++p_cnt[j & 1];
-                tc_fence_after();
-                issue_pv(tO, tmem + (j & 1) * G::TMEM_TILE_STRIDE, dv + ((vs * G::TILE_BYTES) >> 4),
-                         j == nkv - 1 ? last_keys : G::BN, j == 0);
-                mma_commit(bar(G::BAR_KVE + vs));
-                mma_commit(bar(G::BAR_PVD));
-                if (j == nkv - 1) mma_commit(bar(G::BAR_OF));
-                if (j + 2 < nkv) ok = next_s(j + 2);
+                if (j + 2 < nkv) next_s(j + 2);
             }
             if (!ok) break;
             if (nkv == 0) {
                 // no key to see: O counts as made, once the last unit's has
                 // been read out (its barrier must not run two phases ahead)
-                if (!mbar_wait(bar(G::BAR_OE), (o_cnt[0] & 1) ^ 1, g, 7)) break;
-                mma_commit(bar(G::BAR_QE + qbuf));
-                mma_commit(bar(G::BAR_OF));
-            }
-            ++o_cnt[0];
-        } else {
-            const int n_qt = live_tiles<G::QT>(x, a);
-            // every wait or commit sits right after a group of MMAs, while
-            // those are queued, never in a clump between two groups
-            for (int j = 0; ok && j <= nkv; ++j) {
-                const int nk = 2 * (kv_base + j), nv = nk - 1;  // ring items K_j, V_{j-1}
-                const int ks = nk % G::SLOTS, vs = nv % G::SLOTS;
-                if (j == nkv && v_tail(x)) {
-                    if (!mbar_wait(bar(G::BAR_VFIX), fix_cnt & 1, g, 11)) {
-                        ok = false;
-                        break;
-                    }
-                    ++fix_cnt;
+                ok = await(bar(G::BAR_OE), o_phase ^ 1u, g, 7);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                if (lane == 0) {
+                    mma_commit(qe);
+                    mma_commit(bar(G::BAR_OF));
                 }
-                for (int t = 0; t < n_qt; ++t) {
-                    const uint32_t tS = tmem + t * G::TMEM_TILE_STRIDE;
-                    if (j > 0) {
-                        if (j == 1 && !mbar_wait(bar(G::BAR_OE + t), (o_cnt[t] & 1) ^ 1, g, 7)) {
-                            ok = false;
-                            break;
-                        }
-                        if (!mbar_wait(bar(G::BAR_PF + t), p_cnt[t] & 1, g, 8)) {
-                            ok = false;
-                            break;
-                        }
-                        ++p_cnt[t];
-                        tc_fence_after();
-                        issue_pv(tS + G::TMEM_O_OFF, tS, dv + ((vs * G::TILE_BYTES) >> 4),
-                                 j == nkv ? last_keys : G::BN, j == 1);
-                        if (t == n_qt - 1) mma_commit(bar(G::BAR_KVE + vs));
+            }
+        } else {
+            // The issuers take turns, P V and the next S of one tile together:
+            // otherwise the tiles fall into step, their products side by side
+            // and then both in the softmax with the tensor pipe idle (b1 s8192
+            // h32 d128: 965 us).
+            const bool live = t < live_tiles<G::QT>(x, a);
+            const uint32_t tS = tmem + t * G::TMEM_TILE_STRIDE;
+#pragma unroll 1
+            for (int j = 0; ok && j <= nkv; ++j) {
+                const int keys = j == nkv ? last_keys : G::BN;  // of step j - 1
+                const Ring<G::SLOTS> vr = ring;
+                if (j > 0) ring.next();
+                const Ring<G::SLOTS> kr = ring;
+                if (j < nkv) ring.next();
+                // everything the turn needs: V_{j-1} (its tail zeroed), K_j, P_{j-1}
+                if (j > 0) {
+                    ok = await(bar(G::BAR_KVF + vr.slot), vr.phase, g, 6);
+                    if (live && (keys & 15)) {
+                        if (!__all_sync(0xffffffffu, ok)) break;
+                        zero_tail(vr.slot, keys);
                     }
-                    if (j < nkv) {
-                        if (t == 0 && !mbar_wait(bar(G::BAR_KVF + ks), (nk / G::SLOTS) & 1, g, 5)) {
-                            ok = false;
-                            break;
+                }
+                if (j < nkv) ok = ok && await(bar(G::BAR_KVF + kr.slot), kr.phase, g, 5);
+                if (live) {
+                    // the first P V overwrites O: the last unit's must have been
+                    // read out (also where there is no key to see: O's barrier
+                    // must not run two phases ahead)
+                    if (j == (nkv > 0 ? 1 : 0)) ok = ok && await(bar(G::BAR_OE + t), o_phase ^ 1u, g, 7);
+                    if (j > 0) {
+                        ok = ok && await(bar(G::BAR_PF + t), p_phase, g, 8);
+                        p_phase ^= 1u;
+                    }
+                }
+                ok = ok && await(bar(G::BAR_TURN + t), turn, g, 22);
+                turn ^= 1u;
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    if (live) {
+                        if (j > 0) {  // O += P_{j-1} V_{j-1}
+                            issue_pv(tS + G::TMEM_O_OFF, tS, dv + vr.slot * tile16, keys, j == 1);
+                            mma_commit(bar(G::BAR_KVE + vr.slot));
                         }
-                        tc_fence_after();
-                        issue_s(tS, qdesc + ((t * G::TILE_BYTES) >> 4), dk + ((ks * G::TILE_BYTES) >> 4));
-                        mma_commit(bar(G::BAR_SF + t));
-                        if (t == n_qt - 1) {
-                            mma_commit(bar(G::BAR_KVE + ks));
-                            if (j == nkv - 1) mma_commit(bar(G::BAR_QE + qbuf));
+                        if (j < nkv) {
+                            issue_s(tS, qdesc, dk + kr.slot * tile16);
+                            mma_commit(bar(G::BAR_SF + t));
+                            mma_commit(bar(G::BAR_KVE + kr.slot));
+                            if (j == nkv - 1) mma_commit(qe);
+                        } else {
+                            mma_commit(bar(G::BAR_OF + t));
+                            mbar_arrive(bar(G::BAR_TURN + (t ^ 1)));
+                            if (nkv == 0) mma_commit(qe);
                         }
                     } else {
-                        // (no key to see: as above)
-                        if (nkv == 0 && !mbar_wait(bar(G::BAR_OE + t), (o_cnt[t] & 1) ^ 1, g, 7)) {
-                            ok = false;
-                            break;
-                        }
-                        mma_commit(bar(G::BAR_OF + t));
+                        // not this tile's unit: pass, and release the slots (they
+                        // are full, so that a release cannot run ahead)
+                        mbar_arrive(bar(G::BAR_TURN + (t ^ 1)));
+                        if (j > 0) mbar_arrive(bar(G::BAR_KVE + vr.slot));
+                        if (j < nkv) mbar_arrive(bar(G::BAR_KVE + kr.slot));
+                        if (j == (nkv > 0 ? nkv - 1 : 0)) mbar_arrive(qe);
                     }
                 }
-                if (!ok) break;
-                if (j < nkv &&
-                    !mbar_wait(bar(G::BAR_KVF + (nk + 1) % G::SLOTS), ((nk + 1) / G::SLOTS) & 1, g, 6)) {
-                    ok = false;
-                    break;
-                }
-                if (j == nkv - 1 && v_tail(x)) mbar_arrive(bar(G::BAR_VLAND));
             }
-            if (nkv == 0) mma_commit(bar(G::BAR_QE + qbuf));
-            for (int t = 0; t < n_qt; ++t) ++o_cnt[t];
+            if (!live) continue;
         }
-        kv_base += nkv;
+        o_phase ^= 1u;
     }
     // No MMA may still be running when TMEM is released.
-    mma_commit(bar(G::BAR_DONE));
+    if (lane == 0) mma_commit(bar(G::BAR_DONE + t));
     WaitGuard drain = g;
     uint32_t no_abort = 0;
     drain.abort = &no_abort;
-    mbar_wait(bar(G::BAR_DONE), 0, drain, 12);
+    await(bar(G::BAR_DONE + t), 0, drain, 12);
 }
 
 // Joins a cut unit's partial results of one query tile: with M the largest
 // LSE_i, l = sum_i 2^(LSE_i - M), O = sum_i 2^(LSE_i - M) O_i / l, LSE = M +
 // log2 l. Run by the tile's 128 threads; a row's columns lie over D / 4 lanes
-// (16-byte loads), a warp takes 4 row slots at a time so that several loads
-// are in flight per thread. Ranges are taken in order with a running maximum.
-template <int D, bool BF16>
-__device__ __forceinline__ void pack_join(int first_part, int nparts, int t, int tiles, int64_t tok0, int head0,
+// (16-byte loads). Bound by the latency of loads from L2, so a warp takes R
+// rows times P ranges of them at once. Ranges are taken in order with a
+// running maximum.
+template <int D, bool BF16, int R, int P>
+__device__ __forceinline__ void join_rows(int first_part, int nparts, int t, int tiles, int64_t tok0, int head0,
                                           int rows, const PackArgs &a) {
-    constexpr int LPR = D / 4, RPW = 32 / LPR, R = 4;
+    constexpr int LPR = D / 4, RPW = 32 / LPR;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
     const int sub = lane % LPR;
+#pragma unroll 1
     for (int r0 = 0; r0 < rows; r0 += 4 * RPW * R) {
         float m[R], l[R];
         float4 acc[R];
@@ -440,38 +477,44 @@ __device__ __forceinline__ void pack_join(int first_part, int nparts, int t, int
             l[i] = 0.f;
             acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-#pragma unroll 2
-        for (int p = 0; p < nparts; ++p) {
-            const int64_t part = (static_cast<int64_t>(2 * (first_part + p) + (p == 0 ? 1 : 0)) * tiles + t) * 128;
-            float lp[R];
-            float4 op[R];
+#pragma unroll 1
+        for (int p0 = 0; p0 < nparts; p0 += P) {
+            float lp[P][R];
+            float4 op[P][R];
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                lp[i] = -INFINITY;
-                op[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (row[i] < rows) {
-                    lp[i] = __ldcg(a.lse_part + part + row[i]);
-                    op[i] = __ldcg(reinterpret_cast<const float4 *>(a.o_part + (part + row[i]) * D) + sub);
+            for (int p = 0; p < P; ++p) {
+                const int part = ((2 * (first_part + p0 + p) + (p0 + p == 0 ? 1 : 0)) * tiles + t) * 128;
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    lp[p][i] = -INFINITY;
+                    op[p][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (p0 + p < nparts && row[i] < rows) {
+                        lp[p][i] = __ldcg(a.lse_part + part + row[i]);
+                        op[p][i] = __ldcg(reinterpret_cast<const float4 *>(a.o_part) + (part + row[i]) * LPR + sub);
+                    }
                 }
             }
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const float mn = fmaxf(m[i], lp[i]);
-                const float f = m[i] == -INFINITY ? 0.f : fast_exp2(m[i] - mn);
-                const float e = lp[i] == -INFINITY ? 0.f : fast_exp2(lp[i] - mn);
-                m[i] = mn;
-                l[i] = l[i] * f + e;
-                acc[i].x = acc[i].x * f + op[i].x * e;
-                acc[i].y = acc[i].y * f + op[i].y * e;
-                acc[i].z = acc[i].z * f + op[i].z * e;
-                acc[i].w = acc[i].w * f + op[i].w * e;
-            }
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const float mn = fmaxf(m[i], lp[p][i]);
+                    const float f = m[i] == -INFINITY ? 0.f : fast_exp2(m[i] - mn);
+                    const float e = lp[p][i] == -INFINITY ? 0.f : fast_exp2(lp[p][i] - mn);
+                    m[i] = mn;
+                    l[i] = l[i] * f + e;
+                    acc[i].x = acc[i].x * f + op[p][i].x * e;
+                    acc[i].y = acc[i].y * f + op[p][i].y * e;
+                    acc[i].z = acc[i].z * f + op[p][i].z * e;
+                    acc[i].w = acc[i].w * f + op[p][i].w * e;
+                }
         }
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             if (row[i] >= rows) continue;
-            const int64_t tok = tok0 + row[i] / a.group;
-            const int head = head0 + row[i] % a.group;
+            const int rt = (row[i] * a.group_inv) >> 16;
+            const int64_t tok = tok0 + rt;
+            const int head = head0 + row[i] - rt * a.group;
             const float inv = l[i] == 0.f ? 0.f : 1.0f / l[i];
             *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + (tok * a.h + head) * D + 4 * sub) =
                 make_uint2(pack2p<BF16>(acc[i].x * inv, acc[i].y * inv),
@@ -483,6 +526,17 @@ __device__ __forceinline__ void pack_join(int first_part, int nparts, int t, int
     }
 }
 
+template <int D, bool BF16>
+__device__ __forceinline__ void pack_join(int first_part, int nparts, int t, int tiles, int64_t tok0, int head0,
+                                          int rows, const PackArgs &a) {
+    // few rows: the ranges side by side (b1 sk32768, 20 ranges: one at a time
+    // took 20 us); many: the rows
+    if (rows <= 16)
+        join_rows<D, BF16, 1, 8>(first_part, nparts, t, tiles, tok0, head0, rows, a);
+    else
+        join_rows<D, BF16, 4, 2>(first_part, nparts, t, tiles, tok0, head0, rows, a);
+}
+
 template <int D, bool BF16, bool ONE>
 __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint32_t tmem, const UnitMsg *msgs,
                                              int t, int q4, const PackArgs &a, const WaitGuard &g) {
@@ -490,7 +544,7 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
     auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
     const uint32_t lane = threadIdx.x & 31;
     const int row = q4 * 32 + lane;
-    const int row_tok = row / a.group, row_head = row - row_tok * a.group;
+    const int row_tok = (row * a.group_inv) >> 16, row_head = row - row_tok * a.group;
     const bool row_used = row_tok < a.tile_tokens;
     const uint32_t tS0 = tmem + t * G::TMEM_TILE_STRIDE + (static_cast<uint32_t>(q4 * 32) << 16);
     const uint32_t tO = tS0 + G::TMEM_O_OFF;
@@ -522,7 +576,7 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
         for (int j = 0; j < nstep; ++j) {
             const bool alt = ONE && (j & 1);  // ONE: odd steps use the second tile's S columns
             const uint32_t tS = alt ? tS0 + G::TMEM_TILE_STRIDE : tS0;
-            const bool ok = mbar_wait(bar(alt ? G::BAR_SF + 1 : G::BAR_SF + t), (alt ? s2_cnt : s_cnt) & 1, g, 13);
+            const bool ok = await(bar(alt ? G::BAR_SF + 1 : G::BAR_SF + t), (alt ? s2_cnt : s_cnt) & 1, g, 13);
             if (alt)
                 ++s2_cnt;
             else
@@ -536,12 +590,30 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
                 const int valid = sees - j * G::BN;
                 const int vmax = __reduce_max_sync(0xffffffffu, valid);
                 const bool ragged = __any_sync(0xffffffffu, valid < G::BN);
-                uint32_t sr[G::BN];
-                const float *s = reinterpret_cast<const float *>(sr);
-                float mx[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) mx[i] = -INFINITY;
+                // the row's max over the tile; `step(mraw)` moves the reference max
+                // when a tile exceeds it by more than 8 (log2): P stays at most
+                // 2^8, exact in 16 bits as below 1. A row that has seen no key
+                // yet keeps m = -inf and alpha 1.
+                bool need = false;
+                float alpha = 1.0f;
+                auto step = [&](float mraw) {
+                    // (a scale of 0 makes every score 0: 0 * -inf must not be NaN)
+                    const float m_tile = mraw == -INFINITY ? -INFINITY : mraw * c;
+                    need = m_tile > m_ref + 8.0f;
+                    const float m_new = need ? m_tile : m_ref;
+                    if (m_new != -INFINITY) alpha = fast_exp2(m_ref - m_new);
+                    m_ref = m_new;
+                };
+                uint64_t acc2[2] = {0ull, 0ull};
+                // P = 2^(s*c - m_ref), rounded to 16 bits for the P V product
+                // (the row sum takes the unrounded values), packed in pairs
+                // into the S columns
                 if (!ragged) {
+                    uint32_t sr[G::BN];
+                    const float *s = reinterpret_cast<const float *>(sr);
+                    float mx[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mx[i] = -INFINITY;
                     // the max of the first 64 scores runs while the rest load
                     tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
                     tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
@@ -555,46 +627,12 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
                         for (int i = part * G::BN / 4; i < (part + 1) * G::BN / 4; ++i)
                             mx[i & 3] = max3f(mx[i & 3], s[2 * i], s[2 * i + 1]);
                     }
-                } else {
-                    // whole 32-key chunks that no row of the warp sees are skipped
+                    step(fmaxf(max3f(mx[0], mx[1], mx[2]), mx[3]));
+                    const float neg_m = -m_ref;
+                    const uint64_t c2 = f2_make(c, c), nm2 = f2_make(neg_m, neg_m);
 #pragma unroll
-                    for (int c0 = 0; c0 < G::BN; c0 += 32) {
-                        if (c0 < vmax) tmem_ld32(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(&sr[c0]));
-                    }
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int c0 = 0; c0 < G::BN; c0 += 32) {
-                        if (c0 < vmax) {
-#pragma unroll
-                            for (int i = c0; i < c0 + 32; ++i) {
-                                if (i < valid) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-                            }
-                        }
-                    }
-                }
-                const float mraw = fmaxf(max3f(mx[0], mx[1], mx[2]), mx[3]);
-                // (a scale of 0 makes every score 0: 0 * -inf must not be NaN)
-                const float m_tile = mraw == -INFINITY ? -INFINITY : mraw * c;
-
-                // the reference max moves only when a tile exceeds it by more
-                // than 8: P stays at most 2^8, exact in 16 bits as below 1
-                const bool need = m_tile > m_ref + 8.0f;
-                const float m_new = need ? m_tile : m_ref;
-                // a row that has seen no key yet keeps m = -inf and alpha 1
-                const float alpha = m_new == -INFINITY ? 1.0f : fast_exp2(m_ref - m_new);
-                m_ref = m_new;
-                const bool rescale = j > 0 && __any_sync(0xffffffffu, need);
-
-                // P = 2^(s*c - m_ref), rounded to 16 bits for the P V product
-                // (the row sum takes the unrounded values), 64 keys at a time;
-                // keys the row does not see get exactly 0
-                const float neg_m = -m_ref;
-                const uint64_t c2 = f2_make(c, c), nm2 = f2_make(neg_m, neg_m);
-                uint64_t acc2[2] = {0ull, 0ull};
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t pk[G::BN / 4];
-                    if (!ragged) {
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t pk[G::BN / 4];
 #pragma unroll
                         for (int i = 0; i < G::BN / 4; ++i) {
                             const int k0 = half * (G::BN / 2) + 2 * i;
@@ -605,43 +643,65 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
                             acc2[i & 1] = f2_add(acc2[i & 1], f2_make(p0, p1));
                             pk[i] = pack2p<BF16>(p0, p1);
                         }
-                    } else {
+                        tmem_st32(tS + half * (G::BN / 4), pk);
+                    }
+                } else {
+                    // A masked or ragged tile, 32 keys at a time: chunks that no
+                    // row of the warp sees are skipped, keys the row does not see
+                    // get exactly 0. Scores are read twice rather than kept, and
+                    // the chunks stay a loop: code four times smaller. (A chunk's
+                    // P goes to columns whose scores have been read.)
+                    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+                    for (int c0 = 0; c0 < vmax && c0 < G::BN; c0 += 32) {
+                        uint32_t sr[32];
+                        tmem_ld32(tS + c0, sr);
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int ch = 0; ch < 2; ++ch) {
-                            if (half * (G::BN / 2) + ch * 32 < vmax) {
+                        for (int i = 0; i < 32; ++i)
+                            if (c0 + i < valid) mx[i & 1] = fmaxf(mx[i & 1], __uint_as_float(sr[i]));
+                    }
+                    step(fmaxf(mx[0], mx[1]));
+                    const float neg_m = -m_ref;
+                    const uint64_t c2 = f2_make(c, c), nm2 = f2_make(neg_m, neg_m);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < G::BN; c0 += 32) {
+                        uint32_t pk[16];
 #pragma unroll
-                                for (int i = ch * 16; i < ch * 16 + 16; ++i) {
-                                    const int k0 = half * (G::BN / 2) + 2 * i;
-                                    float x0, x1;
-                                    f2_split(f2_fma(f2_make(s[k0], s[k0 + 1]), c2, nm2), x0, x1);
-                                    x0 = (k0 < valid) ? x0 : -INFINITY;
-                                    x1 = (k0 + 1 < valid) ? x1 : -INFINITY;
-                                    const float p0 = fast_exp2(x0);
-                                    const float p1 = fast_exp2(x1);
-                                    acc2[i & 1] = f2_add(acc2[i & 1], f2_make(p0, p1));
-                                    pk[i] = pack2p<BF16>(p0, p1);
-                                }
-                            } else {
+                        for (int i = 0; i < 16; ++i) pk[i] = 0u;
+                        if (c0 < vmax) {
+                            uint32_t sr[32];
+                            tmem_ld32(tS + c0, sr);
+                            tmem_wait_ld();
 #pragma unroll
-                                for (int i = ch * 16; i < ch * 16 + 16; ++i) pk[i] = 0u;
+                            for (int i = 0; i < 16; ++i) {
+                                float x0, x1;
+                                f2_split(f2_fma(f2_make(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])),
+                                                c2, nm2),
+                                         x0, x1);
+                                const float p0 = fast_exp2(c0 + 2 * i < valid ? x0 : -INFINITY);
+                                const float p1 = fast_exp2(c0 + 2 * i + 1 < valid ? x1 : -INFINITY);
+                                acc2[i & 1] = f2_add(acc2[i & 1], f2_make(p0, p1));
+                                pk[i] = pack2p<BF16>(p0, p1);
                             }
                         }
+                        tmem_st16(tS + c0 / 2, pk);
                     }
-                    tmem_st32(tS + half * (G::BN / 4), pk);
                 }
+                const bool rescale = j > 0 && __any_sync(0xffffffffu, need);
                 if (rescale) {
                     // O row *= alpha once P_{j-1} V_{j-1} is done: S_j's
                     // commit covers it where S_j was issued after it; ONE
                     // issues S_j earlier and waits for that product's own barrier
                     if (ONE) {
-                        const bool okv = mbar_wait(bar(G::BAR_PVD), (pv_done + j - 1) & 1, g, 15);
+                        const bool okv = await(bar(G::BAR_PVD), (pv_done + j - 1) & 1, g, 15);
                         if (!__all_sync(0xffffffffu, okv)) {
                             alive = false;
                             break;
                         }
                         tc_fence_after();
                     }
-#pragma unroll
+#pragma unroll 1
                     for (int c0 = 0; c0 < D; c0 += 16) {
                         uint32_t ov[16];
                         tmem_ld16(tO + c0, ov);
@@ -682,12 +742,12 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
         const int64_t prow =
             (static_cast<int64_t>(2 * static_cast<int>(blockIdx.x) + max(slot, 0)) * G::QT + t) * 128 + row;
         const bool o_al32 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
-        const bool ok = mbar_wait(bar(G::BAR_OF + t), o_cnt & 1, g, 14);
+        const bool ok = await(bar(G::BAR_OF + t), o_cnt & 1, g, 14);
         ++o_cnt;
         if (!__all_sync(0xffffffffu, ok)) return;
         tc_fence_after();
         if (warp_live) {
-#pragma unroll
+#pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += G::OCH) {
                 uint32_t ov[G::OCH];
                 if constexpr (G::OCH == 32)
@@ -707,10 +767,13 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
                 } else {
                     uint32_t pk[G::OCH / 2];
 #pragma unroll
-                    for (int i = 0; i < G::OCH / 2; ++i)
-                        pk[i] = empty_row ? 0u
-                                          : pack2p<BF16>(__uint_as_float(ov[2 * i]) * inv_l,
-                                                         __uint_as_float(ov[2 * i + 1]) * inv_l);
+                    for (int i = 0; i < G::OCH / 2; ++i) {
+                        float lo, hi;
+                        f2_split(f2_mul(f2_make(__uint_as_float(ov[2 * i]), __uint_as_float(ov[2 * i + 1])),
+                                        f2_make(inv_l, inv_l)),
+                                 lo, hi);
+                        pk[i] = empty_row ? 0u : pack2p<BF16>(lo, hi);
+                    }
                     if (o_al32) {
 #pragma unroll
                         for (int i = 0; i < G::OCH / 16; ++i)
@@ -734,6 +797,10 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
             continue;
         }
         // A cut unit: count this range's arrival; the last one joins them all.
+        {
+            const bool ok = await(bar(G::BAR_MS + n % kMsgSlots), (n / kMsgSlots) & 1, g, 23);
+            if (!__all_sync(0xffffffffu, ok)) return;
+        }
         if (row_out) a.lse_part[prow] = lse2;
         __threadfence();
         if (!meet(bar(G::BAR_WG + t), met, g)) return;
@@ -777,7 +844,9 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             if ((i >= G::BAR_PF && i < G::BAR_PF + 2) || (i >= G::BAR_OE && i < G::BAR_OE + 2))
                 count = 4;  // the tile's softmax warps
             if (i >= G::BAR_WG) count = 4;
-            if (i >= G::BAR_ME && i < G::BAR_WG) count = 3 + 4 * G::QT;  // producer, issuer, zeroing, softmax warps
+            if (i >= G::BAR_ME && i < G::BAR_MS) count = 1 + 5 * G::QT + (PAGED && ONE ? 1 : 0);  // producers, issuers, softmax warps
+            // released by each tile's issuer
+            if ((i >= G::BAR_QE && i < G::BAR_KVF) || (i >= G::BAR_KVE && i < G::BAR_SF)) count = G::QT;
             mbar_init(bar(i), count);
         }
         *abort_flag = 0u;
@@ -790,7 +859,7 @@ __global__ void __launch_bounds__(kPackThreads, 1)
         tmem_alloc(smem_u32(tmem_slot), G::TMEM_COLS);
         tmem_relinquish();
     }
-    line_sum_warps(a.seqs, a.line, sums);
+    line_sum_warps<0>(a.seqs, a.line, sums);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -801,14 +870,17 @@ __global__ void __launch_bounds__(kPackThreads, 1)
         reg_dealloc<kPackRegsControl>();
         if (warp == 0) {
             if ((PAGED || lane == 0) && !(a.flags & kFlagSkipLoads))
-                pack_producer<D, PAGED, ONE>(&tq, &tk, &tv, sbase, msgs, a, g);
-        } else if (warp == 1) {
-            if (lane == 0) pack_mma<D, BF16, ONE>(sbase, tmem, msgs, a, g);
-        } else if (warp == 2) {
-            pack_fix_v<D, ONE>(sbase, msgs, g);
+                pack_producer<D, PAGED, ONE, PAGED && ONE ? 0 : 2>(&tq, &tk, &tv, sbase, msgs, a, g);
+        } else if (warp < 3) {
+            if (warp <= G::QT) {
+                pack_issue<D, BF16, ONE>(sbase, tmem, msgs, warp - 1, a, g);
+            } else if constexpr (PAGED && ONE) {
+                if (!(a.flags & kFlagSkipLoads)) pack_producer<D, PAGED, ONE, 1>(&tq, &tk, &tv, sbase, msgs, a, g);
+            }
         } else {
-            post_units(a.seqs, a.line, line_total(sums, kPackThreads / 32), msgs, bar(G::BAR_MF), bar(G::BAR_ME),
-                       g, 18, blockIdx.x, gridDim.x);
+            post_units<0>(
+                a.seqs, a.line, [&] { return line_total(sums, kPackThreads / 32); }, msgs, bar(G::BAR_MF),
+                bar(G::BAR_ME), bar(G::BAR_MS), g, 18, blockIdx.x, gridDim.x);
         }
     } else {
         reg_alloc<kPackRegsSoftmax>();

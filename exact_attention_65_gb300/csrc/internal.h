@@ -213,6 +213,7 @@ struct PackArgs {
     void *o;
     float *lse;  // [h, total_q]
     int h, group;     // query heads, query heads per K/V head
+    int group_inv;    // row / group = row * group_inv >> 16 for rows below 128
     int tile_tokens;  // tokens of a 128-row query tile: floor(128 / group)
     int total_q;
     int causal;
@@ -233,8 +234,16 @@ struct PackArgs {
 };
 // Query tokens of a 128-row tile, and where work is cut.
 inline int pack_tile_tokens(int group) { return 128 / group; }
-LineShape pack_line(int heads, int tile_tokens, bool one_tile, bool causal);
-LineShape bwd_key_line(int heads, int tile_tokens, bool causal);
+// ceil(2^16 / group): exact for rows below 128, as 128 * group_inv errs by
+// less than 128 / 2^16 < 1 / group.
+inline int pack_group_inv(int group) { return (65536 + group - 1) / group; }
+// The most the work line of a call can hold, from what the host knows.
+struct LineBound {
+    int b, total_q;
+    int64_t total_k, max_k;  // keys of all sequences, and of one, at most
+};
+LineShape pack_line(int heads, int group, bool one_tile, bool causal, const LineBound &bound);
+LineShape bwd_key_line(int heads, int group, bool causal, const LineBound &bound);
 cudaError_t launch_fwd_packed(int d, bool bf16, const CUtensorMap &tq, const CUtensorMap &tk,
                               const CUtensorMap &tv, const PackArgs &a, cudaStream_t stream);
 cudaError_t launch_chunk_paged(int d, bool bf16, const CUtensorMap &tq, const CUtensorMap &tk,
@@ -250,7 +259,7 @@ struct PackBwdArgs {
     float2 *ld;            // workspace [h_kv, total_q, group]: (LSE log2 e, D)
     void *dq, *dk, *dv;
     int64_t dq_stride, dk_stride, dv_stride;  // elements from one token's row to the next
-    int h, group, tile_tokens, total_q, causal;
+    int h, group, group_inv, tile_tokens, total_q, causal;
     float scale, scale_log2;
     uint32_t *status;
     uint32_t flags;
@@ -261,7 +270,7 @@ struct PackBwdArgs {
     uint32_t *arrivals;
     uint32_t call;
 };
-LineShape bwd_query_line(int heads, int tile_tokens, bool causal);
+LineShape bwd_query_line(int heads, int group, bool causal, const LineBound &bound);
 cudaError_t launch_bwd_packed(int d, bool bf16, const CUtensorMap &tq, const CUtensorMap &tk,
                               const CUtensorMap &tv, const CUtensorMap &tdo, const PackBwdArgs &a,
                               cudaStream_t stream);

@@ -4,14 +4,19 @@
 // The work of a call is a line: sequences one behind the other, within a
 // sequence its K/V heads, within a head its units (row tiles of the forward
 // and dQ kernels, key tiles of the dK/dV kernel), within a unit its steps
-// (the streamed tiles). A unit of n steps takes a fixed cost plus the keys
-// (or query tokens) it streams; under the causal mask that is linear in the
-// unit's index, so that the line's length and any place on it have closed
-// forms, and no list of tiles is made or sorted. CTA c of G takes the part
-// [W c / G, W (c + 1) / G) of a line of length W, cut at step boundaries: a
-// long sequence is spread over many CTAs and short ones share a CTA, whatever
-// the mix of lengths. The CTAs that share a unit join their partial results
-// (no CTA waits for another: the last one to finish joins them).
+// (the streamed tiles). A unit costs a fixed amount plus what it streams;
+// under the causal mask that is linear in the unit's index, so that the
+// line's length and any place on it have closed forms, and no list of tiles
+// is made or sorted. CTA c of G takes the part [W c / G, W (c + 1) / G) of a
+// line of length W, cut at step boundaries: a long sequence is spread over
+// many CTAs and short ones share a CTA, whatever the mix of lengths. The CTAs
+// that share a unit join their partial results (no CTA waits for another: the
+// last one to finish joins them).
+//
+// All of this runs on every CTA before its first load, from a cold
+// instruction cache, so it is kept small: 32-bit sums, few divisions, loops
+// that stay loops. (With 64-bit divisions inlined it was 85 KB of code and
+// took 7 us of a 14 us call; the softmax loop, too, was slowed down by it.)
 #pragma once
 
 #include <cstdint>
@@ -24,128 +29,149 @@
 
 namespace exattn {
 
-EXATTN_HD int64_t smax64(int64_t a, int64_t b) { return a > b ? a : b; }
-EXATTN_HD int64_t smin64(int64_t a, int64_t b) { return a < b ? a : b; }
 EXATTN_HD int smax(int a, int b) { return a > b ? a : b; }
 EXATTN_HD int smin(int a, int b) { return a < b ? a : b; }
 
-// What the line is made of; the same for every CTA of a launch.
+// What the line is made of; the same for every CTA of a launch. Costs are in
+// steps of 128 rows (of keys, or of query heads times tokens), or 2^k of them
+// where a call is so large that its sum would not fit 31 bits.
 struct LineShape {
-    int heads;       // K/V heads
-    int unit_len;    // tokens (or keys) of one unit
-    int step_len;    // keys (or tokens) of one step
+    int heads;      // K/V heads
+    int unit_len;   // tokens (or keys) of one unit
+    int step_len;   // keys (or tokens) of one step
     int causal;
-    int by_key;      // 0: units over query tokens, steps over keys; 1: the other way round
-    int unit_cost;   // a unit's fixed cost, in keys (or tokens) streamed
-    int min_steps;   // a unit is not cut this close to its ends
-    int64_t min_part;  // the least a CTA takes of the line before units are cut
+    int by_key;     // 0: units over query tokens, steps over keys; 1: the other way round
+    int weight;     // 128-row steps count weight / 2^shift of the keys (tokens) streamed;
+    int shift;      //   weight 0: every unit counts the same
+    int unit_cost;  // a unit's fixed cost
+    int min_steps;  // a unit is not cut this close to its ends
+    int min_part;   // the least a CTA takes of the line before units are cut
+    uint32_t unit_mul, step_mul;  // x / len = x * mul >> shift for x < 2^31
+    int unit_div, step_div;       //   (the shifts)
 };
+
+// mul and shift of a division by len (1 .. 256): with 2^k >= len, mul =
+// ceil(2^(31 + k) / len) fits 32 bits, and x * mul >> (31 + k) is exact for x <
+// 2^31, as mul errs by less than 1 and x / 2^(31 + k) < 1 / len.
+inline void fast_division(int len, uint32_t *mul, int *shift) {
+    int k = 0;
+    while ((1 << k) < len) ++k;
+    *shift = 31 + k;
+    *mul = static_cast<uint32_t>(((1ull << *shift) + len - 1) / len);
+}
+EXATTN_HD int divided(uint32_t x, uint32_t mul, int shift) {
+    return static_cast<int>((static_cast<uint64_t>(x) * mul) >> shift);
+}
 
 // Units of one head of a sequence of sq query rows and sk keys.
 EXATTN_HD int line_units(const LineShape &s, int sq, int sk) {
-    const int n = s.by_key ? sk : sq;
-    return n <= 0 ? 0 : (n - 1) / s.unit_len + 1;
+    return divided((s.by_key ? sk : sq) + s.unit_len - 1, s.unit_mul, s.unit_div);
 }
 
 // The steps [first, first + count) of unit u. With the causal mask query
 // token i sees key j only if j <= i + sk - sq.
 EXATTN_HD void line_steps(const LineShape &s, int sq, int sk, int u, int *first, int *count) {
-    *first = 0;
-    if (!s.by_key) {
-        const int all = sk <= 0 ? 0 : (sk - 1) / s.step_len + 1;
-        *count = all;
-        if (s.causal) {
-            const int64_t last = smin64(static_cast<int64_t>(u + 1) * s.unit_len, sq) - 1;
-            const int64_t kmax = last + sk - sq;
-            *count = kmax < 0 ? 0 : static_cast<int>(smin64(all, kmax / s.step_len + 1));
-        }
-    } else {
-        const int all = sq <= 0 ? 0 : (sq - 1) / s.step_len + 1;
-        *count = all;
-        if (s.causal) {
-            const int64_t q0 = static_cast<int64_t>(u) * s.unit_len - (static_cast<int64_t>(sk) - sq);
-            *first = q0 <= 0 ? 0 : static_cast<int>(smin64(q0 / s.step_len, all));
-            *count = all - *first;
-        }
+    const int len = s.by_key ? sq : sk;  // what is streamed
+    int lo = 0, hi = len;                // the part of it that the unit sees
+    if (s.causal) {
+        if (s.by_key)
+            lo = smin(smax(u * s.unit_len - (sk - sq), 0), len);
+        else
+            hi = smax(smin((u + 1) * s.unit_len, sq) + sk - sq, 0);
     }
+    const int a = divided(lo, s.step_mul, s.step_div);
+    const int z = divided(hi + s.step_len - 1, s.step_mul, s.step_div);
+    // (a unit over keys that no row sees starts at the end of the rows)
+    *first = a;
+    *count = lo < hi ? z - a : 0;
 }
 
 // Cost of the units before unit n of one head (n up to line_units()).
-EXATTN_HD int64_t line_before(const LineShape &s, int sq, int sk, int n) {
-    const int64_t off = static_cast<int64_t>(sk) - sq, len = s.unit_len;
-    int64_t sum = static_cast<int64_t>(n) * s.unit_cost;
-    if (!s.causal) return sum + static_cast<int64_t>(n) * (s.by_key ? sq : sk);
-    if (!s.by_key) {
+EXATTN_HD int line_before(const LineShape &s, int sq, int sk, int n) {
+    const int off = sk - sq;
+    int64_t sum;  // keys (tokens) streamed
+    if (!s.causal) {
+        sum = static_cast<int64_t>(n) * (s.by_key ? sq : sk);
+    } else if (!s.by_key) {
         // unit u streams max(0, off + (u + 1) len) keys
-        const int64_t u0 = off >= 0 ? 0 : smin64(-off / len, n);
-        sum += (n - u0) * off + len * ((static_cast<int64_t>(n) * (n + 1) - u0 * (u0 + 1)) / 2);
+        const int u0 = off < 0 ? smin(divided(-off, s.unit_mul, s.unit_div), n) : 0;
+        const int64_t pairs = static_cast<int64_t>(n - u0) * (n + u0 + 1);  // / 2
+        sum = static_cast<int64_t>(n - u0) * off + ((pairs * s.unit_len) >> 1);
     } else {
-        // unit u streams sq tokens while u len <= off, then sk - u len
-        const int64_t u0 = off < 0 ? 0 : smin64(off / len + 1, n);
-        sum += u0 * sq + (n - u0) * sk - len * ((static_cast<int64_t>(n) * (n - 1) - u0 * (u0 - 1)) / 2);
+        // unit u streams sq tokens while 128 u <= off, then sk - 128 u
+        const int u0 = off < 0 ? 0 : smin((off >> 7) + 1, n);
+        const int64_t pairs = static_cast<int64_t>(n - u0) * (n + u0 - 1);
+        sum = static_cast<int64_t>(u0) * sq + static_cast<int64_t>(n - u0) * sk - 64 * pairs;
     }
-    return sum;
+    return n * s.unit_cost + static_cast<int>((sum * s.weight) >> s.shift);
 }
 
-// The longest unit of a head: the last one over query tokens, the first one
-// over keys.
-EXATTN_HD int64_t line_longest(const LineShape &s, int sq, int sk) {
-    const int n = line_units(s, sq, sk);
-    if (n == 0) return 0;
-    const int u = s.by_key ? 0 : n - 1;
-    return line_before(s, sq, sk, u + 1) - line_before(s, sq, sk, u);
-}
-
-// Sums over the sequences, and what follows from them.
+// Sums over the sequences.
 struct LineSum {
-    int64_t cost;     // with the heads
-    int64_t units;    // with the heads
-    int64_t longest;  // of one unit
+    int cost;     // with the heads
+    int units;    // with the heads
+    int longest;  // unit: the last one over query tokens, the first one over keys
 };
 
 EXATTN_HD void line_add(LineSum *t, const LineShape &s, int sq, int sk) {
     const int n = line_units(s, sq, sk);
-    t->cost += static_cast<int64_t>(s.heads) * line_before(s, sq, sk, n);
-    t->units += static_cast<int64_t>(s.heads) * n;
-    t->longest = smax64(t->longest, line_longest(s, sq, sk));
+    if (n == 0) return;
+    const int all = line_before(s, sq, sk, n);
+    t->cost += s.heads * all;
+    t->units += s.heads * n;
+    t->longest = smax(t->longest, s.by_key ? line_before(s, sq, sk, 1) : all - line_before(s, sq, sk, n - 1));
 }
 
-// How the line is dealt: `parts` CTAs take a share each. Where every unit is
-// short and there is a CTA for each, each takes one whole unit (`whole`:
-// every unit then counts 1).
+// How the line is dealt: `parts` CTAs take a share each; part c begins at
+// q c + r c / parts. Where every unit is short and there is a CTA for each,
+// each takes one whole unit: every unit then counts 1 (weight 0).
 struct LineDeal {
-    int64_t length;
-    int parts;
-    int whole;
+    int length, parts, q, r;
 };
 
-EXATTN_HD LineDeal line_deal(const LineShape &s, const LineSum &t, int ctas) {
+EXATTN_HD bool line_whole(const LineShape &s, const LineSum &t, int ctas) {
+    return t.units <= ctas && t.longest <= 2 * s.min_part;
+}
+
+EXATTN_HD LineDeal line_deal(LineShape *s, const LineSum &t, int ctas) {
     LineDeal d;
-    d.whole = t.units <= ctas && t.longest <= 2 * s.min_part;
-    d.length = d.whole ? t.units : t.cost;
-    d.parts = static_cast<int>(d.whole ? t.units : smin64(ctas, smax64(1, t.cost / s.min_part)));
+    d.length = t.cost;
+    d.parts = smin(ctas, smax(1, static_cast<int>(static_cast<uint32_t>(t.cost) / static_cast<uint32_t>(s->min_part))));
+    if (line_whole(*s, t, ctas)) {
+        s->weight = 0;
+        s->unit_cost = 1;
+        d.length = d.parts = t.units;
+    }
+    d.q = d.parts > 0 ? static_cast<int>(static_cast<uint32_t>(d.length) / static_cast<uint32_t>(d.parts)) : 0;
+    d.r = d.length - d.q * d.parts;
     return d;
 }
 
-EXATTN_HD int64_t deal_before(const LineShape &s, const LineDeal &d, int sq, int sk, int n) {
-    return d.whole ? n : line_before(s, sq, sk, n);
-}
-
-// Where part c begins on the line.
-EXATTN_HD int64_t part_begin(const LineDeal &d, int c) {
-    // length < 2^62 / parts: tokens times keys of one device's memory
-    return d.parts > 0 ? d.length * c / d.parts : 0;
+// (r c and parts are below 2^16 and 2^8: the quotient of floats, half a unit
+// up, has the integer quotient's floor)
+EXATTN_HD int part_begin(const LineDeal &d, int c) {
+#if defined(__CUDA_ARCH__)
+    return d.q * c + static_cast<int>(__fdividef(static_cast<float>(d.r * c) + 0.5f, static_cast<float>(d.parts)));
+#else
+    return d.q * c + d.r * c / d.parts;
+#endif
 }
 
 // A place x (counted from the unit's beginning) as a step of a unit of n
-// steps. Cuts near the unit's ends move to the ends.
-EXATTN_HD int place_step(const LineShape &s, const LineDeal &d, int64_t x, int n) {
-    if (d.whole || n == 0) return 0;
-    const int64_t y = x - s.unit_cost;
-    int64_t t = y <= 0 ? 0 : (y + s.step_len / 2) / s.step_len;
+// steps and cost c. Cuts near the unit's ends move to the ends.
+EXATTN_HD int place_step(const LineShape &s, int x, int c, int n) {
+    const int y = x - s.unit_cost, all = c - s.unit_cost;
+    if (y <= 0 || all <= 0) return 0;
+    // (an approximate quotient: every CTA forms the same one)
+    const float at = static_cast<float>(y) * static_cast<float>(n);
+#if defined(__CUDA_ARCH__)
+    const int t = smin(static_cast<int>(__fdividef(at, static_cast<float>(all)) + 0.5f), n);
+#else
+    const int t = smin(static_cast<int>(at / static_cast<float>(all) + 0.5f), n);
+#endif
     if (n < 2 * s.min_steps) return 2 * t < n ? 0 : n;
     if (t < s.min_steps) return 0;
-    return n - t < s.min_steps ? n : static_cast<int>(t);
+    return n - t < s.min_steps ? n : t;
 }
 
 // A place on the line: step `step` of `unit` of `head` of sequence `seq`.
@@ -155,40 +181,31 @@ struct Place {
 };
 
 // The place `rem` into the sequence's part of the line (0 <= rem < its cost).
-EXATTN_HD Place place_in_seq(const LineShape &s, const LineDeal &d, int seq, int sq, int sk, int64_t rem) {
+// (The kernels try many units at once.)
+inline Place place_in_seq(const LineShape &s, int seq, int sq, int sk, int rem) {
     Place p;
     p.seq = seq;
     const int n = line_units(s, sq, sk);
-    const int64_t per_head = deal_before(s, d, sq, sk, n);
-    p.head = static_cast<int>(rem / per_head);
+    const int per_head = line_before(s, sq, sk, n);
+    p.head = rem / per_head;
     rem -= p.head * per_head;
-    int lo = 0, hi = n - 1;  // the last unit that begins at or before rem
-    while (lo < hi) {
-        const int mid = lo + (hi - lo + 1) / 2;
-        if (deal_before(s, d, sq, sk, mid) <= rem)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    p.unit = lo;
+    p.unit = 0;  // the last unit that begins at or before rem
+    while (p.unit + 1 < n && line_before(s, sq, sk, p.unit + 1) <= rem) ++p.unit;
     int first, count;
-    line_steps(s, sq, sk, lo, &first, &count);
-    p.step = place_step(s, d, rem - deal_before(s, d, sq, sk, lo), count);
+    line_steps(s, sq, sk, p.unit, &first, &count);
+    const int u0 = line_before(s, sq, sk, p.unit);
+    p.step = place_step(s, rem - u0, line_before(s, sq, sk, p.unit + 1) - u0, count);
     return p;
 }
 
-// The parts that share a unit whose place on the line is [x0, x1) and which
-// has n steps: the first one, and how many. The unit is known to be cut.
-EXATTN_HD void unit_sharers(const LineShape &s, const LineDeal &d, int64_t x0, int64_t x1, int n, int *first,
-                            int *count) {
-    // part c cuts the unit if it begins inside it, away from its ends
-    int a = static_cast<int>(x0 * d.parts / d.length);
-    while (part_begin(d, a) < x0) ++a;
-    while (a < d.parts && place_step(s, d, part_begin(d, a) - x0, n) == 0) ++a;
-    int z = static_cast<int>(smin64((x1 * d.parts + d.length - 1) / d.length, d.parts - 1));
-    while (z > a && (part_begin(d, z) >= x1 || place_step(s, d, part_begin(d, z) - x0, n) >= n)) --z;
-    *first = a - 1;
-    *count = z - a + 2;
+// Whether part c begins inside a unit that begins at x0, costs `cost` and has n
+// steps, away from its ends: where it cuts it. The parts that share a unit are
+// the one before the first cut, and one per cut.
+EXATTN_HD bool part_cuts(const LineShape &s, const LineDeal &d, int c, int x0, int cost, int n) {
+    const int x = part_begin(d, c) - x0;
+    if (x <= 0 || x >= cost) return false;
+    const int t = place_step(s, x, cost, n);
+    return t > 0 && t < n;
 }
 
 // A sequence of the line: its query rows and keys.
@@ -201,56 +218,58 @@ struct UnitRange {
     int seq, head, unit;
     int step0, nstep;  // steps [step0, step0 + nstep), counted from the sequence's first key (token)
     int slot;          // -1: the whole unit; 0: a range that does not begin the unit; 1: one that does
-    int first_part;    // the parts that share the unit
-    int nparts;
+    int x0, cost, steps;  // of a cut unit: its place on the line and its steps, for part_cuts()
 };
 
-// Part `part`'s units in order, from place p (before it lie seq_x0 of the
-// line up to p's sequence) to place e (seq == b: the line's end). len(i): a
-// sequence's lengths; emit(range): false ends the walk.
+// A part's units in order, from place p to place e (seq == b: the line's end).
+// x, units: the lengths and units per head of p's sequence, before which
+// seq_x0 of the line lie. len(i): a sequence's lengths; emit(range): false
+// ends the walk.
 template <class Len, class Emit>
-EXATTN_HD void walk_part(const LineShape &s, const LineDeal &d, int b, int part, Place p, const Place &e,
-                         int64_t seq_x0, Len len, Emit emit) {
-    if (p.seq >= b) return;
-    SeqLen x = len(p.seq);
-    int units = line_units(s, x.sq, x.sk);
+EXATTN_HD void walk_part(const LineShape &s, int b, Place p, const Place &e, SeqLen x, int units, int seq_x0,
+                         Len len, Emit emit) {
+    bool fresh = false;  // p.seq's lengths are still to be read
+#pragma unroll 1
     for (;;) {
-        const bool last = p.seq == e.seq && p.head == e.head && p.unit == e.unit;
-        if (last && p.step >= e.step) return;
-        int first, count;
-        line_steps(s, x.sq, x.sk, p.unit, &first, &count);
-        const int stop = last ? e.step : count;
-        if (p.step < count || count == 0) {
-            UnitRange r;
-            r.seq = p.seq;
-            r.head = p.head;
-            r.unit = p.unit;
-            r.step0 = first + p.step;
-            r.nstep = stop - p.step;
-            r.slot = -1;
-            r.first_part = part;
-            r.nparts = 1;
-            if (p.step > 0 || stop < count) {
-                r.slot = p.step > 0 ? 0 : 1;
-                const int64_t u0 = line_before(s, x.sq, x.sk, p.unit);
-                const int64_t x0 = seq_x0 + p.head * line_before(s, x.sq, x.sk, units) + u0;
-                const int64_t x1 = x0 + line_before(s, x.sq, x.sk, p.unit + 1) - u0;
-                unit_sharers(s, d, x0, x1, count, &r.first_part, &r.nparts);
-            }
-            if (!emit(r)) return;
-        }
-        if (last) return;
-        p.step = 0;
-        if (++p.unit < units) continue;
-        p.unit = 0;
-        if (++p.head < s.heads) continue;
-        p.head = 0;
-        do {
-            seq_x0 += s.heads * deal_before(s, d, x.sq, x.sk, units);
-            if (++p.seq >= b) return;
+        if (p.seq >= b) return;
+        if (fresh) {
             x = len(p.seq);
             units = line_units(s, x.sq, x.sk);
-        } while (units == 0);
+            fresh = false;
+        }
+        if (p.unit < units) {
+            const bool last = p.seq == e.seq && p.head == e.head && p.unit == e.unit;
+            if (last && p.step >= e.step) return;
+            int first, count;
+            line_steps(s, x.sq, x.sk, p.unit, &first, &count);
+            const int stop = last ? e.step : count;
+            if (p.step < count || count == 0) {
+                UnitRange r;
+                r.seq = p.seq;
+                r.head = p.head;
+                r.unit = p.unit;
+                r.step0 = first + p.step;
+                r.nstep = stop - p.step;
+                r.slot = p.step == 0 && stop == count ? -1 : p.step > 0 ? 0 : 1;
+                r.x0 = r.cost = r.steps = 0;
+                if (r.slot >= 0) {
+                    const int u0 = line_before(s, x.sq, x.sk, p.unit);
+                    r.x0 = seq_x0 + p.head * line_before(s, x.sq, x.sk, units) + u0;
+                    r.cost = line_before(s, x.sq, x.sk, p.unit + 1) - u0;
+                    r.steps = count;
+                }
+                if (!emit(r)) return;
+            }
+            if (last) return;
+            p.step = 0;
+            if (++p.unit < units) continue;
+            p.unit = 0;
+            if (++p.head < s.heads) continue;
+        }
+        p.head = 0;
+        seq_x0 += s.heads * line_before(s, x.sq, x.sk, units);
+        ++p.seq;
+        fresh = true;
     }
 }
 
