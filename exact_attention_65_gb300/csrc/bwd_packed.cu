@@ -35,6 +35,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "internal.h"
 #include "packed_dev.cuh"
 #include "ptx.cuh"
@@ -74,8 +76,8 @@ struct PBwdGeom {
     static constexpr int BAR_FF = 0, BAR_FE = 1;
     static constexpr int BAR_RF = 2;
     static constexpr int BAR_RE = BAR_RF + SLOTS;
-    static constexpr int BAR_SF = BAR_RE + SLOTS;  // a step's S and dP made
-    static constexpr int BAR_PF = BAR_SF + 1;      // [2] a half's P / dS stored
+    static constexpr int BAR_SF = BAR_RE + SLOTS;  // [2] a step's S made, its dP made
+    static constexpr int BAR_PF = BAR_SF + 2;      // [2] a half's P / dS stored
     static constexpr int BAR_AF = BAR_PF + 2;
     static constexpr int BAR_AE = BAR_AF + 1;
     static constexpr int BAR_LDF = BAR_AE + 1;         // [kStages]
@@ -292,37 +294,48 @@ __device__ __forceinline__ void pbwd_mma(uint32_t sbase, uint32_t tmem, const Un
     const uint64_t ring_mn = smem_desc(sbase + G::OFF_RING, G::PANEL_BYTES, G::SBO, G::LAYOUT);
     constexpr uint32_t tile16 = G::TILE_BYTES >> 4;
 
-    // S and dP of a step: the fixed tiles (A: from TMEM in the query-tile
-    // kind) times the streamed pair (B, K-major), over the head dim
-    auto issue_sdp = [&](int sa, int sb) {
-        const uint64_t ba = ring_k + sa * tile16, bb = ring_k + sb * tile16;
+    // S (w = 0) or dP (w = 1) of a step: a fixed tile (A: from TMEM in the
+    // query-tile kind) times a streamed tile (B, K-major), over the head dim
+    auto issue_s = [&](auto which, int slot) {
+        constexpr int w = decltype(which)::value;
+        const uint64_t b = ring_k + slot * tile16;
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const int p = (kk * 16) / G::PANEL_ELEMS;
-                const int off = ((kk * 16) % G::PANEL_ELEMS) * 2;
-                const uint32_t o16 = (p * G::PANEL_BYTES + off) >> 4;
-                if constexpr (MODE == kModeDQ)
-                    mma_ts(tmem + (w ? G::T_P : G::T_S), tmem + (w ? G::T_DO : G::T_Q) + kk * 8,
-                           (w ? bb : ba) + o16, idesc_s, kk > 0 ? 1u : 0u);
-                else
-                    mma_ss(tmem + (w ? G::T_P : G::T_S), fix_k + (w ? tile16 : 0u) + o16, (w ? bb : ba) + o16,
-                           idesc_s, kk > 0 ? 1u : 0u);
-            }
-        mma_commit(bar(G::BAR_SF));
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const int p = (kk * 16) / G::PANEL_ELEMS;
+            const int off = ((kk * 16) % G::PANEL_ELEMS) * 2;
+            const uint32_t o16 = (p * G::PANEL_BYTES + off) >> 4;
+            if constexpr (MODE == kModeDQ)
+                mma_ts(tmem + (w ? G::T_P : G::T_S), tmem + (w ? G::T_DO : G::T_Q) + kk * 8, b + o16, idesc_s,
+                       kk > 0 ? 1u : 0u);
+            else
+                mma_ss(tmem + (w ? G::T_P : G::T_S), fix_k + (w ? tile16 : 0u) + o16, b + o16, idesc_s,
+                       kk > 0 ? 1u : 0u);
+        }
+        mma_commit(bar(G::BAR_SF + w));
     };
+    using IsS = std::integral_constant<int, 0>;
+    using IsP = std::integral_constant<int, 1>;
     // acc (+)= A[TMEM: 128 rows x HN, 16-bit] times rows [h HN, h HN + HN) of
     // a streamed tile (MN-major), up to row `rows`. The group that made
     // columns [32g, 32g + 32) of the half packed them into its columns
-    // [32g, 32g + 16).
-    auto acc_half = [&](uint32_t dst, uint32_t a_tmem, uint64_t b_mn, int h, int rows, bool first) {
+    // [32g, 32g + 16). Whole halves are the case that counts: without a
+    // condition per product (with one, a product took 150 cycles to issue
+    // instead of 64).
+    auto acc_half = [&](uint32_t dst, uint32_t a_tmem, uint64_t b_mn, auto half, int rows, bool first) {
+        constexpr int h = decltype(half)::value;
+        if (rows >= (h + 1) * G::HN) {
 #pragma unroll
-        for (int kk = 0; kk < G::HN / 16; ++kk)
-            if (h * G::HN + kk * 16 < rows)
+            for (int kk = 0; kk < G::HN / 16; ++kk)
                 mma_ts(dst, a_tmem + h * G::HN + (kk >> 1) * 32 + (kk & 1) * 8,
                        b_mn + (((h * G::HN + kk * 16) * G::ROW_BYTES) >> 4), idesc_acc,
                        (!first || kk > 0) ? 1u : 0u);
+        } else {
+#pragma unroll 1
+            for (int kk = 0; h * G::HN + kk * 16 < rows; ++kk)
+                mma_ts(dst, a_tmem + h * G::HN + (kk >> 1) * 32 + (kk & 1) * 8,
+                       b_mn + (((h * G::HN + kk * 16) * G::ROW_BYTES) >> 4), idesc_acc,
+                       (!first || kk > 0) ? 1u : 0u);
+        }
     };
     auto wait_ring = [&](int gs, int &sa, int &sb) {
         const int na = 2 * gs, nb = na + 1;
@@ -364,50 +377,48 @@ __device__ __forceinline__ void pbwd_mma(uint32_t sbase, uint32_t tmem, const Un
         int sa = 0, sb = 0;
         if (!wait_ring(base, sa, sb)) break;
         tc_fence_after();
-        issue_sdp(sa, sb);
-        for (int j = 0; ok && j < count; ++j) {
+        issue_s(IsS{}, sa);
+        issue_s(IsP{}, sb);
+#pragma unroll 1
+        for (int j = 0; j < count; ++j) {
             const int gs = base + j;
-            int na = 0, nb = 0;
+            int na = sa, nb = sb;  // ring slots of step j + 1
             const bool last = j == count - 1;
             if (last && zero_tail) {
                 mbar_arrive(bar(G::BAR_LAND));
-                if (!await(bar(G::BAR_ZERO), zeroed & 1, g, 11)) {
-                    ok = false;
-                    break;
-                }
+                if (!(ok = await(bar(G::BAR_ZERO), zeroed & 1, g, 11))) break;
                 ++zeroed;
             }
             const int rows = last ? rows_tail : rows_full;
-            for (int h = 0; h < 2; ++h) {
-                if (!await(bar(G::BAR_PF + h), gs & 1, g, 8)) {
-                    ok = false;
-                    break;
-                }
-                if (j == 0 && h == 0 && !await(bar(G::BAR_AE), (it_u & 1) ^ 1, g, 7)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const bool first = j == 0 && h == 0;
-                if constexpr (MODE == kModeDQ) {
-                    acc_half(tmem + G::T_A0, tmem + G::T_S, ring_mn + sa * tile16, h, rows, first);
-                } else {
-                    acc_half(tmem + G::T_A0, tmem + G::T_S, ring_mn + sb * tile16, h, rows, first);
-                    acc_half(tmem + G::T_A1, tmem + G::T_P, ring_mn + sa * tile16, h, rows, first);
-                }
-                if (h == 1) {
-                    mma_commit(bar(G::BAR_RE + sa));
-                    mma_commit(bar(G::BAR_RE + sb));
-                    if (!last) {
-                        if (!wait_ring(gs + 1, na, nb)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        issue_sdp(na, nb);
-                    }
-                }
+            // first half: added up while the warps work on the second
+            ok = await(bar(G::BAR_PF), gs & 1, g, 8);
+            // (the unit's first addition overwrites the accumulators: the last
+            // unit's epilogue must have read them out)
+            if (j == 0) ok = ok && await(bar(G::BAR_AE), (it_u & 1) ^ 1, g, 7);
+            if (!ok) break;
+            tc_fence_after();
+            if constexpr (MODE == kModeDQ) {
+                acc_half(tmem + G::T_A0, tmem + G::T_S, ring_mn + sa * tile16, IsS{}, rows, j == 0);
+            } else {
+                acc_half(tmem + G::T_A0, tmem + G::T_S, ring_mn + sb * tile16, IsS{}, rows, j == 0);
+                acc_half(tmem + G::T_A1, tmem + G::T_P, ring_mn + sa * tile16, IsS{}, rows, j == 0);
             }
+            if (!last && !(ok = wait_ring(gs + 1, na, nb))) break;
+            // second half, then the next step's S as soon as what it overwrites
+            // has been read, and its dP: the warps begin with S
+            if (!(ok = await(bar(G::BAR_PF + 1), gs & 1, g, 8))) break;
+            tc_fence_after();
+            if constexpr (MODE == kModeDQ) {
+                acc_half(tmem + G::T_A0, tmem + G::T_S, ring_mn + sa * tile16, IsP{}, rows, false);
+                if (!last) issue_s(IsS{}, na);
+            } else {
+                acc_half(tmem + G::T_A0, tmem + G::T_S, ring_mn + sb * tile16, IsP{}, rows, false);
+                if (!last) issue_s(IsS{}, na);
+                acc_half(tmem + G::T_A1, tmem + G::T_P, ring_mn + sa * tile16, IsP{}, rows, false);
+            }
+            mma_commit(bar(G::BAR_RE + sa));
+            mma_commit(bar(G::BAR_RE + sb));
+            if (!last) issue_s(IsP{}, nb);
             sa = na;
             sb = nb;
         }
@@ -539,55 +550,65 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
             const bool ok = await(bar(G::BAR_SF), step & 1, g, 13);
             if (!__all_sync(0xffffffffu, ok)) return;
             tc_fence_after();
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                const int c0 = h * G::HN + 32 * cg;  // this group's 32 columns of the half
+            // a half: P from S, then dS from dP, columns [c0, c0 + 32)
+            auto half = [&](auto is_masked, int h) {
+                constexpr bool MASKED = decltype(is_masked)::value;
+                const int c0 = h * G::HN + 32 * cg;
+                const uint32_t tS = tmem + lanes + G::T_S + c0, tP = tmem + lanes + G::T_P + c0;
+                const float4 *ld4 = reinterpret_cast<const float4 *>(ldbuf) + (c0 >> 2);
                 uint32_t sv[32], pv[32];
-                tmem_ld32(tmem + lanes + G::T_S + c0, sv);
-                tmem_ld32(tmem + lanes + G::T_P + c0, pv);
+                float *p = reinterpret_cast<float *>(sv);
+                tmem_ld32(tS, sv);
                 tmem_wait_ld();
                 if constexpr (MODE == kModeDQ) {
-                    uint32_t pk[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float d0 = fast_exp2(__uint_as_float(sv[2 * i]) * c - lse2) *
-                                   (__uint_as_float(pv[2 * i]) - drow);
-                        float d1 = fast_exp2(__uint_as_float(sv[2 * i + 1]) * c - lse2) *
-                                   (__uint_as_float(pv[2 * i + 1]) - drow);
-                        if (masked) {  // keys that the row does not see take no part
-                            d0 = c0 + 2 * i < cmax ? d0 : 0.f;
-                            d1 = c0 + 2 * i + 1 < cmax ? d1 : 0.f;
-                        }
-                        pk[i] = pack2q<BF16>(d0, d1);
-                    }
-                    tmem_st16(tmem + lanes + G::T_S + c0, pk);
+                    for (int i = 0; i < 32; ++i) p[i] = fast_exp2(p[i] * c - lse2);
                 } else {
-                    const float4 *ld4 = reinterpret_cast<const float4 *>(ldbuf);
-                    uint32_t pp[16], pd[16];
+                    uint32_t pp[16];
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {  // four columns per shared-memory read
-                        const float4 l4 = ld4[(c0 >> 2) + q], d4 = ld4[(G::BT >> 2) + (c0 >> 2) + q];
-                        const float lv[4] = {l4.x, l4.y, l4.z, l4.w}, dv[4] = {d4.x, d4.y, d4.z, d4.w};
-                        float pr[4], dr[4];
+                        const float4 l4 = ld4[q];
+                        const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int i = 4 * q + e;
-                            pr[e] = fast_exp2(__uint_as_float(sv[i]) * c - lv[e]);
-                            dr[e] = pr[e] * (__uint_as_float(pv[i]) - dv[e]);
-                            if (masked) {
-                                const bool in = c0 + i >= cmin && c0 + i < cmax;
-                                pr[e] = in ? pr[e] : 0.f;
-                                dr[e] = in ? dr[e] : 0.f;
-                            }
+                            p[i] = fast_exp2(p[i] * c - lv[e]);
+                            // (by selection: what a masked place holds may be NaN)
+                            if (MASKED) p[i] = c0 + i >= cmin && c0 + i < cmax ? p[i] : 0.f;
                         }
-                        pp[2 * q] = pack2q<BF16>(pr[0], pr[1]);
-                        pp[2 * q + 1] = pack2q<BF16>(pr[2], pr[3]);
-                        pd[2 * q] = pack2q<BF16>(dr[0], dr[1]);
-                        pd[2 * q + 1] = pack2q<BF16>(dr[2], dr[3]);
+                        pp[2 * q] = pack2q<BF16>(p[4 * q], p[4 * q + 1]);
+                        pp[2 * q + 1] = pack2q<BF16>(p[4 * q + 2], p[4 * q + 3]);
                     }
-                    tmem_st16(tmem + lanes + G::T_S + c0, pp);
-                    tmem_st16(tmem + lanes + G::T_P + c0, pd);
+                    tmem_st16(tS, pp);
                 }
+                if (h == 0) {
+                    const bool okp = await(bar(G::BAR_SF + 1), step & 1, g, 13);
+                    if (!__all_sync(0xffffffffu, okp)) return false;
+                    tc_fence_after();
+                }
+                tmem_ld32(tP, pv);
+                tmem_wait_ld();
+                uint32_t pd[16];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    float dv[4] = {drow, drow, drow, drow}, dr[4];
+                    if constexpr (MODE == kModeDKV) {
+                        const float4 d4 = ld4[(G::BT >> 2) + q];
+                        dv[0] = d4.x;
+                        dv[1] = d4.y;
+                        dv[2] = d4.z;
+                        dv[3] = d4.w;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = 4 * q + e;
+                        dr[e] = p[i] * (__uint_as_float(pv[i]) - dv[e]);
+                        if (MASKED) dr[e] = c0 + i >= cmin && c0 + i < cmax ? dr[e] : 0.f;
+                    }
+                    pd[2 * q] = pack2q<BF16>(dr[0], dr[1]);
+                    pd[2 * q + 1] = pack2q<BF16>(dr[2], dr[3]);
+                }
+                tmem_st16(MODE == kModeDQ ? tS : tP, pd);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -595,7 +616,17 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
                     mbar_arrive(bar(G::BAR_PF + h));
                     if (MODE == kModeDKV && h == 1) mbar_arrive(bar(G::BAR_LDE + step % kStages));
                 }
+                return true;
+            };
+            bool done;
+            if (!masked) {
+                done = half(std::false_type{}, 0) && half(std::false_type{}, 1);
+            } else {
+                done = true;
+#pragma unroll 1
+                for (int h = 0; h < 2 && done; ++h) done = half(std::true_type{}, h);
             }
+            if (!done) return;
         }
 
         // ---------------------------------------------------- epilogue
