@@ -364,25 +364,30 @@ def attn_bwd(q, k, v, o, lse, dout, scale: float | None = None, dq=None, dk=None
     return dq, dk, dv
 
 
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+
+
 def _rows(name, t, idx, dt):
     """Token stride of packed rows [tokens, heads, d] whose heads lie side by
     side (a tensor of their own, or a slice of wider rows)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
-        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, d]")
+        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, d] (there is no CPU path)")
     if t.dtype is not dt:
-        raise TypeError("q, k, v must share one dtype")
+        raise TypeError(f"{name} must be {dt}, got {t.dtype}: all rows share one dtype")
     if t.get_device() != idx:
-        raise ValueError(f"{name} must be on q's device")
+        raise ValueError(f"{name} must be on the same device as the other tensors")
     n, h, d = t.shape
     s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != d and h != 1) or (s0 < h * d and n != 1) or s0 % 8:
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: heads must lie d apart within a token's row, and rows a multiple of 8 apart")
-    # a lone row has no distance to the next
-    return s0 if n != 1 and s0 >= h * d else h * d
+    if s2 == 1 and (s1 == d or h == 1) and s0 >= h * d and s0 % 8 == 0:
+        return s0
+    # (a lone row has no distance to the next one)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: heads must lie d apart within a token's row, and rows a multiple of 8 apart")
+    return h * d
 
 
-def _int_array(name, t, shape, idx, dtype=torch.int32):
+def _array(name, t, shape, idx, dtype):
+    """Raises if t is not a contiguous array of that shape and dtype on device idx."""
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != idx \
             or tuple(t.shape) != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor {list(shape)} on the same device")
@@ -390,30 +395,66 @@ def _int_array(name, t, shape, idx, dtype=torch.int32):
 
 def _packed_q(q, cu_seqlens_q, out, lse):
     """Sizes, dtype code, device index and token stride of packed query rows,
-    with their outputs."""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
-        raise ValueError("q must be a CUDA tensor [total_q, h, d] (there is no CPU path)")
-    idx = q.get_device()
-    dt = q.dtype
+    with their outputs. (Kept lean: short batches issue in a few microseconds,
+    and this runs on every call.)"""
+    try:
+        idx = q.get_device()
+        dt = q.dtype
+        t, h, d = q.shape
+        s0, s1, s2 = q.stride()
+        b = cu_seqlens_q.shape[0] - 1
+        fine = (idx >= 0 and s2 == 1 and s1 == d and s0 >= h * d and s0 % 8 == 0 and cu_seqlens_q.dtype is _I32
+                and cu_seqlens_q.get_device() == idx and cu_seqlens_q.is_contiguous()
+                and cu_seqlens_q.dim() == 1 and b >= 1)
+    except (AttributeError, ValueError, TypeError, IndexError):
+        fine = False
+    if not fine:
+        if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
+            raise ValueError("q must be a CUDA tensor [total_q, h, d] (there is no CPU path)")
+        idx, dt = q.get_device(), q.dtype
+        t, h, d = q.shape
+        s0 = _rows("q", q, idx, dt)
+        if not isinstance(cu_seqlens_q, torch.Tensor) or cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] < 2:
+            raise ValueError("cu_seqlens_q must be an int32 tensor [b + 1]")
+        b = cu_seqlens_q.shape[0] - 1
+        _array("cu_seqlens_q", cu_seqlens_q, (b + 1,), idx, _I32)
     code = _DTYPE_CODE.get(dt)
     if code is None:
         raise TypeError(f"exattn takes float16 or bfloat16 tensors, got {dt}")
-    t, h, d = q.shape
-    stride = _rows("q", q, idx, dt)
-    if not isinstance(cu_seqlens_q, torch.Tensor) or cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] < 2:
-        raise ValueError("cu_seqlens_q must be an int32 tensor [b + 1]")
-    b = cu_seqlens_q.shape[0] - 1
-    _int_array("cu_seqlens_q", cu_seqlens_q, (b + 1,), idx)
     if out is None:
         out = torch.empty((t, h, d), dtype=dt, device=q.device)
     elif out.shape != q.shape or out.dtype is not dt or not out.is_contiguous() or out.get_device() != idx:
         raise ValueError("out must be a contiguous tensor with q's shape and dtype")
     if lse is None:
-        lse = torch.empty((h, t), dtype=torch.float32, device=q.device)
-    elif (lse.shape != (h, t) or lse.dtype is not torch.float32 or not lse.is_contiguous()
+        lse = torch.empty((h, t), dtype=_F32, device=q.device)
+    elif (lse.shape != (h, t) or lse.dtype is not _F32 or not lse.is_contiguous()
           or lse.get_device() != idx):
         raise ValueError("lse must be a contiguous float32 tensor [h, total_q]")
-    return b, t, h, d, code, idx, stride, out, lse
+    return b, t, h, d, code, idx, s0, out, lse
+
+
+def _packed_kv(q, k, v, cu_seqlens_k, b, h, d, idx):
+    """Rows, heads and token strides of packed k and v."""
+    try:
+        dt = q.dtype
+        tk, hk, dk = k.shape
+        ks, k1, k2 = k.stride()
+        vs, v1, v2 = v.stride()
+        row = hk * d
+        fine = (k.dtype is dt and v.dtype is dt and k.get_device() == idx and v.get_device() == idx
+                and v.shape == k.shape and dk == d and k2 == 1 and v2 == 1 and k1 == d and v1 == d and ks >= row
+                and vs >= row and ks % 8 == 0 and vs % 8 == 0 and hk >= 1 and h % hk == 0
+                and cu_seqlens_k.dtype is _I32 and cu_seqlens_k.get_device() == idx
+                and cu_seqlens_k.shape == (b + 1,) and cu_seqlens_k.is_contiguous())
+    except (AttributeError, ValueError, TypeError):
+        fine = False
+    if not fine:
+        ks, vs = _rows("k", k, idx, q.dtype), _rows("v", v, idx, q.dtype)
+        tk, hk, dk = k.shape
+        if v.shape != k.shape or dk != d or hk < 1 or h % hk:
+            raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
+        _array("cu_seqlens_k", cu_seqlens_k, (b + 1,), idx, _I32)
+    return tk, hk, ks, vs
 
 
 def attn_fwd_packed(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int = 0,
@@ -430,16 +471,12 @@ def attn_fwd_packed(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int = 0,
     [total_q, h, d] and lse [h, total_q]; rows of no sequence are left as
     they were."""
     b, t, h, d, dt, idx, qs, out, lse = _packed_q(q, cu_seqlens_q, out, lse)
-    ks, vs = _rows("k", k, idx, q.dtype), _rows("v", v, idx, q.dtype)
-    tk, hk, dk = k.shape
-    if v.shape != k.shape or dk != d or hk < 1 or h % hk:
-        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
-    _int_array("cu_seqlens_k", cu_seqlens_k, (b + 1,), idx)
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    tk, hk, ks, vs = _packed_kv(q, k, v, cu_seqlens_k, b, h, d, idx)
     lib = _lib or load_library()
     rc = _call(lib.attn_fwd_packed, idx, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), out.data_ptr(), lse.data_ptr(), b, t, tk,
-               int(max_seqlen_q), h, hk, d, qs, ks, vs, scale, 1 if causal else 0, dt)
+               max_seqlen_q, h, hk, d, qs, ks, vs, 1.0 / math.sqrt(d) if scale is None else scale,
+               1 if causal else 0, dt)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_fwd_packed")
     return out, lse
@@ -453,16 +490,13 @@ def attn_bwd_packed(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, scale: fl
     lse: its results; dout: [total_q, h, d], contiguous. dq, dk, dv may be
     slices of wider rows, as q, k, v may (tensors of their own where they are
     not given); rows of no sequence are left as they were."""
-    if not isinstance(dout, torch.Tensor) or not dout.is_contiguous():
-        raise ValueError("dout must be a contiguous tensor like o")
+    if o is None or lse is None:
+        raise ValueError("o and lse must be the forward's results")
     b, t, h, d, dt, idx, qs, o, lse = _packed_q(q, cu_seqlens_q, o, lse)
-    ks, vs = _rows("k", k, idx, q.dtype), _rows("v", v, idx, q.dtype)
-    tk, hk, dk_ = k.shape
-    if v.shape != k.shape or dk_ != d or hk < 1 or h % hk:
-        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
-    if dout.shape != q.shape or dout.dtype is not q.dtype or dout.get_device() != idx:
+    tk, hk, ks, vs = _packed_kv(q, k, v, cu_seqlens_k, b, h, d, idx)
+    if not isinstance(dout, torch.Tensor) or dout.shape != q.shape or dout.dtype is not q.dtype \
+            or not dout.is_contiguous() or dout.get_device() != idx:
         raise ValueError("dout must be a contiguous tensor with q's shape and dtype")
-    _int_array("cu_seqlens_k", cu_seqlens_k, (b + 1,), idx)
     grads, strides = [], []
     for name, x, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         if x is None:
@@ -471,26 +505,33 @@ def attn_bwd_packed(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, scale: fl
         if x.shape != like.shape:
             raise ValueError(f"{name} must have {name[1]}'s shape")
         grads.append(x)
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     lib = _lib or load_library()
     rc = _call(lib.attn_bwd_packed, idx, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                lse.data_ptr(), dout.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(),
                grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(), b, t, tk, h, hk, d, qs, ks, vs,
-               *strides, scale, 1 if causal else 0, dt)
+               *strides, 1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0, dt)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_bwd_packed")
     return tuple(grads)
 
 
 def _pools(k_pages, v_pages, idx, dt):
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.get_device() != idx or t.dtype is not dt \
-                or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous tensor [num_pages, page_size, h_kv, d] with the "
-                             "rows' dtype and device")
-    if k_pages.shape != v_pages.shape:
+    """Shape [num_pages, page_size, h_kv, d] of a pair of page pools."""
+    try:
+        shape = k_pages.shape
+        fine = (len(shape) == 4 and v_pages.shape == shape and k_pages.dtype is dt and v_pages.dtype is dt
+                and k_pages.get_device() == idx and v_pages.get_device() == idx and k_pages.is_contiguous()
+                and v_pages.is_contiguous())
+    except AttributeError:
+        fine = False
+    if not fine:
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+            if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.get_device() != idx or t.dtype is not dt \
+                    or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous tensor [num_pages, page_size, h_kv, d] with the "
+                                 "rows' dtype and device")
         raise ValueError("k_pages and v_pages must have the same shape")
-    return k_pages.shape
+    return shape
 
 
 def attn_chunk_paged(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q: int = 0,
@@ -511,14 +552,13 @@ def attn_chunk_paged(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens_k, 
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be an int32 tensor [b, max_pages]")
     max_pages = block_table.shape[1]
-    _int_array("block_table", block_table, (b, max_pages), idx)
-    _int_array("seqlens_k", seqlens_k, (b,), idx)
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    _array("block_table", block_table, (b, max_pages), idx, _I32)
+    _array("seqlens_k", seqlens_k, (b,), idx, _I32)
     lib = _lib or load_library()
     rc = _call(lib.attn_chunk_paged, idx, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                block_table.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), out.data_ptr(),
-               lse.data_ptr(), b, t, int(max_seqlen_q), h, hk, d, num_pages, page_size, max_pages, qs, scale,
-               1 if causal else 0, dt)
+               lse.data_ptr(), b, t, max_seqlen_q, h, hk, d, num_pages, page_size, max_pages, qs,
+               1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0, dt)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_chunk_paged")
     return out, lse
@@ -540,37 +580,39 @@ def attn_paged_plan(seqlens_k, new_lens, block_table, free_pages, free_count, pa
     free_left are the next step's seqlens_k and free_count."""
     if not isinstance(seqlens_k, torch.Tensor) or not seqlens_k.is_cuda or seqlens_k.dim() != 1:
         raise ValueError("seqlens_k must be an int32 CUDA tensor [b] (there is no CPU path)")
-    b, idx, device = seqlens_k.shape[0], seqlens_k.get_device(), seqlens_k.device
-    _int_array("seqlens_k", seqlens_k, (b,), idx)
-    _int_array("new_lens", new_lens, (b,), idx)
-    for name, t, n in (("block_table", block_table, 2), ("free_pages", free_pages, 1)):
-        if not isinstance(t, torch.Tensor) or t.dim() != n:
-            raise ValueError(f"{name} must be an int32 tensor of {n} dimension(s)")
-    max_pages, num_free = block_table.shape[1], free_pages.shape[0]
-    _int_array("block_table", block_table, (b, max_pages), idx)
-    _int_array("free_pages", free_pages, (num_free,), idx)
-    _int_array("free_count", free_count, (1,), idx)
+    b, idx = seqlens_k.shape[0], seqlens_k.get_device()
     if cu_seqlens_q is None:
-        cu_seqlens_q = torch.empty(b + 1, dtype=torch.int32, device=device)
+        cu_seqlens_q = torch.empty(b + 1, dtype=_I32, device=seqlens_k.device)
     if seqlens_out is None:
-        seqlens_out = torch.empty(b, dtype=torch.int32, device=device)
+        seqlens_out = torch.empty(b, dtype=_I32, device=seqlens_k.device)
     if free_left is None:
-        free_left = torch.empty(1, dtype=torch.int32, device=device)
+        free_left = torch.empty(1, dtype=_I32, device=seqlens_k.device)
     if slot_map is None:
         if max_tokens is None:
             raise ValueError("give max_tokens or slot_map")
-        slot_map = torch.empty(int(max_tokens), dtype=torch.int64, device=device)
+        slot_map = torch.empty(int(max_tokens), dtype=_I64, device=seqlens_k.device)
     elif max_tokens is not None and int(max_tokens) != slot_map.numel():
         raise ValueError("slot_map must have max_tokens entries")
-    _int_array("cu_seqlens_q", cu_seqlens_q, (b + 1,), idx)
-    _int_array("seqlens_out", seqlens_out, (b,), idx)
-    _int_array("free_left", free_left, (1,), idx)
-    _int_array("slot_map", slot_map, (slot_map.numel(),), idx, torch.int64)
+    for name, t, n in (("block_table", block_table, 2), ("free_pages", free_pages, 1), ("slot_map", slot_map, 1)):
+        if not isinstance(t, torch.Tensor) or t.dim() != n:
+            raise ValueError(f"{name} must be a tensor of {n} dimension(s)")
+    max_pages, num_free, room = block_table.shape[1], free_pages.shape[0], slot_map.shape[0]
+    for name, t, shape in (("seqlens_k", seqlens_k, (b,)), ("new_lens", new_lens, (b,)),
+                           ("block_table", block_table, (b, max_pages)), ("free_pages", free_pages, (num_free,)),
+                           ("free_count", free_count, (1,)), ("cu_seqlens_q", cu_seqlens_q, (b + 1,)),
+                           ("seqlens_out", seqlens_out, (b,)), ("free_left", free_left, (1,))):
+        try:
+            fine = t.dtype is _I32 and t.get_device() == idx and t.shape == shape and t.is_contiguous()
+        except AttributeError:
+            fine = False
+        if not fine:
+            _array(name, t, shape, idx, _I32)
+    _array("slot_map", slot_map, (room,), idx, _I64)
     lib = _lib or load_library()
     rc = _call(lib.attn_paged_plan, idx, stream, seqlens_k.data_ptr(), new_lens.data_ptr(),
                block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), cu_seqlens_q.data_ptr(),
-               seqlens_out.data_ptr(), slot_map.data_ptr(), free_left.data_ptr(), b, max_pages, int(page_size),
-               num_free, slot_map.shape[0])
+               seqlens_out.data_ptr(), slot_map.data_ptr(), free_left.data_ptr(), b, max_pages, page_size,
+               num_free, room)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_paged_plan")
     return cu_seqlens_q, seqlens_out, slot_map, free_left
@@ -586,14 +628,14 @@ def attn_paged_write(k, v, slot_map, k_pages, v_pages, stream=None):
     written in place."""
     if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dim() != 3:
         raise ValueError("k must be a CUDA tensor [tokens, h_kv, d] (there is no CPU path)")
-    idx = k.get_device()
+    idx, dt = k.get_device(), k.dtype
     code = _dtype_code(k)
-    ks, vs = _rows("k", k, idx, k.dtype), _rows("v", v, idx, k.dtype)
-    num_pages, page_size, hk, d = _pools(k_pages, v_pages, idx, k.dtype)
-    t = k.shape[0]
-    if v.shape != k.shape or k.shape[1] != hk or k.shape[2] != d:
+    ks, vs = _rows("k", k, idx, dt), _rows("v", v, idx, dt)
+    num_pages, page_size, hk, d = _pools(k_pages, v_pages, idx, dt)
+    t, h, dk = k.shape
+    if v.shape != k.shape or h != hk or dk != d:
         raise ValueError(f"shape mismatch: k {tuple(k.shape)}, v {tuple(v.shape)}, pages {tuple(k_pages.shape)}")
-    _int_array("slot_map", slot_map, (t,), idx, torch.int64)
+    _array("slot_map", slot_map, (t,), idx, _I64)
     lib = _lib or load_library()
     rc = _call(lib.attn_paged_write, idx, stream, k.data_ptr(), v.data_ptr(), slot_map.data_ptr(),
                k_pages.data_ptr(), v_pages.data_ptr(), t, hk, d, num_pages, page_size, ks, vs, code)

@@ -345,89 +345,107 @@ __device__ __forceinline__ void pbwd_mma(uint32_t sbase, uint32_t tmem, const Un
                await(bar(G::BAR_RF + sb), (nb / G::SLOTS) & 1, g, 6);
     };
 
+    // (the whole warp follows the control flow; one lane issues)
     int it_u = 0, base = 0, zeroed = 0;
     bool ok = true;
     UnitMsg x;
-    for (; ok && take_unit<false>(&x, it_u, msgs, bar(G::BAR_MF), bar(G::BAR_ME), g, 17); ++it_u) {
-        if (!await(bar(G::BAR_FF), it_u & 1, g, 4)) break;
+#pragma unroll 1
+    for (; ok && take_unit<true>(&x, it_u, msgs, bar(G::BAR_MF), bar(G::BAR_ME), g, 17); ++it_u) {
+        ok = await(bar(G::BAR_FF), it_u & 1, g, 4);
         const int count = x.nstep;
         if (count == 0) {  // nothing to add: the accumulators count as made
-            if (!await(bar(G::BAR_AE), (it_u & 1) ^ 1, g, 7)) break;
-            mma_commit(bar(G::BAR_FE));
-            mma_commit(bar(G::BAR_AF));
+            ok = ok && await(bar(G::BAR_AE), (it_u & 1) ^ 1, g, 7);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            if (elect_one()) {
+                mma_commit(bar(G::BAR_FE));
+                mma_commit(bar(G::BAR_AF));
+            }
             continue;
         }
         const int rows_tail = tail_rows<MODE>(x, a);
         const bool zero_tail = tail_zeroed<MODE>(rows_tail, a);
         const int rows_full = MODE == kModeDQ ? G::BT : a.tile_tokens * a.group;
-        if constexpr (MODE == kModeDQ) {
-            // Q and dO into TMEM after the last unit's S / dP products (same
-            // thread, in order); their shared tiles are then free
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const int p = (kk * 16) / G::PANEL_ELEMS;
-                const int off = ((kk * 16) % G::PANEL_ELEMS) * 2;
-                const uint32_t o16 = (p * G::PANEL_BYTES + off) >> 4;
-                tmem_cp_128x256b(tmem + G::T_Q + kk * 8, fix_k + o16);
-                tmem_cp_128x256b(tmem + G::T_DO + kk * 8, fix_k + tile16 + o16);
-            }
-            mma_commit(bar(G::BAR_FE));
-        }
         int sa = 0, sb = 0;
-        if (!wait_ring(base, sa, sb)) break;
+        ok = ok && wait_ring(base, sa, sb);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tc_fence_after();
-        issue_s(IsS{}, sa);
-        issue_s(IsP{}, sb);
+        sa = uniform(sa);
+        sb = uniform(sb);
+        if (elect_one()) {
+            if constexpr (MODE == kModeDQ) {
+                // Q and dO into TMEM after the last unit's S / dP products (same
+                // thread, in order); their shared tiles are then free
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const int p = (kk * 16) / G::PANEL_ELEMS;
+                    const int off = ((kk * 16) % G::PANEL_ELEMS) * 2;
+                    const uint32_t o16 = (p * G::PANEL_BYTES + off) >> 4;
+                    tmem_cp_128x256b(tmem + G::T_Q + kk * 8, fix_k + o16);
+                    tmem_cp_128x256b(tmem + G::T_DO + kk * 8, fix_k + tile16 + o16);
+                }
+                mma_commit(bar(G::BAR_FE));
+            }
+            issue_s(IsS{}, sa);
+            issue_s(IsP{}, sb);
+        }
 #pragma unroll 1
         for (int j = 0; j < count; ++j) {
             const int gs = base + j;
             int na = sa, nb = sb;  // ring slots of step j + 1
             const bool last = j == count - 1;
             if (last && zero_tail) {
-                mbar_arrive(bar(G::BAR_LAND));
-                if (!(ok = await(bar(G::BAR_ZERO), zeroed & 1, g, 11))) break;
+                if (elect_one()) mbar_arrive(bar(G::BAR_LAND));
+                ok = await(bar(G::BAR_ZERO), zeroed & 1, g, 11);
                 ++zeroed;
             }
-            const int rows = last ? rows_tail : rows_full;
+            const int rows = uniform(last ? rows_tail : rows_full);
             // first half: added up while the warps work on the second
-            ok = await(bar(G::BAR_PF), gs & 1, g, 8);
+            ok = ok && await(bar(G::BAR_PF), gs & 1, g, 8);
             // (the unit's first addition overwrites the accumulators: the last
             // unit's epilogue must have read them out)
             if (j == 0) ok = ok && await(bar(G::BAR_AE), (it_u & 1) ^ 1, g, 7);
-            if (!ok) break;
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
-            if constexpr (MODE == kModeDQ) {
-                acc_half(tmem + G::T_A0, tmem + G::T_S, ring_mn + sa * tile16, IsS{}, rows, j == 0);
-            } else {
-                acc_half(tmem + G::T_A0, tmem + G::T_S, ring_mn + sb * tile16, IsS{}, rows, j == 0);
-                acc_half(tmem + G::T_A1, tmem + G::T_P, ring_mn + sa * tile16, IsS{}, rows, j == 0);
+            if (elect_one()) {
+                if constexpr (MODE == kModeDQ) {
+                    acc_half(tmem + G::T_A0, tmem + G::T_S, ring_mn + sa * tile16, IsS{}, rows, j == 0);
+                } else {
+                    acc_half(tmem + G::T_A0, tmem + G::T_S, ring_mn + sb * tile16, IsS{}, rows, j == 0);
+                    acc_half(tmem + G::T_A1, tmem + G::T_P, ring_mn + sa * tile16, IsS{}, rows, j == 0);
+                }
             }
-            if (!last && !(ok = wait_ring(gs + 1, na, nb))) break;
+            if (!last) ok = wait_ring(gs + 1, na, nb);
             // second half, then the next step's S as soon as what it overwrites
             // has been read, and its dP: the warps begin with S
-            if (!(ok = await(bar(G::BAR_PF + 1), gs & 1, g, 8))) break;
+            ok = ok && await(bar(G::BAR_PF + 1), gs & 1, g, 8);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
-            if constexpr (MODE == kModeDQ) {
-                acc_half(tmem + G::T_A0, tmem + G::T_S, ring_mn + sa * tile16, IsP{}, rows, false);
-                if (!last) issue_s(IsS{}, na);
-            } else {
-                acc_half(tmem + G::T_A0, tmem + G::T_S, ring_mn + sb * tile16, IsP{}, rows, false);
-                if (!last) issue_s(IsS{}, na);
-                acc_half(tmem + G::T_A1, tmem + G::T_P, ring_mn + sa * tile16, IsP{}, rows, false);
+            na = uniform(na);
+            nb = uniform(nb);
+            if (elect_one()) {
+                if constexpr (MODE == kModeDQ) {
+                    acc_half(tmem + G::T_A0, tmem + G::T_S, ring_mn + sa * tile16, IsP{}, rows, false);
+                    if (!last) issue_s(IsS{}, na);
+                } else {
+                    acc_half(tmem + G::T_A0, tmem + G::T_S, ring_mn + sb * tile16, IsP{}, rows, false);
+                    if (!last) issue_s(IsS{}, na);
+                    acc_half(tmem + G::T_A1, tmem + G::T_P, ring_mn + sa * tile16, IsP{}, rows, false);
+                }
+                mma_commit(bar(G::BAR_RE + sa));
+                mma_commit(bar(G::BAR_RE + sb));
+                if (!last) {
+                    issue_s(IsP{}, nb);
+                } else {
+                    if constexpr (MODE == kModeDKV) mma_commit(bar(G::BAR_FE));
+                    mma_commit(bar(G::BAR_AF));
+                }
             }
-            mma_commit(bar(G::BAR_RE + sa));
-            mma_commit(bar(G::BAR_RE + sb));
-            if (!last) issue_s(IsP{}, nb);
             sa = na;
             sb = nb;
         }
-        if (!ok) break;
-        if constexpr (MODE == kModeDKV) mma_commit(bar(G::BAR_FE));
-        mma_commit(bar(G::BAR_AF));
         base += count;
     }
-    mma_commit(bar(G::BAR_DONE));
+    if (elect_one()) mma_commit(bar(G::BAR_DONE));
     WaitGuard drain = g;
     uint32_t no_abort = 0;
     drain.abort = &no_abort;
@@ -717,7 +735,7 @@ __device__ __forceinline__ void pbwd_run(const CUtensorMap *tq, const CUtensorMa
         if ((threadIdx.x & 31) == 0 && !(a.flags & kFlagSkipLoads))
             pbwd_producer<D, MODE>(tq, tk, tv, tdo, sbase, msgs, a, g);
     } else if (warp == 1) {
-        if ((threadIdx.x & 31) == 0) pbwd_mma<D, MODE, BF16>(sbase, tmem, msgs, a, g);
+        pbwd_mma<D, MODE, BF16>(sbase, tmem, msgs, a, g);
     } else if (warp == 2) {
         pbwd_stage<D, MODE>(smem, sbase, msgs, a, g);
     } else if (warp == 3) {
@@ -787,7 +805,7 @@ __global__ void __launch_bounds__(kPBwdThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
     const WaitGuard g{abort_flag, a.status, kKernBwd};
     if (keys)
         pbwd_run<D, kModeDKV, BF16>(&tq, &tk, &tv, &tdo, smem, sbase, tmem, blockIdx.x, a.ctas_kv, a, g);

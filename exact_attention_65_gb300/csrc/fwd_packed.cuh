@@ -281,12 +281,19 @@ __device__ __forceinline__ void pack_issue(uint32_t sbase, uint32_t tmem, const 
         }
     };
     // O (+)= P V over the first `keys` keys of the tile, 16 per instruction
+    // (whole tiles without a condition per product)
     auto issue_pv = [&](uint32_t tO, uint32_t tP, uint64_t vdesc, int keys, bool first) {
+        if (keys == G::BN) {
 #pragma unroll
-        for (int kk = 0; kk < G::BN / 16; ++kk)
-            if (kk * 16 < keys)
+            for (int kk = 0; kk < G::BN / 16; ++kk)
                 mma_ts(tO, tP + kk * 8, vdesc + ((kk * 16 * G::ROW_BYTES) >> 4), idesc_o,
                        (!first || kk > 0) ? 1u : 0u);
+        } else {
+#pragma unroll 1
+            for (int kk = 0; kk * 16 < keys; ++kk)
+                mma_ts(tO, tP + kk * 8, vdesc + ((kk * 16 * G::ROW_BYTES) >> 4), idesc_o,
+                       (!first || kk > 0) ? 1u : 0u);
+        }
     };
     // zeros into the rows of a landed V tile from `keys` up to a multiple of 16
     auto zero_tail = [&](int slot, int keys) {
@@ -334,10 +341,11 @@ __device__ __forceinline__ void pack_issue(uint32_t sbase, uint32_t tmem, const 
                 ok = await(bar(G::BAR_KVF + kr.slot), kr.phase, g, 5);
                 if (!__all_sync(0xffffffffu, ok)) return;
                 tc_fence_after();
-                if (lane == 0) {
-                    issue_s(tmem + (j & 1) * G::TMEM_TILE_STRIDE, qdesc, dk + kr.slot * tile16);
+                const int ks = uniform(kr.slot);
+                if (elect_one()) {
+                    issue_s(tmem + (j & 1) * G::TMEM_TILE_STRIDE, qdesc, dk + ks * tile16);
                     mma_commit(bar(G::BAR_SF + (j & 1)));
-                    mma_commit(bar(G::BAR_KVE + kr.slot));
+                    mma_commit(bar(G::BAR_KVE + ks));
                     if (j == nkv - 1) mma_commit(qe);
                 }
                 kr.next();
@@ -357,9 +365,10 @@ __device__ __forceinline__ void pack_issue(uint32_t sbase, uint32_t tmem, const 
                     if (!__all_sync(0xffffffffu, ok)) break;
                     p_phase ^= 1u << (j & 1);
                     tc_fence_after();
-                    if (lane == 0) {
-                        issue_pv(tO, tmem + (j & 1) * G::TMEM_TILE_STRIDE, dv + ring.slot * tile16, keys, j == 0);
-                        mma_commit(bar(G::BAR_KVE + ring.slot));
+                    const int vs = uniform(ring.slot), ukeys = uniform(keys);
+                    if (elect_one()) {
+                        issue_pv(tO, tmem + (j & 1) * G::TMEM_TILE_STRIDE, dv + vs * tile16, ukeys, j == 0);
+                        mma_commit(bar(G::BAR_KVE + vs));
                         mma_commit(bar(G::BAR_PVD));
                         if (j == nkv - 1) mma_commit(bar(G::BAR_OF));
                     }
@@ -373,7 +382,7 @@ __device__ __forceinline__ void pack_issue(uint32_t sbase, uint32_t tmem, const 
                 // been read out (its barrier must not run two phases ahead)
                 ok = await(bar(G::BAR_OE), o_phase ^ 1u, g, 7);
                 if (!__all_sync(0xffffffffu, ok)) break;
-                if (lane == 0) {
+                if (elect_one()) {
                     mma_commit(qe);
                     mma_commit(bar(G::BAR_OF));
                 }
@@ -415,16 +424,17 @@ __device__ __forceinline__ void pack_issue(uint32_t sbase, uint32_t tmem, const 
                 turn ^= 1u;
                 if (!__all_sync(0xffffffffu, ok)) break;
                 tc_fence_after();
-                if (lane == 0) {
+                const int vs = uniform(vr.slot), ks = uniform(kr.slot), ukeys = uniform(keys);
+                if (elect_one()) {
                     if (live) {
                         if (j > 0) {  // O += P_{j-1} V_{j-1}
-                            issue_pv(tS + G::TMEM_O_OFF, tS, dv + vr.slot * tile16, keys, j == 1);
-                            mma_commit(bar(G::BAR_KVE + vr.slot));
+                            issue_pv(tS + G::TMEM_O_OFF, tS, dv + vs * tile16, ukeys, j == 1);
+                            mma_commit(bar(G::BAR_KVE + vs));
                         }
                         if (j < nkv) {
-                            issue_s(tS, qdesc, dk + kr.slot * tile16);
+                            issue_s(tS, qdesc, dk + ks * tile16);
                             mma_commit(bar(G::BAR_SF + t));
-                            mma_commit(bar(G::BAR_KVE + kr.slot));
+                            mma_commit(bar(G::BAR_KVE + ks));
                             if (j == nkv - 1) mma_commit(qe);
                         } else {
                             mma_commit(bar(G::BAR_OF + t));
@@ -446,7 +456,7 @@ __device__ __forceinline__ void pack_issue(uint32_t sbase, uint32_t tmem, const 
         o_phase ^= 1u;
     }
     // No MMA may still be running when TMEM is released.
-    if (lane == 0) mma_commit(bar(G::BAR_DONE + t));
+    if (elect_one()) mma_commit(bar(G::BAR_DONE + t));
     WaitGuard drain = g;
     uint32_t no_abort = 0;
     drain.abort = &no_abort;
@@ -863,7 +873,7 @@ __global__ void __launch_bounds__(kPackThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
     const WaitGuard g{abort_flag, a.status, kKernFwd};
 
     if (warp < 4) {

@@ -30,6 +30,17 @@ __device__ __forceinline__ bool await(uint32_t bar, uint32_t parity, const WaitG
     return true;
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// A value that all lanes hold, known as such to the compiler: what an MMA's
+// descriptors are made of then stays in uniform registers.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // One sequence of a packed batch: its first query row and first key row (0 in
 // a paged cache) and its lengths. Whatever the arrays on the device hold, the
 // rows stay inside the tensors.
