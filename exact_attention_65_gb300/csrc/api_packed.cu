@@ -53,7 +53,9 @@ LineShape pack_line(int heads, int group, bool one_tile, bool causal, const Line
 
 // The backward's query-tile units: one tile against steps of 128 keys.
 LineShape bwd_query_line(int heads, int group, bool causal, const LineBound &bound) {
-    return pack_line(heads, group, true, causal, bound);
+    LineShape s = pack_line(heads, group, true, causal, bound);
+    s.unit_cost *= 2;
+    return s;
 }
 
 // Its key-tile units: 128 keys against tiles of query tokens, whose heads
@@ -435,6 +437,12 @@ attn_status_t attn_bwd_packed(const void *q, const void *k, const void *v, const
     a.seqs.b = b;
     a.seqs.total_q = total_q;
     a.seqs.max_k = total_k;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
     a.o = o;
     a.dout = dout;
     a.lse = lse;
@@ -454,13 +462,11 @@ attn_status_t attn_bwd_packed(const void *q, const void *k, const void *v, const
     a.status = status;
     a.flags = debug_flags();
     a.group_inv = pack_group_inv(a.group);
+    fast_division(a.group, &a.group_mul, &a.group_div);
     const LineBound bound{b, total_q, total_k, total_k};
     a.line[0] = bwd_query_line(h_kv, a.group, causal != 0, bound);
     a.line[1] = bwd_key_line(h_kv, a.group, causal != 0, bound);
-    // Both kinds visit the same pairs of tiles; a key-tile step costs about
-    // 1.1 times a query-tile step (four products against three).
-    a.ctas_kv = (sms * 11 + 10) / 21;
-    a.ctas_q = sms - a.ctas_kv;
+    a.ctas = sms;
     CUtensorMap tq, tk, tv, tdo;
     if (!encode_rows(&tq, q, bf16, d, h, h_kv, total_q, q_stride, a.tile_tokens) ||
         !encode_rows(&tdo, dout, bf16, d, h, h_kv, total_q, qrow, a.tile_tokens) ||
@@ -468,7 +474,7 @@ attn_status_t attn_bwd_packed(const void *q, const void *k, const void *v, const
         !encode_keys(&tv, v, bf16, d, h_kv, total_k, v_stride))
         return ATTN_ERR_CUDA;
     const size_t tile = 128 * static_cast<size_t>(d) * sizeof(float);
-    const size_t part_q = 2 * a.ctas_q * tile, part_kv = 4 * a.ctas_kv * tile;
+    const size_t part_q = 2 * a.ctas * tile, part_kv = 4 * a.ctas * tile;
     const size_t ld = static_cast<size_t>(total_q) * h * sizeof(float2);
     Workspace w;
     if ((st = get_workspace(dev, stream, 2 * sms, part_q + part_kv + ld, &w)) != ATTN_OK) return st;

@@ -8,8 +8,8 @@
 //   bwd_prep_kernel   (LSE log2 e, D) of every row, as pairs in the order of
 //                     the tiles' rows: [h_kv][token][head of the group].
 //   bwd_pack_kernel   one persistent grid of two kinds of CTA, in proportion
-//                     to their work (a key-tile step is four products, a
-//                     query-tile step three): the first `ctas_kv` run
+//                     to their work, which every CTA works out from the lengths;
+//                     some run
 //     key tiles       unit = 128 keys of a K/V head, streaming query tiles of
 //                     its group (floor(128 / g) tokens times g heads), so the
 //                     sum over the group's heads is the product's own sum:
@@ -72,7 +72,7 @@ struct PBwdGeom {
     static constexpr int OFF_LD = OFF_RING + SLOTS * TILE_BYTES;  // [kStages][2][128] LSE, then D
     static constexpr int OFF_MSG = OFF_LD + kStages * 2 * BT * 4;
     static constexpr int OFF_SUM = OFF_MSG + kMsgSlots * 64;
-    static constexpr int OFF_BAR = (OFF_SUM + 12 * 12 + 15) & ~15;
+    static constexpr int OFF_BAR = (OFF_SUM + 2 * 12 * 12 + 15) & ~15;
     static constexpr int BAR_FF = 0, BAR_FE = 1;
     static constexpr int BAR_RF = 2;
     static constexpr int BAR_RE = BAR_RF + SLOTS;
@@ -113,36 +113,123 @@ __device__ __forceinline__ float widen(uint32_t bits) {
         return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
 }
 
-// (LSE log2 e, D = sum_t dO O) per row; D / 8 lanes per row, 16 bytes each of
-// O and dO: one pass over both, bound by HBM.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(256) bwd_prep_kernel(const PackBwdArgs a) {
-    constexpr int LPR = D / 8, RPW = 32 / LPR;
+// The last sequence that begins at or before row `tok`, by a warp: 32 starts
+// are tried at a time. (Any index where the starts are out of order.)
+__device__ __forceinline__ int sequence_of(const SeqArrays &s, int tok) {
     const int lane = threadIdx.x & 31;
-    const int64_t rows = static_cast<int64_t>(a.total_q) * a.h;
-    const int64_t r =
-        (static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5)) * RPW + lane / LPR;
-    const int sub = lane % LPR;
-    float acc = 0.f;
-    if (r < rows) {
-        const uint4 wo = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.o) + r * D + sub * 8);
-        const uint4 wd = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.dout) + r * D + sub * 8);
-        const uint32_t uo[4] = {wo.x, wo.y, wo.z, wo.w}, ud[4] = {wd.x, wd.y, wd.z, wd.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            acc = fmaf(widen<BF16>(uo[i] & 0xffffu), widen<BF16>(ud[i] & 0xffffu), acc);
-            acc = fmaf(widen<BF16>(uo[i] >> 16), widen<BF16>(ud[i] >> 16), acc);
-        }
+    int at = 0, left = s.b;
+#pragma unroll 1
+    while (left > 1) {
+        const int stride = (left + 31) >> 5;
+        const bool in = lane * stride < left && (lane == 0 || __ldg(s.cu_q + at + lane * stride) <= tok);
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, in));
+        at += k * stride;
+        left = min(stride, left - k * stride);
     }
+    return at;
+}
+
+// (LSE log2 e, D) per row; D / 8 lanes per row, 16 bytes each of O and dO: one
+// pass over both, bound by HBM.
+//
+// D = sum_j P_j dP_j = sum_t dO O. O was rounded to 16 bits, which puts an error
+// of up to u |dO| |O| (u = eps / 2) into every dS = P (dP - D) of the row. For a
+// row that sees many keys |O| is small beside |dP|; for one that sees few it
+// is not (with one key dS is 0, and the error would be all that is left), so
+// rows that see at most kFewKeys keys form the sum over the keys, in fp32.
+constexpr int kFewKeys = 8;
+
+template <int D, bool BF16>
+__device__ __forceinline__ float dot8(const uint4 &x, const uint4 &y) {
+    const uint32_t ux[4] = {x.x, x.y, x.z, x.w}, uy[4] = {y.x, y.y, y.z, y.w};
+    float acc = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        acc = fmaf(widen<BF16>(ux[i] & 0xffffu), widen<BF16>(uy[i] & 0xffffu), acc);
+        acc = fmaf(widen<BF16>(ux[i] >> 16), widen<BF16>(uy[i] >> 16), acc);
+    }
+    return acc;
+}
+
+// A block takes `tokens` tokens times `heads` heads (all of them, or a share
+// of many), which lie side by side in memory.
+template <int D>
+struct PrepGeom {
+    static constexpr int LPR = D / 8, RPW = 32 / LPR, ROWS = 8 * RPW;
+    int heads, tokens, heads_inv;
+};
+template <int D>
+__host__ __device__ __forceinline__ PrepGeom<D> prep_geom(int h) {
+    PrepGeom<D> x;
+    x.heads = h < PrepGeom<D>::ROWS ? h : PrepGeom<D>::ROWS;
+    x.tokens = PrepGeom<D>::ROWS / x.heads;
+    x.heads_inv = (65536 + x.heads - 1) / x.heads;  // row / heads = row * heads_inv >> 16, rows <= 128
+    return x;
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) bwd_prep_kernel(const PackBwdArgs a, const PrepGeom<D> geom) {
+    griddep_launch_dependents();  // (the main kernel waits before it reads `ld`)
+    constexpr int LPR = D / 8;
+    const int lane = threadIdx.x & 31, sub = lane % LPR;
+    const int row = threadIdx.x / LPR;
+    const int t = (row * geom.heads_inv) >> 16;
+    const int tok = min(static_cast<int>(blockIdx.x) * geom.tokens + t, a.total_q - 1);
+    const int head = min(static_cast<int>(blockIdx.y) * geom.heads + row - t * geom.heads, a.h - 1);
+    // (lanes past the end repeat the last row and store nothing)
+    const bool live = t < geom.tokens && static_cast<int>(blockIdx.x) * geom.tokens + t < a.total_q &&
+                      static_cast<int>(blockIdx.y) * geom.heads + row - t * geom.heads < a.h;
+    const int kh = divided(head, a.group_mul, a.group_div), j = head - kh * a.group;
+    const int64_t r = static_cast<int64_t>(tok) * a.h + head;
+    const uint4 wo = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.o) + r * D + sub * 8);
+    const uint4 wd = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.dout) + r * D + sub * 8);
+    const float lse2 = a.lse[static_cast<int64_t>(head) * a.total_q + tok] * 1.4426950408889634f;
+    // keys this row sees: the warp finds its first row's sequence, lanes of
+    // later tokens go on from there
+    int seq = sequence_of(a.seqs, __shfl_sync(0xffffffffu, tok, 0));
+    while (seq + 1 < a.seqs.b && __ldg(a.seqs.cu_q + seq + 1) <= tok) ++seq;
+    const SeqInfo x = seq_info(a.seqs, seq);
+    int sees = 0;
+    if (tok >= x.q0 && tok < x.q0 + x.sq) sees = a.causal ? min(x.sk, tok - x.q0 + x.sk - x.sq + 1) : x.sk;
+    const bool few = sees > 0 && sees <= kFewKeys;
+    const int most = __reduce_max_sync(0xffffffffu, few ? sees : 0);
+
+    float acc = dot8<D, BF16>(wo, wd);
 #pragma unroll
     for (int off = LPR / 2; off >= 1; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-    if (r < rows && sub == 0) {
-        const int64_t tok = r / a.h;
-        const int head = static_cast<int>(r - tok * a.h);
-        const int kh = head / a.group, j = head - kh * a.group;
-        a.ld[(static_cast<int64_t>(kh) * a.total_q + tok) * a.group + j] =
-            make_float2(a.lse[static_cast<int64_t>(head) * a.total_q + tok] * 1.4426950408889634f, acc);
+    if (most > 0) {
+        const uint16_t *qp = static_cast<const uint16_t *>(a.q) + static_cast<int64_t>(tok) * a.q_stride + head * D;
+        const uint16_t *kp = static_cast<const uint16_t *>(a.k) + x.k0 * a.k_stride + kh * D + sub * 8;
+        const uint16_t *vp = static_cast<const uint16_t *>(a.v) + x.k0 * a.v_stride + kh * D + sub * 8;
+        const uint4 wq = *reinterpret_cast<const uint4 *>(qp + sub * 8);
+        float sum = 0.f;
+        constexpr int U = 4;  // keys at a time: the loop is bound by the loads' latency
+#pragma unroll 1
+        for (int i0 = 0; i0 < most; i0 += U) {
+            uint4 wk[U], wv[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                wk[u] = wv[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (few && i0 + u < sees) {
+                    wk[u] = *reinterpret_cast<const uint4 *>(kp + (i0 + u) * a.k_stride);
+                    wv[u] = *reinterpret_cast<const uint4 *>(vp + (i0 + u) * a.v_stride);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float s = dot8<D, BF16>(wq, wk[u]), dp = dot8<D, BF16>(wd, wv[u]);
+#pragma unroll
+                for (int off = LPR / 2; off >= 1; off >>= 1) {
+                    s += __shfl_xor_sync(0xffffffffu, s, off);
+                    dp += __shfl_xor_sync(0xffffffffu, dp, off);
+                }
+                if (few && i0 + u < sees) sum = fmaf(fast_exp2(s * a.scale_log2 - lse2), dp, sum);
+            }
+        }
+        if (few) acc = sum;
     }
+    if (live && sub == 0)
+        a.ld[(static_cast<int64_t>(kh) * a.total_q + tok) * a.group + j] = make_float2(lse2, acc);
 }
 
 // Rows of a unit's last streamed tile that are the sequence's own, and
@@ -229,6 +316,7 @@ __device__ __forceinline__ void pbwd_stage(uint8_t *smem, uint32_t sbase, const 
     const int lane = threadIdx.x & 31;
     constexpr int CPR = G::ROW_BYTES / 16;
     int step = 0, zeroed = 0;
+    if (MODE == kModeDKV) griddep_wait();  // (LSE, D) are there
     UnitMsg x;
     for (int n = 0; take_unit<true>(&x, n, msgs, bar(G::BAR_MF), bar(G::BAR_ME), g, 17); ++n) {
         if constexpr (MODE == kModeDKV) {
@@ -240,7 +328,7 @@ __device__ __forceinline__ void pbwd_stage(uint8_t *smem, uint32_t sbase, const 
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = lane + 32 * i;
-                    v[i] = r < live ? __ldg(rows + static_cast<int64_t>(tok) * a.group + r)
+                    v[i] = r < live ? __ldcg(rows + static_cast<int64_t>(tok) * a.group + r)
                                     : make_float2(INFINITY, 0.f);
                 }
                 bool ok = await(bar(G::BAR_LDE + s), (((step + j) / kStages) & 1) ^ 1, g, 20);
@@ -453,28 +541,48 @@ __device__ __forceinline__ void pbwd_mma(uint32_t sbase, uint32_t tmem, const Un
 }
 
 // COLS columns of one fp32 TMEM row, scaled, as 16-bit values at dst, or as
-// they are at part (a cut unit's partial sum).
+// they are at part (a cut unit's partial sum). Rows lie far apart, so every
+// lane's store is a line of its own: 32-byte stores where dst allows them
+// (16-byte ones took 3,600 cycles per query tile at d = 128, half of a unit's
+// fixed cost).
 template <int COLS, bool BF16>
 __device__ __forceinline__ void store_acc(uint32_t taddr, float mul, uint16_t *dst, float *part, bool out,
                                           bool zero) {
+    constexpr int CH = COLS < 32 ? COLS : 32;
+    const bool al32 = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
 #pragma unroll 1
-    for (int c0 = 0; c0 < COLS; c0 += 16) {
-        uint32_t v[16];
-        tmem_ld16(taddr + c0, v);
+    for (int c0 = 0; c0 < COLS; c0 += CH) {
+        uint32_t v[CH];
+        if constexpr (CH == 32)
+            tmem_ld32(taddr + c0, *reinterpret_cast<uint32_t(*)[32]>(v));
+        else
+            tmem_ld16(taddr + c0, *reinterpret_cast<uint32_t(*)[16]>(v));
         tmem_wait_ld();
         if (!out) continue;
         if (part != nullptr) {
-            st_global_v8(part + c0, *reinterpret_cast<const uint32_t(*)[8]>(&v[0]));
-            st_global_v8(part + c0 + 8, *reinterpret_cast<const uint32_t(*)[8]>(&v[8]));
+#pragma unroll
+            for (int i = 0; i < CH / 8; ++i)
+                st_global_v8(part + c0 + 8 * i, *reinterpret_cast<const uint32_t(*)[8]>(&v[8 * i]));
             continue;
         }
-        uint32_t pk[8];
+        uint32_t pk[CH / 2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            pk[i] = zero ? 0u : pack2q<BF16>(__uint_as_float(v[2 * i]) * mul, __uint_as_float(v[2 * i + 1]) * mul);
-        uint4 *d4 = reinterpret_cast<uint4 *>(dst + c0);
-        d4[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        d4[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+        for (int i = 0; i < CH / 2; ++i) {
+            float lo, hi;
+            f2_split(f2_mul(f2_make(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2_make(mul, mul)),
+                     lo, hi);
+            pk[i] = zero ? 0u : pack2q<BF16>(lo, hi);
+        }
+        if (al32) {
+#pragma unroll
+            for (int i = 0; i < CH / 16; ++i)
+                st_global_v8(dst + c0 + 16 * i, *reinterpret_cast<const uint32_t(*)[8]>(&pk[8 * i]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < CH / 8; ++i)
+                reinterpret_cast<uint4 *>(dst + c0)[i] =
+                    make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        }
     }
 }
 
@@ -529,6 +637,7 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
     const int row_tok = (row * a.group_inv) >> 16, row_head = row - row_tok * a.group;
     volatile int *joiner = reinterpret_cast<volatile int *>(smem + G::OFF_MISC + 8);
     int step = 0, met = 0;
+    if (MODE == kModeDQ) griddep_wait();  // (LSE, D) are there
     for (int it_u = 0;; ++it_u) {
         const volatile UnitMsg *x = wait_unit(it_u, msgs, bar(G::BAR_MF), g, 17);
         if (x == nullptr) return;
@@ -542,7 +651,7 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
         int from = 0;  // (DKV) first query token that sees this key, from the unit's first step on
         if constexpr (MODE == kModeDQ) {
             if (out) {
-                const float2 v = __ldg(a.ld + (static_cast<int64_t>(x->head) * a.total_q + x->q0 + at) * a.group +
+                const float2 v = __ldcg(a.ld + (static_cast<int64_t>(x->head) * a.total_q + x->q0 + at) * a.group +
                                        row_head);
                 lse2 = v.x;
                 drow = v.y;
@@ -551,6 +660,7 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
         } else {
             from = a.causal ? at - (x->sk - x->sq) - x->step0 * a.tile_tokens : 0;
         }
+        const int own_keys = x->sk - x->step0 * G::BT;  // (DQ) from the unit's first step on
         const int rows_left = MODE == kModeDKV ? x->sq - x->step0 * a.tile_tokens : 0;  // tokens
         for (int j = 0; j < count; ++j, ++step) {
             const float *ldbuf = nullptr;
@@ -564,23 +674,38 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
             } else {
                 cmax = sees - j * G::BT;
             }
-            const bool masked = __any_sync(0xffffffffu, cmin > 0 || cmax < G::BT);
+            // 0: every place is the sequence's own and seen; 1: some are hidden by
+            // the causal mask; 2: some are not the sequence's own
+            int kind = __any_sync(0xffffffffu, cmin > 0 || cmax < G::BT) ? 1 : 0;
+            if (MODE == kModeDKV ? cmax < G::BT : own_keys - j * G::BT < G::BT) kind = 2;
+            kind = uniform(kind);
             const bool ok = await(bar(G::BAR_SF), step & 1, g, 13);
             if (!__all_sync(0xffffffffu, ok)) return;
             tc_fence_after();
             // a half: P from S, then dS from dP, columns [c0, c0 + 32)
-            auto half = [&](auto is_masked, int h) {
-                constexpr bool MASKED = decltype(is_masked)::value;
+            auto half = [&](auto kind_of, int h) {
+                constexpr int KIND = decltype(kind_of)::value;
                 const int c0 = h * G::HN + 32 * cg;
                 const uint32_t tS = tmem + lanes + G::T_S + c0, tP = tmem + lanes + G::T_P + c0;
                 const float4 *ld4 = reinterpret_cast<const float4 *>(ldbuf) + (c0 >> 2);
                 uint32_t sv[32], pv[32];
                 float *p = reinterpret_cast<float *>(sv);
+                // bit i: column c0 + i is seen
+                uint32_t seen = ~0u;
+                if constexpr (KIND != 0) {
+                    const int lo = min(max(cmin - c0, 0), 32), hi = min(max(cmax - c0, 0), 32);
+                    seen = static_cast<uint32_t>((1ull << hi) - (1ull << min(lo, hi)));
+                }
                 tmem_ld32(tS, sv);
                 tmem_wait_ld();
+                // hidden places get P = 0 by selection; dS = P (dP - D) is then 0
+                // too, unless what is there may be NaN (kind 2)
                 if constexpr (MODE == kModeDQ) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) p[i] = fast_exp2(p[i] * c - lse2);
+                    for (int i = 0; i < 32; ++i) {
+                        p[i] = fast_exp2(p[i] * c - lse2);
+                        if (KIND != 0) p[i] = (seen >> i & 1u) ? p[i] : 0.f;
+                    }
                 } else {
                     uint32_t pp[16];
 #pragma unroll
@@ -591,8 +716,7 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
                         for (int e = 0; e < 4; ++e) {
                             const int i = 4 * q + e;
                             p[i] = fast_exp2(p[i] * c - lv[e]);
-                            // (by selection: what a masked place holds may be NaN)
-                            if (MASKED) p[i] = c0 + i >= cmin && c0 + i < cmax ? p[i] : 0.f;
+                            if (KIND != 0) p[i] = (seen >> i & 1u) ? p[i] : 0.f;
                         }
                         pp[2 * q] = pack2q<BF16>(p[4 * q], p[4 * q + 1]);
                         pp[2 * q + 1] = pack2q<BF16>(p[4 * q + 2], p[4 * q + 3]);
@@ -621,7 +745,7 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
                     for (int e = 0; e < 4; ++e) {
                         const int i = 4 * q + e;
                         dr[e] = p[i] * (__uint_as_float(pv[i]) - dv[e]);
-                        if (MASKED) dr[e] = c0 + i >= cmin && c0 + i < cmax ? dr[e] : 0.f;
+                        if (KIND == 2) dr[e] = (seen >> i & 1u) ? dr[e] : 0.f;
                     }
                     pd[2 * q] = pack2q<BF16>(dr[0], dr[1]);
                     pd[2 * q + 1] = pack2q<BF16>(dr[2], dr[3]);
@@ -637,12 +761,16 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
                 return true;
             };
             bool done;
-            if (!masked) {
-                done = half(std::false_type{}, 0) && half(std::false_type{}, 1);
+            if (kind == 0) {
+                done = half(std::integral_constant<int, 0>{}, 0) && half(std::integral_constant<int, 0>{}, 1);
+            } else if (kind == 1) {
+                done = true;
+#pragma unroll 1
+                for (int h = 0; h < 2 && done; ++h) done = half(std::integral_constant<int, 1>{}, h);
             } else {
                 done = true;
 #pragma unroll 1
-                for (int h = 0; h < 2 && done; ++h) done = half(std::true_type{}, h);
+                for (int h = 0; h < 2 && done; ++h) done = half(std::integral_constant<int, 2>{}, h);
             }
             if (!done) return;
         }
@@ -685,7 +813,7 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
             __threadfence();
             if (!meet(bar(G::BAR_WG), met, g)) return;
             if (threadIdx.x == 128) {
-                *joiner = arrive_last(a.arrivals + (MODE == kModeDQ ? a.ctas_kv : 0) + x->first_part, a.call,
+                *joiner = arrive_last(a.arrivals + (MODE == kModeDQ ? gridDim.x : 0) + x->first_part, a.call,
                                       x->nparts);
                 __threadfence();
             }
@@ -723,6 +851,18 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
     }
 }
 
+// CTAs of the key-tile kind, of ctas in all. A key-tile step (four products)
+// takes 1.15 times a query-tile step (three); with the units' fixed costs,
+// short sequences have more of their time in query tiles (b16 s512 h32/8 d128:
+// XXX us with 80 of 152 for keys). Where every unit can have a CTA to itself,
+// each kind gets at least its units.
+__device__ __forceinline__ int key_ctas(const LineSum &q, const LineSum &kv, int ctas) {
+    const float wq = static_cast<float>(q.cost), wkv = 1.15f * static_cast<float>(kv.cost);
+    int n = static_cast<int>(__fdividef(static_cast<float>(ctas) * wkv, fmaxf(wq + wkv, 1.f)) + 0.5f);
+    if (q.units + kv.units <= ctas) n = min(max(n, kv.units), ctas - q.units);
+    return min(max(n, 1), ctas - 1);
+}
+
 template <int D, int MODE, bool BF16>
 __device__ __forceinline__ void pbwd_run(const CUtensorMap *tq, const CUtensorMap *tk, const CUtensorMap *tv,
                                          const CUtensorMap *tdo, uint8_t *smem, uint32_t sbase, uint32_t tmem,
@@ -739,7 +879,7 @@ __device__ __forceinline__ void pbwd_run(const CUtensorMap *tq, const CUtensorMa
     } else if (warp == 2) {
         pbwd_stage<D, MODE>(smem, sbase, msgs, a, g);
     } else if (warp == 3) {
-        const LineSum *sums = reinterpret_cast<const LineSum *>(smem + G::OFF_SUM);
+        const LineSum *sums = reinterpret_cast<const LineSum *>(smem + G::OFF_SUM) + MODE * (kPBwdThreads / 32);
         post_units<MODE == kModeDKV>(
             a.seqs, a.line[MODE], [&] { return line_total(sums, kPBwdThreads / 32); },
             reinterpret_cast<UnitMsg *>(smem + G::OFF_MSG), bar(G::BAR_MF), bar(G::BAR_ME), bar(G::BAR_MS), g, 18, cta,
@@ -763,8 +903,6 @@ __global__ void __launch_bounds__(kPBwdThreads, 1)
     const int warp = threadIdx.x >> 5;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + G::OFF_MISC);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + G::OFF_MISC + 4);
-    const bool keys = static_cast<int>(blockIdx.x) < a.ctas_kv;
-
     if (threadIdx.x == 0) {
         for (int i = 0; i < G::NUM_BARS; ++i) {
             uint32_t count = 1;
@@ -788,29 +926,32 @@ __global__ void __launch_bounds__(kPBwdThreads, 1)
     // query tiles of less than 128 rows: the rest of each ring slot is never
     // written by a copy, and read by the key-tile kind's products
     const int used = a.tile_tokens * a.group;
-    if (keys && used < G::BT) {
+    if (used < G::BT) {
         constexpr int CPR = G::ROW_BYTES / 16;
         const int per = (G::BT - used) * CPR;
+#pragma unroll 1
         for (int i = threadIdx.x; i < per * G::PANELS * G::SLOTS; i += kPBwdThreads) {
             const int panel = i / per;
             st_shared_zero16(sbase + G::OFF_RING + panel * G::PANEL_BYTES + used * G::ROW_BYTES + (i - panel * per) * 16);
         }
         fence_proxy_async_smem();
     }
+    // both kinds' work, and from it the CTAs that each gets
     LineSum *sums = reinterpret_cast<LineSum *>(smem + G::OFF_SUM);
-    if (keys)
-        line_sum_warps<1>(a.seqs, a.line[kModeDKV], sums);
-    else
-        line_sum_warps<0>(a.seqs, a.line[kModeDQ], sums);
+    line_sum_warps<0>(a.seqs, a.line[kModeDQ], sums);
+    line_sum_warps<1>(a.seqs, a.line[kModeDKV], sums + kPBwdThreads / 32);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uniform(*tmem_slot);
     const WaitGuard g{abort_flag, a.status, kKernBwd};
-    if (keys)
-        pbwd_run<D, kModeDKV, BF16>(&tq, &tk, &tv, &tdo, smem, sbase, tmem, blockIdx.x, a.ctas_kv, a, g);
+    const int ctas_kv = key_ctas(line_total(sums, kPBwdThreads / 32),
+                                 line_total(sums + kPBwdThreads / 32, kPBwdThreads / 32), gridDim.x);
+    if (static_cast<int>(blockIdx.x) < ctas_kv)
+        pbwd_run<D, kModeDKV, BF16>(&tq, &tk, &tv, &tdo, smem, sbase, tmem, blockIdx.x, ctas_kv, a, g);
     else
-        pbwd_run<D, kModeDQ, BF16>(&tq, &tk, &tv, &tdo, smem, sbase, tmem, blockIdx.x - a.ctas_kv, a.ctas_q, a, g);
+        pbwd_run<D, kModeDQ, BF16>(&tq, &tk, &tv, &tdo, smem, sbase, tmem, blockIdx.x - ctas_kv,
+                                   gridDim.x - ctas_kv, a, g);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -831,15 +972,27 @@ cudaError_t launch_bwd_packed_t(const CUtensorMap &tq, const CUtensorMap &tk, co
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    constexpr int RPW = 32 / (D / 8);
-    const int64_t rows = static_cast<int64_t>(a.total_q) * a.h;
-    const int64_t blocks = (rows + 8 * RPW - 1) / (8 * RPW);
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    bwd_prep_kernel<D, BF16><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
+    const PrepGeom<D> geom = prep_geom<D>(a.h);
+    const dim3 grid((a.total_q + geom.tokens - 1) / geom.tokens, (a.h + geom.heads - 1) / geom.heads);
+    bwd_prep_kernel<D, BF16><<<grid, 256, 0, stream>>>(a, geom);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    bwd_pack_kernel<D, BF16><<<static_cast<unsigned>(a.ctas_kv + a.ctas_q), kPBwdThreads, G::SMEM_BYTES, stream>>>(
-        tq, tk, tv, tdo, a);
-    return cudaGetLastError();
+    // A short batch's main kernel starts while the first one runs: its set-up
+    // and first copies need nothing from it (5 sequences of up to 301 tokens,
+    // h16 d64, forward and backward: 47 -> 39 us). A long one's CTAs would be
+    // placed as SMs come free, neighbours on the work line far apart (b1 s8192
+    // h32/8 d128: 1550 -> 1759 us), so it waits.
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    const bool early = static_cast<int64_t>(a.total_q) * a.h * D <= (2 << 20);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
+    cfg.blockDim = dim3(kPBwdThreads);
+    cfg.dynamicSmemBytes = G::SMEM_BYTES;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, bwd_pack_kernel<D, BF16>, tq, tk, tv, tdo, a);
 }
 
 }  // namespace

@@ -869,11 +869,11 @@ __global__ void __launch_bounds__(kPackThreads, 1)
         tmem_alloc(smem_u32(tmem_slot), G::TMEM_COLS);
         tmem_relinquish();
     }
-    line_sum_warps<0>(a.seqs, a.line, sums);
+    if (a.seqs.b > 32) line_sum_warps<0>(a.seqs, a.line, sums);  // (fewer: post_units does it alone)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = uniform(*tmem_slot);
+    const uint32_t tmem = *tmem_slot;
     const WaitGuard g{abort_flag, a.status, kKernFwd};
 
     if (warp < 4) {

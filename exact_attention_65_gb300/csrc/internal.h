@@ -254,18 +254,22 @@ cudaError_t launch_chunk_paged(int d, bool bf16, const CUtensorMap &tq, const CU
 struct PackBwdArgs {
     SeqArrays seqs;
     LineShape line[2];
+    const void *q, *k, *v;  // rows q_stride, k_stride, v_stride elements apart
+    int64_t q_stride, k_stride, v_stride;
     const void *o, *dout;  // [total_q, h, d]
     const float *lse;      // [h, total_q]
     float2 *ld;            // workspace [h_kv, total_q, group]: (LSE log2 e, D)
     void *dq, *dk, *dv;
     int64_t dq_stride, dk_stride, dv_stride;  // elements from one token's row to the next
     int h, group, group_inv, tile_tokens, total_q, causal;
+    uint32_t group_mul;  // head / group = head * group_mul >> group_div
+    int group_div;
     float scale, scale_log2;
     uint32_t *status;
     uint32_t flags;
-    int ctas_q, ctas_kv;
-    // cut units: fp32 sums [ctas, 2, accumulators, 128, d], and a counter per
-    // CTA (key-tile CTAs first), valid for call number `call`
+    int ctas;
+    // cut units of each kind: fp32 sums [ctas, 2, accumulators, 128, d], and a
+    // counter per CTA (key tiles first), valid for call number `call`
     float *part[2];
     uint32_t *arrivals;
     uint32_t call;

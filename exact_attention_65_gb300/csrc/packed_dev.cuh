@@ -94,12 +94,10 @@ __device__ __forceinline__ void known_shape(LineShape *s) {
     }
 }
 
-// The line's sums of more than 32 sequences: every thread of the block adds
-// some, warp sums go to `sums` (one LineSum per warp) for line_total() after a
-// barrier. (Up to 32 the posting warp sums by itself.)
+// The line's sums: every thread of the block adds some sequences, warp sums go
+// to `sums` (one LineSum per warp) for line_total() after a barrier.
 template <int BY_KEY>
 __device__ __forceinline__ void line_sum_warps(const SeqArrays &s, LineShape shape, LineSum *sums) {
-    if (s.b <= 32) return;
     known_shape<BY_KEY>(&shape);
     LineSum t{0, 0, 0};
 #pragma unroll 1

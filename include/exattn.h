@@ -293,7 +293,7 @@ attn_status_t attn_fwd_packed(const void *q, const void *k, const void *v, const
  * Rows of sequences are written in full (a row without a key gets dq = 0, a
  * key that no row sees dk = dv = 0), rows of no sequence not at all. No
  * atomics add into the results: the same call gives the same bits.
- * Workspace (8 h total_q bytes, and fp32 partial sums of at most 32 MB) as
+ * Workspace (8 h total_q bytes, and fp32 partial sums of at most 60 MB) as
  * attn_fwd_packed's. Errors as attn_fwd.
  */
 attn_status_t attn_bwd_packed(const void *q, const void *k, const void *v, const void *o,
