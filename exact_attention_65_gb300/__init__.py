@@ -475,7 +475,7 @@ def attn_fwd_packed(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int = 0,
     lib = _lib or load_library()
     rc = _call(lib.attn_fwd_packed, idx, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), out.data_ptr(), lse.data_ptr(), b, t, tk,
-               max_seqlen_q, h, hk, d, qs, ks, vs, 1.0 / math.sqrt(d) if scale is None else scale,
+               max_seqlen_q, h, hk, d, qs, ks, vs, 1.0 / math.sqrt(d) if scale is None else float(scale),
                1 if causal else 0, dt)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_fwd_packed")
@@ -509,7 +509,7 @@ def attn_bwd_packed(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, scale: fl
     rc = _call(lib.attn_bwd_packed, idx, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                lse.data_ptr(), dout.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(),
                grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(), b, t, tk, h, hk, d, qs, ks, vs,
-               *strides, 1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0, dt)
+               *strides, 1.0 / math.sqrt(d) if scale is None else float(scale), 1 if causal else 0, dt)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_bwd_packed")
     return tuple(grads)
@@ -558,7 +558,7 @@ def attn_chunk_paged(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens_k, 
     rc = _call(lib.attn_chunk_paged, idx, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                block_table.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), out.data_ptr(),
                lse.data_ptr(), b, t, max_seqlen_q, h, hk, d, num_pages, page_size, max_pages, qs,
-               1.0 / math.sqrt(d) if scale is None else scale, 1 if causal else 0, dt)
+               1.0 / math.sqrt(d) if scale is None else float(scale), 1 if causal else 0, dt)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_chunk_paged")
     return out, lse

@@ -143,7 +143,11 @@ attn_status_t get_workspace(int dev, cudaStream_t stream, int n, size_t part_byt
     if (e == nullptr) {
         PackWs x;
         x.stream = stream;
-        g_ws[dev].push_back(x);
+        try {
+            g_ws[dev].push_back(x);
+        } catch (...) {  // no exception leaves the library
+            return ATTN_ERR_NO_MEMORY;
+        }
         e = &g_ws[dev].back();
     }
     if (e->n_arrivals < n) {
@@ -283,8 +287,13 @@ int attn_debug_packed_plan(const int *seqlens_q, const int *seqlens_k, int b, in
     if (!seqlens_q || !seqlens_k || !out || b < 1 || h < 1 || h_kv < 1 || h % h_kv != 0 || h / h_kv > 128 ||
         ctas < 1 || max_ranges < 1)
         return -1;
-    for (int i = 0; i < b; ++i)
+    int64_t all_q = 0, all_k = 0;
+    for (int i = 0; i < b; ++i) {
         if (seqlens_q[i] < 0 || seqlens_k[i] < 0) return -1;
+        all_q += seqlens_q[i];
+        all_k += seqlens_k[i];
+    }
+    if (all_q > kMaxRows || all_k > kMaxRows) return -1;
     LineBound bound{b, 0, 0, 0};
     for (int i = 0; i < b; ++i) {
         bound.total_q += seqlens_q[i];
@@ -571,7 +580,7 @@ attn_status_t attn_paged_write(const void *k, const void *v, const int64_t *slot
     a.k_pages = static_cast<uint4 *>(k_pages);
     a.v_pages = static_cast<uint4 *>(v_pages);
     a.tokens = tokens;
-    a.words = row / 8;
+    a.words = static_cast<int>(row / 8);
     a.k_stride = k_stride / 8;
     a.v_stride = v_stride / 8;
     a.slots = static_cast<int64_t>(num_pages) * page_size;

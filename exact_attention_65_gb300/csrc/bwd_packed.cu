@@ -28,6 +28,12 @@
 // the 16-row slice that holds the last row, and warp 2 zeroes what is left of
 // that slice in the streamed tile.
 //
+// What bounds it: the chain of a step (S and dP products, P and dS, the sums),
+// which the tensor pipe and the elementwise warps share in turns: about 3,700
+// cycles per key-tile step and 3,300 per query-tile step at d = 128, against
+// 2,048 and 1,536 of products (b1 s8192 h32/8 d128: 2962 us, 928 TFLOP/s on the
+// five products of the chain rule; causal 1540 us, 893 TFLOP/s).
+//
 // Roles (384 threads): warp 0 TMA producer, warp 1 MMA issuer, warp 2 stages
 // the steps' (LSE, D) and zeroes tails, warp 3 deals out units, warps 4-11
 // elementwise work and epilogue (one TMEM lane per thread, two groups that
@@ -853,9 +859,9 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
 
 // CTAs of the key-tile kind, of ctas in all. A key-tile step (four products)
 // takes 1.15 times a query-tile step (three); with the units' fixed costs,
-// short sequences have more of their time in query tiles (b16 s512 h32/8 d128:
-// XXX us with 80 of 152 for keys). Where every unit can have a CTA to itself,
-// each kind gets at least its units.
+// short sequences have more of their time in query tiles (b1 s8192 h32/8 d128
+// causal: 1581 us with 80 of 152 for keys whatever the lengths, 1542 so).
+// Where every unit can have a CTA to itself, each kind gets at least its units.
 __device__ __forceinline__ int key_ctas(const LineSum &q, const LineSum &kv, int ctas) {
     const float wq = static_cast<float>(q.cost), wkv = 1.15f * static_cast<float>(kv.cost);
     int n = static_cast<int>(__fdividef(static_cast<float>(ctas) * wkv, fmaxf(wq + wkv, 1.f)) + 0.5f);

@@ -12,28 +12,34 @@
 // new token fills g rows instead of one, and the causal staircase of a tile
 // is g times flatter. Nothing is padded to a head count.
 //
-// Units and CTAs: a unit is two such tiles (one in the ONE form) of a
-// sequence and K/V head against its keys in steps of 128. Sequence lengths
-// live on the device, so every CTA works its part of the call out for itself
-// (packed_sched.h): equal shares of the total work, cut inside a unit where
-// that is needed. A cut unit's ranges leave normalised fp32 O_i and LSE_i
-// (log2) in the workspace; the range that finishes last joins them in the
-// order of the keys, so the result does not depend on who that is.
+// Units and CTAs: a unit is two such tiles (one in the ONE form, which runs
+// where no sequence has more rows than a tile) of a sequence and K/V head
+// against its keys in steps of 128. Sequence lengths live on the device, so
+// every CTA works its part of the call out for itself (packed_sched.h): equal
+// shares of the total work, cut inside a unit where that is needed. A cut
+// unit's ranges leave normalised fp32 O_i and LSE_i (log2) in the workspace;
+// the range that finishes last joins them in the order of the keys, so the
+// result does not depend on who that is.
 //
 // Roles (384 threads, one CTA per SM): warp 0 TMA producer (a whole warp for
-// pages, one box per lane), warps 1 and 2 issue the MMAs of tile 0 and 1, warp
-// 3 deals out units, warps 4-7 and 8-11 softmax and epilogue of tile 0 and 1.
-// An issuer waits, counts and issues for about 1,300 cycles per step, the
-// tensor pipe's own time for its tile; with one thread for both tiles the pipe
-// stood still a third of the time (b1 s8192 h32 d128: 888 us, now XXX).
+// pages, one box per lane; with V by warp 2 in the ONE form), warps 1 and 2
+// issue the MMAs of tile 0 and 1, warp 3 deals out units, warps 4-7 and 8-11
+// softmax and epilogue of tile 0 and 1. The two issuers take turns: with one
+// thread for both tiles the tensor pipe stood still while it waited and
+// counted (b1 s8192 h32 d128, no mask: 888 us, now 754).
 //
 // V rows of a unit's last tile that lie past the sequence belong to the next
 // sequence or are stale; P is 0 there, and 0 * NaN is NaN: the issuers zero
 // those below the next multiple of 16, where the P V product stops.
 //
-// What bounds it: long prompts, the tensor pipe and the exponentials; single
-// tokens, HBM (each SM keeps the ring, 160 to 192 KB at d = 128, in flight);
-// short calls, the chain launch, lengths, Q, K, S, P, O.
+// What bounds it: long prompts, the tensor pipe, whose products take about 100
+// cycles instead of 64 while the softmax warps read and write TMEM (b2 s8192
+// h32/8 d128 causal: 780 us, 1390 TFLOP/s, 73% of the measured peak); single
+// tokens, HBM and the chain S, softmax, P V of one row tile (64 requests of up
+// to 8192 keys, h32/8, 16-key pages: 164 us, 5.7 TB/s, 84%); batches of short
+// sequences, the change from one unit to the next (about 4.5 us: the epilogue,
+// and code that the instruction cache no longer holds; 16 prompts of 64 to
+// 1500 tokens: 141 us, 750 TFLOP/s).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -298,7 +298,9 @@ struct WriteArgs {
     const uint4 *k, *v;          // rows of `words` 16-byte words, k_stride / v_stride words apart
     const int64_t *slot_map;     // [tokens]
     uint4 *k_pages, *v_pages;    // [slots, words]
-    int64_t tokens, words, k_stride, v_stride, slots;
+    int64_t tokens, k_stride, v_stride, slots;
+    int words, step_words;  // words of a row; of the step from one of a thread's words to the next,
+    int64_t step_tokens;    //   with its tokens (set by the launch)
 };
 cudaError_t launch_paged_write(const WriteArgs &a, cudaStream_t stream);
 

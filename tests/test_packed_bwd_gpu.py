@@ -174,3 +174,59 @@ def test_skipped_loads_time_out_and_recover(gpu):
     again = gpu.attn_bwd_packed(*args, causal=True)
     assert gpu.attn_get_device_status() == gpu.ATTN_OK
     assert all(torch.equal(x, y) for x, y in zip(first, again))
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("lens", [[1] * 60, [1] * 60 + [2], [2, 3, 9, 17]])
+def test_rows_of_few_keys(gpu, oracle_mod, lens, causal):
+    """A row with one key has dS = 0: rounding O must not leave noise in dQ and dK."""
+    q, k, v = make(lens, lens, 4, 2, 64, torch.bfloat16, 41)
+    cu = starts(lens)
+    n = int(cu[-1])
+    dout = torch.randn((n, 4, 64), generator=torch.Generator().manual_seed(5)).bfloat16()
+    dev = [x.cuda() for x in (q, k, v)]
+    o, lse = gpu.attn_fwd_packed(*dev, ints(cu), ints(cu), causal=causal)
+    grads = gpu.attn_bwd_packed(*dev, o, lse, dout.cuda(), ints(cu), ints(cu), causal=causal)
+    assert gpu.attn_get_device_status() == gpu.ATTN_OK
+    refs = oracle_mod.packed_attention_backward(q, k, v, dout, cu, cu, 0.125, causal)
+    # one key: P = 1, dP = D; P is off by f (the LSE's bound) and D by f |dO| |V|
+    f = fp32_slack(q, k, 0.125, 64)
+    one = np.repeat([m == 1 for m in lens], lens)
+    size = (dout.abs().double().numpy() * np.repeat(v.abs().double().numpy(), 2, axis=1)).sum(-1).max()
+    for x, like in zip(grads[:2], (k, q)):
+        noise = np.abs(x.double().cpu().numpy()[one]).max(initial=0.0)
+        assert noise <= 2 * 0.125 * 3 * f * size * float(like.abs().max())
+    for x, r in zip(grads, refs):
+        r = r[~one]
+        if r.size and np.linalg.norm(r) > 0:
+            got = x.double().cpu().numpy()[~one]
+            assert np.linalg.norm(got - r) <= 3 * 2.0 ** -8 * np.linalg.norm(r)
+
+
+def test_binding_refuses(gpu):
+    q = torch.zeros(8, 4, 64, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(8, 2, 64, dtype=torch.bfloat16, device="cuda")
+    cu = ints([0, 8])
+    o, lse = gpu.attn_fwd_packed(q, k, k, cu, cu)
+    bad = [
+        dict(k=k.half()), dict(k=k[:, :, :32]), dict(v=k[:4]), dict(cu_seqlens_q=cu.long()),
+        dict(cu_seqlens_k=ints([0, 4, 8])), dict(q=q.transpose(0, 1)), dict(q=q[0]), dict(k=k.expand(8, 2, 64)[:, :1]),
+        dict(out=o[:4]), dict(lse=lse.half()), dict(out=torch.zeros(8, 4, 128, device="cuda").bfloat16()[:, :, ::2]),
+    ]
+    for kw in bad:
+        args = dict(dict(q=q, k=k, v=k, cu_seqlens_q=cu, cu_seqlens_k=cu), **kw)
+        if kw.keys() == {"k"} and args["k"].shape[1] == 1:
+            args["v"] = k  # shapes differ
+        with pytest.raises((ValueError, TypeError)):
+            gpu.attn_fwd_packed(**args)
+    for kw in (dict(dout=q[:4]), dict(dout=torch.zeros(8, 4, 128, device="cuda").bfloat16()[:, :, ::2]),
+               dict(dq=k), dict(dk=k.half()), dict(o=None), dict(lse=None)):
+        args = dict(dict(q=q, k=k, v=k, o=o, lse=lse, dout=q, cu_seqlens_q=cu, cu_seqlens_k=cu), **kw)
+        with pytest.raises((ValueError, TypeError)):
+            gpu.attn_bwd_packed(**args)
+    # heads that do not divide, and too many for one K/V head
+    with pytest.raises(ValueError):
+        gpu.attn_fwd_packed(q[:, :3].contiguous(), k, k, cu, cu)
+    many = torch.zeros(8, 129, 16, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(gpu.AttnError):
+        gpu.attn_fwd_packed(many, many[:, :1].contiguous(), many[:, :1].contiguous(), cu, cu)
