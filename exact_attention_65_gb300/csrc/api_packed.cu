@@ -32,9 +32,12 @@ void fit_line(LineShape *s, const LineBound &x) {
 }  // namespace
 
 // Where the forward's work is cut (packed_sched.h). A unit's fixed cost (Q,
-// first S, epilogue) counts as one step of 128 keys; units are cut only
-// where each CTA's share is at least four steps, and two steps away from
-// their ends, as joining a cut unit costs about as much as two steps.
+// first S, epilogue) counts as two steps of 128 keys (one: b2 s8192 h32/8 d128
+// 783 us, two: 740). Joining a cut unit costs as much as several steps of two
+// tiles, so these are cut only where a CTA's share is 16 steps, six away from
+// a unit's ends (16 prompts of 64 to 1500 tokens: 145 us with 4 and 2, 132
+// with 16 and 6); units of one tile, where a long cache has to be spread over
+// many CTAs and few rows are joined, from 4 steps on, two from the ends.
 LineShape pack_line(int heads, int group, bool one_tile, bool causal, const LineBound &bound) {
     LineShape s;
     s.heads = heads;
@@ -44,18 +47,16 @@ LineShape pack_line(int heads, int group, bool one_tile, bool causal, const Line
     s.by_key = 0;
     s.weight = 1;
     s.shift = 7;
-    s.unit_cost = 1;
-    s.min_steps = 2;
-    s.min_part = 4;
+    s.unit_cost = 2;
+    s.min_steps = one_tile ? 2 : 6;
+    s.min_part = one_tile ? 4 : 16;
     fit_line(&s, bound);
     return s;
 }
 
 // The backward's query-tile units: one tile against steps of 128 keys.
 LineShape bwd_query_line(int heads, int group, bool causal, const LineBound &bound) {
-    LineShape s = pack_line(heads, group, true, causal, bound);
-    s.unit_cost *= 2;
-    return s;
+    return pack_line(heads, group, true, causal, bound);
 }
 
 // Its key-tile units: 128 keys against tiles of query tokens, whose heads
