@@ -23,7 +23,7 @@
 //
 // Roles (384 threads, one CTA per SM): warp 0 TMA producer (a whole warp for
 // pages, one box per lane; with V by warp 2 in the ONE form), warps 1 and 2
-// issue the MMAs of tile 0 and 1, warp 3 deals out units, warps 4-7 and 8-11
+// issue the MMAs of tile 0 and 1 (ONE: warp 1 S, warp 8 P V), warp 3 deals out units, warps 4-7 and 8-11
 // softmax and epilogue of tile 0 and 1. The two issuers take turns: with one
 // thread for both tiles the tensor pipe stood still while it waited and
 // counted (b1 s8192 h32 d128, no mask: 888 us, now 754).
@@ -34,12 +34,12 @@
 //
 // What bounds it: long prompts, the tensor pipe, whose products take about 100
 // cycles instead of 64 while the softmax warps read and write TMEM (b2 s8192
-// h32/8 d128 causal: 780 us, 1390 TFLOP/s, 73% of the measured peak); single
-// tokens, HBM and the chain S, softmax, P V of one row tile (64 requests of up
-// to 8192 keys, h32/8, 16-key pages: 164 us, 5.7 TB/s, 84%); batches of short
+// h32/8 d128 causal: 745 us, 1460 TFLOP/s, 77% of the measured peak); single
+// tokens, HBM and the change from unit to unit (64 requests of up
+// to 8192 keys, h32/8, 16-key pages: 158 us, 5.9 TB/s, 87%); batches of short
 // sequences, the change from one unit to the next (about 4.5 us: the epilogue,
 // and code that the instruction cache no longer holds; 16 prompts of 64 to
-// 1500 tokens: 141 us, 750 TFLOP/s).
+// 1500 tokens: 129 us, 820 TFLOP/s).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -87,12 +87,12 @@ struct PackGeom {
     static constexpr int BAR_KVE = BAR_KVF + SLOTS;
     static constexpr int BAR_SF = BAR_KVE + SLOTS;  // [2] S made (ONE: of even, odd steps)
     static constexpr int BAR_PF = BAR_SF + 2;       // [2] P stored
-    static constexpr int BAR_OF = BAR_PF + 2;       // [2] O complete (ONE: [1] every P V done)
+    static constexpr int BAR_OF = BAR_PF + 2;       // [2] O complete
     static constexpr int BAR_OE = BAR_OF + 2;       // [2] O read out
-    static constexpr int BAR_PVD = BAR_OF + 1;
     static constexpr int BAR_DONE = BAR_OE + 2;
     static constexpr int BAR_TURN = BAR_DONE + 2;  // [2] the tile's issuer may issue
-    static constexpr int BAR_MF = BAR_TURN + 2;    // [kMsgSlots] unit message posted
+    static constexpr int BAR_PVD = BAR_TURN + 2;  // ONE: [2] P V of an even, an odd step done
+    static constexpr int BAR_MF = BAR_PVD + 2;     // [kMsgSlots] unit message posted
     static constexpr int BAR_ME = BAR_MF + kMsgSlots;
     static constexpr int BAR_MS = BAR_ME + kMsgSlots;  // [kMsgSlots] who shares a cut unit
     static constexpr int BAR_WG = BAR_MS + kMsgSlots;  // [2] a tile's softmax warps meet (cut units)
@@ -256,39 +256,44 @@ __device__ __forceinline__ void pack_producer(const CUtensorMap *tq, const CUten
     }
 }
 
-// The MMAs of tile t (ONE: of the only tile). A whole warp: lane 0 issues, all
-// lanes zero the V tail.
+// The products of a tile and the zeroing of its V tail, as the issuers use
+// them: one lane issues, a whole warp zeroes.
 template <int D, bool BF16, bool ONE>
-__device__ __forceinline__ void pack_issue(uint32_t sbase, uint32_t tmem, const UnitMsg *msgs, int t,
-                                           const PackArgs &a, const WaitGuard &g) {
+struct TileMma {
     using G = PackGeom<D, ONE>;
-    auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
-    const int lane = threadIdx.x & 31;
-    // with a negative scale the S MMAs negate Q, so that the softmax always
-    // works with a scale >= 0
-    const uint32_t idesc_s =
-        mma_idesc_f16(G::BM, G::BN, BF16, false, false) | (a.scale_log2 < 0.f ? kNegateA : 0u);
-    constexpr uint32_t idesc_o = mma_idesc_f16(G::BM, D, BF16, false, true);
-    const uint64_t dq = smem_desc(sbase + G::OFF_Q + t * G::TILE_BYTES, 16, G::SBO, G::LAYOUT);  // K-major
-    const uint64_t dk = smem_desc(sbase + G::OFF_KV, 16, G::SBO, G::LAYOUT);                     // K-major
-    const uint64_t dv = smem_desc(sbase + G::OFF_KV, G::PANEL_BYTES, G::SBO, G::LAYOUT);         // MN-major
-    constexpr uint32_t tile16 = G::TILE_BYTES >> 4;
+    uint32_t sbase, idesc_s;
+    uint64_t dq, dk, dv;
+    static constexpr uint32_t idesc_o = mma_idesc_f16(G::BM, D, BF16, false, true);
+    static constexpr uint32_t tile16 = G::TILE_BYTES >> 4;
+    static_assert(G::PANELS <= 2, "panels of a tile");
 
-    // S = Q_t K^T, 16 head-dim elements per instruction
-    auto issue_s = [&](uint32_t tS, uint64_t qdesc, uint64_t kdesc) {
+    __device__ __forceinline__ TileMma(uint32_t base, int t, const PackArgs &a) {
+        sbase = base;
+        // with a negative scale the S MMAs negate Q, so that the softmax always
+        // works with a scale >= 0
+        idesc_s = mma_idesc_f16(G::BM, G::BN, BF16, false, false) | (a.scale_log2 < 0.f ? kNegateA : 0u);
+        dq = smem_desc(base + G::OFF_Q + t * G::TILE_BYTES, 16, G::SBO, G::LAYOUT);  // K-major
+        dk = smem_desc(base + G::OFF_KV, 16, G::SBO, G::LAYOUT);                     // K-major
+        dv = smem_desc(base + G::OFF_KV, G::PANEL_BYTES, G::SBO, G::LAYOUT);         // MN-major
+    }
+    // S = Q K^T of Q buffer qbuf and ring slot `slot`, 16 head-dim elements per
+    // instruction; turn: the barrier of the other tile's turn, which passes
+    // while the last quarter is still to be queued (0: none)
+    __device__ __forceinline__ void s(uint32_t tS, int qbuf, int slot, uint32_t turn) const {
+        const uint64_t qdesc = dq + ((qbuf * G::Q_BUF_BYTES) >> 4), kdesc = dk + slot * tile16;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
             const int p = (kk * 16) / G::PANEL_ELEMS;
             const int off = ((kk * 16) % G::PANEL_ELEMS) * 2;
             const uint32_t o16 = (p * G::PANEL_BYTES + off) >> 4;
-            // the turn passes while the last quarter is still to be queued
-            if (!ONE && kk == D / 16 * 3 / 4) mbar_arrive(bar(G::BAR_TURN + (t ^ 1)));
+            if (!ONE && kk == D / 16 * 3 / 4) mbar_arrive(turn);
             mma_ss(tS, qdesc + o16, kdesc + o16, idesc_s, kk > 0 ? 1u : 0u);
         }
-    };
+    }
     // O (+)= P V over the first `keys` keys of the tile, 16 per instruction
     // (whole tiles without a condition per product)
-    auto issue_pv = [&](uint32_t tO, uint32_t tP, uint64_t vdesc, int keys, bool first) {
+    __device__ __forceinline__ void pv(uint32_t tO, uint32_t tP, int slot, int keys, bool first) const {
+        const uint64_t vdesc = dv + slot * tile16;
         if (keys == G::BN) {
 #pragma unroll
             for (int kk = 0; kk < G::BN / 16; ++kk)
@@ -300,26 +305,137 @@ __device__ __forceinline__ void pack_issue(uint32_t sbase, uint32_t tmem, const 
                 mma_ts(tO, tP + kk * 8, vdesc + ((kk * 16 * G::ROW_BYTES) >> 4), idesc_o,
                        (!first || kk > 0) ? 1u : 0u);
         }
-    };
+    }
     // zeros into the rows of a landed V tile from `keys` up to a multiple of 16
-    auto zero_tail = [&](int slot, int keys) {
+    __device__ __forceinline__ void zero_tail(int slot, int keys) const {
         constexpr int CPR = G::ROW_BYTES / 16;
         const int per_panel = (((keys + 15) & ~15) - keys) * CPR;
         const uint32_t base = sbase + G::OFF_KV + slot * G::TILE_BYTES + keys * G::ROW_BYTES;
 #pragma unroll 1
-        for (int c = lane; c < per_panel * G::PANELS; c += 32) {
+        for (int c = threadIdx.x & 31; c < per_panel * G::PANELS; c += 32) {
             const int p = c >= per_panel ? 1 : 0;
             st_shared_zero16(base + p * G::PANEL_BYTES + (c - p * per_panel) * 16);
         }
         fence_proxy_async_smem();
         __syncwarp();
-    };
-    static_assert(G::PANELS <= 2, "panels of a tile");
+    }
+    // No MMA of the calling warp may still be running when TMEM is released.
+    __device__ __forceinline__ void finish(int bar, const WaitGuard &g) const {
+        const uint32_t b = sbase + G::OFF_BAR + 8u * bar;
+        if (elect_one()) mma_commit(b);
+        WaitGuard drain = g;
+        uint32_t no_abort = 0;
+        drain.abort = &no_abort;
+        await(b, 0, drain, 12);
+    }
+};
 
+// The ONE form's two issuers, a warp each: S of step j goes to the S columns
+// of tile (j & 1) once the P V product that read them last is done, so S_{j+1}
+// is made while the softmax works on S_j. One thread for both kinds took 2,350
+// cycles per step for its waiting, counting and issuing. K tiles lie in the
+// ring's even slots and V tiles in the odd ones (SLOTS is even), so each slot's
+// barriers are seen in order by the warp that waits on them.
+template <int D, bool BF16>
+__device__ __forceinline__ void issue_one_s(uint32_t sbase, uint32_t tmem, const UnitMsg *msgs, const PackArgs &a,
+                                            const WaitGuard &g) {
+    using G = PackGeom<D, true>;
+    static_assert(G::SLOTS % 2 == 0, "K and V in slots of their own");
+    auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
+    const TileMma<D, BF16, true> mma(sbase, 0, a);
+    Ring<G::SLOTS> ring;
+    int qbuf = 0;
+    uint32_t q_phase = 0, used = 0;  // bit i of used: phase of the uses of S columns i
+    bool ok = true;
+    UnitMsg x;
+#pragma unroll 1
+    for (int n = 0; ok && take_unit<true>(&x, n, msgs, bar(G::BAR_MF), bar(G::BAR_ME), g, 17); ++n) {
+        ok = await(bar(G::BAR_QF + qbuf), q_phase, g, 4);
+#pragma unroll 1
+        for (int j = 0; ok && j < x.nstep; ++j) {
+            const int c = j & 1;
+            ok = await(bar(G::BAR_PVD + c), (used >> c & 1u) ^ 1u, g, 22);
+            ok = ok && await(bar(G::BAR_KVF + ring.slot), ring.phase, g, 5);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            used ^= 1u << c;
+            tc_fence_after();
+            const int ks = uniform(ring.slot), qs = uniform(qbuf);
+            if (elect_one()) {
+                mma.s(tmem + c * G::TMEM_TILE_STRIDE, qs, ks, 0);
+                mma_commit(bar(G::BAR_SF + c));
+                mma_commit(bar(G::BAR_KVE + ks));
+            }
+            ring.next();
+            ring.next();
+        }
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (elect_one()) mma_commit(bar(G::BAR_QE + qbuf));
+        if (++qbuf == G::QBUF) {
+            qbuf = 0;
+            q_phase ^= 1u;
+        }
+    }
+    mma.finish(G::BAR_DONE, g);
+}
+
+template <int D, bool BF16>
+__device__ __forceinline__ void issue_one_pv(uint32_t sbase, uint32_t tmem, const UnitMsg *msgs, const PackArgs &a,
+                                             const WaitGuard &g) {
+    using G = PackGeom<D, true>;
+    auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
+    const TileMma<D, BF16, true> mma(sbase, 0, a);
+    const uint32_t tO = tmem + G::TMEM_O_OFF;
+    Ring<G::SLOTS> ring;
+    ring.next();               // V_0
+    uint32_t p_phase = 0;      // bit 0 and 1: P of even and odd steps
+    uint32_t o_phase = 0;      // O handed back
+    bool ok = true;
+    UnitMsg x;
+#pragma unroll 1
+    for (int n = 0; ok && take_unit<true>(&x, n, msgs, bar(G::BAR_MF), bar(G::BAR_ME), g, 17); ++n) {
+        const int nkv = x.nstep;
+        // O is overwritten: the last unit's must have been read out (also where
+        // there is no key to see: O's barrier must not run two phases ahead)
+        ok = await(bar(G::BAR_OE), o_phase ^ 1u, g, 7);
+        o_phase ^= 1u;
+#pragma unroll 1
+        for (int j = 0; ok && j < nkv; ++j) {
+            const int keys = min(G::BN, x.sk - (x.step0 + j) * G::BN);
+            ok = await(bar(G::BAR_KVF + ring.slot), ring.phase, g, 6);
+            if (keys & 15) {
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                mma.zero_tail(ring.slot, keys);
+            }
+            ok = ok && await(bar(G::BAR_PF + (j & 1)), p_phase >> (j & 1) & 1u, g, 8);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            p_phase ^= 1u << (j & 1);
+            tc_fence_after();
+            const int vs = uniform(ring.slot), ukeys = uniform(keys);
+            if (elect_one()) {
+                mma.pv(tO, tmem + (j & 1) * G::TMEM_TILE_STRIDE, vs, ukeys, j == 0);
+                mma_commit(bar(G::BAR_KVE + vs));
+                mma_commit(bar(G::BAR_PVD + (j & 1)));
+            }
+            ring.next();
+            ring.next();
+        }
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (elect_one()) mma_commit(bar(G::BAR_OF));
+    }
+    mma.finish(G::BAR_DONE + 1, g);
+}
+
+// The MMAs of tile t of two.
+template <int D, bool BF16>
+__device__ __forceinline__ void pack_issue(uint32_t sbase, uint32_t tmem, const UnitMsg *msgs, int t,
+                                           const PackArgs &a, const WaitGuard &g) {
+    using G = PackGeom<D, false>;
+    auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
+    const TileMma<D, BF16, false> mma(sbase, t, a);
     Ring<G::SLOTS> ring;
     int qbuf = 0;
     uint32_t q_phase = 0;         // of the Q buffers
-    uint32_t p_phase = 0;         // P stored; ONE: bit 0 and 1, of even and odd steps
+    uint32_t p_phase = 0;         // P stored
     uint32_t o_phase = 0;         // O handed back
     uint32_t turn = t ^ 1u;       // tile 0 goes first
     bool ok = true;
@@ -330,143 +446,79 @@ __device__ __forceinline__ void pack_issue(uint32_t sbase, uint32_t tmem, const 
         ok = await(bar(G::BAR_QF + qbuf), q_phase, g, 4);
         if (!__all_sync(0xffffffffu, ok)) break;
         const uint32_t qe = bar(G::BAR_QE + qbuf);
-        const uint64_t qdesc = dq + ((qbuf * G::Q_BUF_BYTES) >> 4);
+        const int qs = uniform(qbuf);
         if (++qbuf == G::QBUF) {
             qbuf = 0;
             q_phase ^= 1u;
         }
         const int last_keys = min(G::BN, x.sk - (x.step0 + nkv - 1) * G::BN);  // of the last step
-        if constexpr (ONE) {
-            // S of step j goes to the S columns of tile (j & 1), so S_{j+1}
-            // is made while the softmax works on S_j; S_{j+2} goes out right
-            // after P_j V_j, which has read the columns it overwrites. So K is
-            // taken two steps ahead of V: K_0 K_1 V_0 K_2 V_1 ...
-            const uint32_t tO = tmem + G::TMEM_O_OFF;
-            Ring<G::SLOTS> kr = ring;
-            auto next_s = [&](int j) {
-                ok = await(bar(G::BAR_KVF + kr.slot), kr.phase, g, 5);
-                if (!__all_sync(0xffffffffu, ok)) return;
-                tc_fence_after();
-                const int ks = uniform(kr.slot);
-                if (elect_one()) {
-                    issue_s(tmem + (j & 1) * G::TMEM_TILE_STRIDE, qdesc, dk + ks * tile16);
-                    mma_commit(bar(G::BAR_SF + (j & 1)));
-                    mma_commit(bar(G::BAR_KVE + ks));
-                    if (j == nkv - 1) mma_commit(qe);
-                }
-                kr.next();
-                kr.next();
-            };
+        // The issuers take turns, P V and the next S of one tile together:
+        // otherwise the tiles fall into step, their products side by side
+        // and then both in the softmax with the tensor pipe idle (b1 s8192
+        // h32 d128: 965 us).
+        const bool live = t < live_tiles<2>(x, a);
+        const uint32_t tS = tmem + t * G::TMEM_TILE_STRIDE;
 #pragma unroll 1
-            for (int j = -2; ok && j < nkv; ++j) {
-                if (j >= 0) {
-                    ring.next();  // past K_j
-                    ok = await(bar(G::BAR_KVF + ring.slot), ring.phase, g, 6);
+        for (int j = 0; ok && j <= nkv; ++j) {
+            const int keys = j == nkv ? last_keys : G::BN;  // of step j - 1
+            const Ring<G::SLOTS> vr = ring;
+            if (j > 0) ring.next();
+            const Ring<G::SLOTS> kr = ring;
+            if (j < nkv) ring.next();
+            // everything the turn needs: V_{j-1} (its tail zeroed), K_j, P_{j-1}
+            if (j > 0) {
+                ok = await(bar(G::BAR_KVF + vr.slot), vr.phase, g, 6);
+                if (live && (keys & 15)) {
                     if (!__all_sync(0xffffffffu, ok)) break;
-                    const int keys = j == nkv - 1 ? last_keys : G::BN;
-                    if (keys & 15) zero_tail(ring.slot, keys);
-                    // the first P V overwrites O: the last unit's must have been read out
-                    if (j == 0) ok = await(bar(G::BAR_OE), o_phase ^ 1u, g, 7);
-                    ok = ok && await(bar(G::BAR_PF + (j & 1)), p_phase >> (j & 1) & 1u, g, 8);
-                    if (!__all_sync(0xffffffffu, ok)) break;
-                    p_phase ^= 1u << (j & 1);
-                    tc_fence_after();
-                    const int vs = uniform(ring.slot), ukeys = uniform(keys);
-                    if (elect_one()) {
-                        issue_pv(tO, tmem + (j & 1) * G::TMEM_TILE_STRIDE, dv + vs * tile16, ukeys, j == 0);
-                        mma_commit(bar(G::BAR_KVE + vs));
-                        mma_commit(bar(G::BAR_PVD));
-                        if (j == nkv - 1) mma_commit(bar(G::BAR_OF));
-                    }
-                    ring.next();
-                }
-                if (j + 2 < nkv) next_s(j + 2);
-            }
-            if (!ok) break;
-            if (nkv == 0) {
-                // no key to see: O counts as made, once the last unit's has
-                // been read out (its barrier must not run two phases ahead)
-                ok = await(bar(G::BAR_OE), o_phase ^ 1u, g, 7);
-                if (!__all_sync(0xffffffffu, ok)) break;
-                if (elect_one()) {
-                    mma_commit(qe);
-                    mma_commit(bar(G::BAR_OF));
+                    mma.zero_tail(vr.slot, keys);
                 }
             }
-        } else {
-            // The issuers take turns, P V and the next S of one tile together:
-            // otherwise the tiles fall into step, their products side by side
-            // and then both in the softmax with the tensor pipe idle (b1 s8192
-            // h32 d128: 965 us).
-            const bool live = t < live_tiles<G::QT>(x, a);
-            const uint32_t tS = tmem + t * G::TMEM_TILE_STRIDE;
-#pragma unroll 1
-            for (int j = 0; ok && j <= nkv; ++j) {
-                const int keys = j == nkv ? last_keys : G::BN;  // of step j - 1
-                const Ring<G::SLOTS> vr = ring;
-                if (j > 0) ring.next();
-                const Ring<G::SLOTS> kr = ring;
-                if (j < nkv) ring.next();
-                // everything the turn needs: V_{j-1} (its tail zeroed), K_j, P_{j-1}
+            if (j < nkv) ok = ok && await(bar(G::BAR_KVF + kr.slot), kr.phase, g, 5);
+            if (live) {
+                // the first P V overwrites O: the last unit's must have been
+                // read out (also where there is no key to see: O's barrier
+                // must not run two phases ahead)
+                if (j == (nkv > 0 ? 1 : 0)) ok = ok && await(bar(G::BAR_OE + t), o_phase ^ 1u, g, 7);
                 if (j > 0) {
-                    ok = await(bar(G::BAR_KVF + vr.slot), vr.phase, g, 6);
-                    if (live && (keys & 15)) {
-                        if (!__all_sync(0xffffffffu, ok)) break;
-                        zero_tail(vr.slot, keys);
-                    }
-                }
-                if (j < nkv) ok = ok && await(bar(G::BAR_KVF + kr.slot), kr.phase, g, 5);
-                if (live) {
-                    // the first P V overwrites O: the last unit's must have been
-                    // read out (also where there is no key to see: O's barrier
-                    // must not run two phases ahead)
-                    if (j == (nkv > 0 ? 1 : 0)) ok = ok && await(bar(G::BAR_OE + t), o_phase ^ 1u, g, 7);
-                    if (j > 0) {
-                        ok = ok && await(bar(G::BAR_PF + t), p_phase, g, 8);
-                        p_phase ^= 1u;
-                    }
-                }
-                ok = ok && await(bar(G::BAR_TURN + t), turn, g, 22);
-                turn ^= 1u;
-                if (!__all_sync(0xffffffffu, ok)) break;
-                tc_fence_after();
-                const int vs = uniform(vr.slot), ks = uniform(kr.slot), ukeys = uniform(keys);
-                if (elect_one()) {
-                    if (live) {
-                        if (j > 0) {  // O += P_{j-1} V_{j-1}
-                            issue_pv(tS + G::TMEM_O_OFF, tS, dv + vs * tile16, ukeys, j == 1);
-                            mma_commit(bar(G::BAR_KVE + vs));
-                        }
-                        if (j < nkv) {
-                            issue_s(tS, qdesc, dk + ks * tile16);
-                            mma_commit(bar(G::BAR_SF + t));
-                            mma_commit(bar(G::BAR_KVE + ks));
-                            if (j == nkv - 1) mma_commit(qe);
-                        } else {
-                            mma_commit(bar(G::BAR_OF + t));
-                            mbar_arrive(bar(G::BAR_TURN + (t ^ 1)));
-                            if (nkv == 0) mma_commit(qe);
-                        }
-                    } else {
-                        // not this tile's unit: pass, and release the slots (they
-                        // are full, so that a release cannot run ahead)
-                        mbar_arrive(bar(G::BAR_TURN + (t ^ 1)));
-                        if (j > 0) mbar_arrive(bar(G::BAR_KVE + vr.slot));
-                        if (j < nkv) mbar_arrive(bar(G::BAR_KVE + kr.slot));
-                        if (j == (nkv > 0 ? nkv - 1 : 0)) mbar_arrive(qe);
-                    }
+                    ok = ok && await(bar(G::BAR_PF + t), p_phase, g, 8);
+                    p_phase ^= 1u;
                 }
             }
-            if (!live) continue;
+            ok = ok && await(bar(G::BAR_TURN + t), turn, g, 22);
+            turn ^= 1u;
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const int vs = uniform(vr.slot), ks = uniform(kr.slot), ukeys = uniform(keys);
+            if (elect_one()) {
+                if (live) {
+                    if (j > 0) {  // O += P_{j-1} V_{j-1}
+                        mma.pv(tS + G::TMEM_O_OFF, tS, vs, ukeys, j == 1);
+                        mma_commit(bar(G::BAR_KVE + vs));
+                    }
+                    if (j < nkv) {
+                        mma.s(tS, qs, ks, bar(G::BAR_TURN + (t ^ 1)));
+                        mma_commit(bar(G::BAR_SF + t));
+                        mma_commit(bar(G::BAR_KVE + ks));
+                        if (j == nkv - 1) mma_commit(qe);
+                    } else {
+                        mma_commit(bar(G::BAR_OF + t));
+                        mbar_arrive(bar(G::BAR_TURN + (t ^ 1)));
+                        if (nkv == 0) mma_commit(qe);
+                    }
+                } else {
+                    // not this tile's unit: pass, and release the slots (they
+                    // are full, so that a release cannot run ahead)
+                    mbar_arrive(bar(G::BAR_TURN + (t ^ 1)));
+                    if (j > 0) mbar_arrive(bar(G::BAR_KVE + vr.slot));
+                    if (j < nkv) mbar_arrive(bar(G::BAR_KVE + kr.slot));
+                    if (j == (nkv > 0 ? nkv - 1 : 0)) mbar_arrive(qe);
+                }
+            }
         }
+        if (!live) continue;
         o_phase ^= 1u;
     }
-    // No MMA may still be running when TMEM is released.
-    if (elect_one()) mma_commit(bar(G::BAR_DONE + t));
-    WaitGuard drain = g;
-    uint32_t no_abort = 0;
-    drain.abort = &no_abort;
-    await(bar(G::BAR_DONE + t), 0, drain, 12);
+    mma.finish(G::BAR_DONE + t, g);
 }
 
 // Joins a cut unit's partial results of one query tile: with M the largest
@@ -566,7 +618,6 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
     const uint32_t tO = tS0 + G::TMEM_O_OFF;
     const float c = fabsf(a.scale_log2);
     int s_cnt = 0, s2_cnt = 0, o_cnt = 0;
-    int pv_done = 0;  // ONE: P V products issued before this unit
     int met = 0;      // meetings of the tile's warps
     volatile int *joiner = reinterpret_cast<volatile int *>(smem + G::OFF_MISC + 8);
 
@@ -710,7 +761,8 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
                     // commit covers it where S_j was issued after it; ONE
                     // issues S_j earlier and waits for that product's own barrier
                     if (ONE) {
-                        const bool okv = await(bar(G::BAR_PVD), (pv_done + j - 1) & 1, g, 15);
+                        const bool okv =
+                            await(bar(G::BAR_PVD + (alt ? 0 : 1)), ((alt ? s_cnt : s2_cnt) - 1) & 1, g, 15);
                         if (!__all_sync(0xffffffffu, okv)) {
                             alive = false;
                             break;
@@ -743,7 +795,6 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
             }
         }
         if (!alive) return;
-        if (ONE) pv_done += nstep;
 
         // ---------------------------------------------------- epilogue
         // A row that saw no key of the range: O = 0, LSE = -inf. (Not told by
@@ -860,7 +911,7 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             if ((i >= G::BAR_PF && i < G::BAR_PF + 2) || (i >= G::BAR_OE && i < G::BAR_OE + 2))
                 count = 4;  // the tile's softmax warps
             if (i >= G::BAR_WG) count = 4;
-            if (i >= G::BAR_ME && i < G::BAR_MS) count = 1 + 5 * G::QT + (PAGED && ONE ? 1 : 0);  // producers, issuers, softmax warps
+            if (i >= G::BAR_ME && i < G::BAR_MS) count = ONE ? 7 + (PAGED ? 1 : 0) : 11;  // producers, issuers, softmax warps
             // released by each tile's issuer
             if ((i >= G::BAR_QE && i < G::BAR_KVF) || (i >= G::BAR_KVE && i < G::BAR_SF)) count = G::QT;
             mbar_init(bar(i), count);
@@ -888,10 +939,14 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             if ((PAGED || lane == 0) && !(a.flags & kFlagSkipLoads))
                 pack_producer<D, PAGED, ONE, PAGED && ONE ? 0 : 2>(&tq, &tk, &tv, sbase, msgs, a, g);
         } else if (warp < 3) {
-            if (warp <= G::QT) {
-                pack_issue<D, BF16, ONE>(sbase, tmem, msgs, warp - 1, a, g);
-            } else if constexpr (PAGED && ONE) {
-                if (!(a.flags & kFlagSkipLoads)) pack_producer<D, PAGED, ONE, 1>(&tq, &tk, &tv, sbase, msgs, a, g);
+            if constexpr (!ONE) {
+                pack_issue<D, BF16>(sbase, tmem, msgs, warp - 1, a, g);
+            } else {
+                if (warp == 1)
+                    issue_one_s<D, BF16>(sbase, tmem, msgs, a, g);
+                else if constexpr (PAGED)
+                    if (!(a.flags & kFlagSkipLoads))
+                        pack_producer<D, PAGED, ONE, 1>(&tq, &tk, &tv, sbase, msgs, a, g);
             }
         } else {
             post_units<0>(
@@ -900,6 +955,8 @@ __global__ void __launch_bounds__(kPackThreads, 1)
         }
     } else {
         reg_alloc<kPackRegsSoftmax>();
+        if (ONE && warp == 8)
+            issue_one_pv<D, BF16>(sbase, tmem, msgs, a, g);
         if (warp < 4 + 4 * G::QT)
             pack_softmax<D, BF16, ONE>(smem, sbase, tmem, msgs, (warp - 4) >> 2, warp & 3, a, g);
     }
