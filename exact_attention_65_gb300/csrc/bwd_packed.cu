@@ -29,9 +29,9 @@
 // that slice in the streamed tile.
 //
 // What bounds it: the chain of a step (S and dP products, P and dS, the sums),
-// which the tensor pipe and the elementwise warps share in turns: about 3,700
-// cycles per key-tile step and 3,300 per query-tile step at d = 128, against
-// 2,048 and 1,536 of products (b1 s8192 h32/8 d128: 2962 us, 928 TFLOP/s on the
+// which the tensor pipe and the elementwise warps share in turns: 3,950 cycles
+// per key-tile step and 3,430 per query-tile step at d = 128 in a trace of an
+// earlier form, against 2,048 and 1,536 of products (b1 s8192 h32/8 d128: 2962 us, 928 TFLOP/s on the
 // five products of the chain rule; causal 1540 us, 893 TFLOP/s).
 //
 // Roles (384 threads): warp 0 TMA producer, warp 1 MMA issuer, warp 2 stages
@@ -143,7 +143,7 @@ __device__ __forceinline__ int sequence_of(const SeqArrays &s, int tok) {
 // row that sees many keys |O| is small beside |dP|; for one that sees few it
 // is not (with one key dS is 0, and the error would be all that is left), so
 // rows that see at most kFewKeys keys form the sum over the keys, in fp32.
-constexpr int kFewKeys = 8;
+constexpr int kFewKeys = 16;
 
 template <int D, bool BF16>
 __device__ __forceinline__ float dot8(const uint4 &x, const uint4 &y) {
