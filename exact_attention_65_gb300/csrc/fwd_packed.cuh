@@ -23,23 +23,24 @@
 //
 // Roles (384 threads, one CTA per SM): warp 0 TMA producer (a whole warp for
 // pages, one box per lane; with V by warp 2 in the ONE form), warps 1 and 2
-// issue the MMAs of tile 0 and 1 (ONE: warp 1 S, warp 8 P V), warp 3 deals out units, warps 4-7 and 8-11
-// softmax and epilogue of tile 0 and 1. The two issuers take turns: with one
-// thread for both tiles the tensor pipe stood still while it waited and
-// counted (b1 s8192 h32 d128, no mask: 888 us, now 754).
+// issue the MMAs of tile 0 and 1 (ONE: warp 1 S, warp 8 P V), warp 3 deals
+// out units, warps 4-7 and 8-11 softmax and epilogue of tile 0 and 1. The two
+// issuers take turns: with one thread for both tiles the tensor pipe stood
+// still while it waited and counted (b1 s8192 h32 d128, no mask: 888 us, now
+// 754).
 //
 // V rows of a unit's last tile that lie past the sequence belong to the next
 // sequence or are stale; P is 0 there, and 0 * NaN is NaN: the issuers zero
 // those below the next multiple of 16, where the P V product stops.
 //
-// What bounds it: long prompts, the tensor pipe, whose products take about 100
-// cycles instead of 64 while the softmax warps read and write TMEM (b2 s8192
-// h32/8 d128 causal: 745 us, 1460 TFLOP/s, 77% of the measured peak); single
-// tokens, HBM and the change from unit to unit (64 requests of up
-// to 8192 keys, h32/8, 16-key pages: 158 us, 5.9 TB/s, 87%); batches of short
-// sequences, the change from one unit to the next (about 4.5 us: the epilogue,
-// and code that the instruction cache no longer holds; 16 prompts of 64 to
-// 1500 tokens: 129 us, 820 TFLOP/s).
+// What bounds it: long prompts, the tensor pipe, whose products took about 100
+// cycles instead of 64 in a trace, probably because the softmax warps use TMEM
+// at the same time (7777 and 8192 tokens h32/8 d128 causal: 743 to 788 us, 1380
+// to 1460 TFLOP/s, 72 to 77% of the measured peak); single tokens, HBM and the
+// change from unit to unit (64 requests of up to 8192 keys, h32/8, 16-key pages:
+// 154 to 160 us, 5.8 to 6.1 TB/s, 86 to 90%); batches of short sequences, that
+// change (an estimate of 4.5 us: the epilogue, and code that the instruction
+// cache no longer holds; 16 prompts of 64 to 1500 tokens: 128 us, 830 TFLOP/s).
 #pragma once
 
 #include <cuda_bf16.h>
