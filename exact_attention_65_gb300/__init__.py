@@ -93,6 +93,8 @@ def load_library() -> ctypes.CDLL:
         lib.attn_paged_write.argtypes = [vp] * 5 + [i64] + [i32] * 4 + [i64] * 2 + [i32, vp]
         lib.attn_debug_packed_plan.restype = i32
         lib.attn_debug_packed_plan.argtypes = [vp, vp] + [i32] * 8 + [vp]
+        lib.attn_debug_packed_starts.restype = i32
+        lib.attn_debug_packed_starts.argtypes = [vp, vp] + [i32] * 10 + [vp]
         lib.attn_decode_splitkv_noalloc.restype = i32
         lib.attn_decode_splitkv_noalloc.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
                                                     f32, i32, i32, vp]

@@ -84,6 +84,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kDevices = 64;
 constexpr int kMaxRows = 0x7fffff00;  // the ends of tiles stay below 2^31
+constexpr int64_t kMaxUnits = 1 << 29;  // of a call (fit_line() leaves a unit a cost of 1 at least)
 
 bool misaligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
@@ -182,6 +183,13 @@ attn_status_t get_workspace(int dev, cudaStream_t stream, int n, size_t part_byt
     return ATTN_OK;
 }
 
+// Units are counted in 31 bits: those of h_kv heads, of `rows` rows in b
+// sequences, unit_len rows at least in each.
+attn_status_t check_units(int b, int rows, int unit_len, int h_kv) {
+    const int64_t units = rows / unit_len + (b < rows ? b : rows);
+    return units * h_kv <= kMaxUnits ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
+}
+
 // What every packed attention call checks. Strides are in elements, of the
 // token dimension of q, k and v.
 attn_status_t check_packed(int b, int total_q, int h, int h_kv, int d, float scale, int dtype) {
@@ -192,7 +200,7 @@ attn_status_t check_packed(int b, int total_q, int h, int h_kv, int d, float sca
     if (d != 16 && d != 32 && d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
     if (b > 65535 || h > 65535 || h / h_kv > 128) return ATTN_ERR_UNSUPPORTED;
     if (total_q > kMaxRows) return ATTN_ERR_UNSUPPORTED;
-    return ATTN_OK;
+    return check_units(b, total_q, pack_tile_tokens(h / h_kv), h_kv);
 }
 
 attn_status_t check_stride(int64_t stride, int64_t row) {
@@ -281,37 +289,21 @@ void exattn::packed_release(int dev) {
     g_ws[dev].clear();
 }
 
-extern "C" {
+namespace {
 
-int attn_debug_packed_plan(const int *seqlens_q, const int *seqlens_k, int b, int h, int h_kv, int one_tile,
-                           int causal, int by_key, int ctas, int max_ranges, int *out) {
-    if (!seqlens_q || !seqlens_k || !out || b < 1 || h < 1 || h_kv < 1 || h % h_kv != 0 || h / h_kv > 128 ||
-        ctas < 1 || max_ranges < 1)
-        return -1;
-    int64_t all_q = 0, all_k = 0;
-    for (int i = 0; i < b; ++i) {
-        if (seqlens_q[i] < 0 || seqlens_k[i] < 0) return -1;
-        all_q += seqlens_q[i];
-        all_k += seqlens_k[i];
-    }
-    if (all_q > kMaxRows || all_k > kMaxRows) return -1;
-    LineBound bound{b, 0, 0, 0};
-    for (int i = 0; i < b; ++i) {
-        bound.total_q += seqlens_q[i];
-        bound.total_k += seqlens_k[i];
-    }
-    bound.max_k = bound.total_k;
-    LineShape s = by_key ? bwd_key_line(h_kv, h / h_kv, causal != 0, bound)
-                         : pack_line(h_kv, h / h_kv, one_tile != 0, causal != 0, bound);
+// The plan of the line of these sequences for ctas CTAs, as the kernels make
+// it: rows of 9 ints (attn_debug_packed_plan). in_order: what the starts say.
+int plan_on_host(LineShape s, const std::vector<SeqLen> &seqs, bool in_order, int ctas, int max_ranges, int *out) {
+    const int b = static_cast<int>(seqs.size());
     LineSum sum{0, 0, 0};
-    for (int i = 0; i < b; ++i) line_add(&sum, s, seqlens_q[i], seqlens_k[i]);
+    for (const SeqLen &x : seqs) line_add(&sum, s, x.sq, x.sk, in_order);
     const LineDeal d = line_deal(&s, sum, ctas);
     auto find = [&](int at, int *before) {
         *before = 0;
         for (int i = 0; i < b; ++i) {
-            const int cost =
-                s.heads * line_before(s, seqlens_q[i], seqlens_k[i], line_units(s, seqlens_q[i], seqlens_k[i]));
-            if (at < *before + cost) return place_in_seq(s, i, seqlens_q[i], seqlens_k[i], at - *before);
+            const int sq = seqs[i].sq, sk = seqs[i].sk;
+            const int cost = s.heads * line_before(s, sq, sk, line_units(s, sq, sk));
+            if (at < *before + cost) return place_in_seq(s, i, sq, sk, at - *before);
             *before += cost;
         }
         return Place{b, 0, 0, 0};
@@ -321,9 +313,8 @@ int attn_debug_packed_plan(const int *seqlens_q, const int *seqlens_k, int b, in
         int x0 = 0, unused = 0;
         const Place p = find(part_begin(d, c), &x0), e = find(part_begin(d, c + 1), &unused);
         if (p.seq >= b) continue;
-        walk_part(s, b, p, e, SeqLen{seqlens_q[p.seq], seqlens_k[p.seq]},
-                  line_units(s, seqlens_q[p.seq], seqlens_k[p.seq]), x0,
-                  [&](int i) { return SeqLen{seqlens_q[i], seqlens_k[i]}; },
+        walk_part(s, b, p, e, seqs[p.seq], line_units(s, seqs[p.seq].sq, seqs[p.seq].sk), x0,
+                  [&](int i) { return seqs[i]; },
                   [&](const UnitRange &r) {
                       if (n >= max_ranges) return false;
                       int first = c, cuts = 0;
@@ -336,6 +327,57 @@ int attn_debug_packed_plan(const int *seqlens_q, const int *seqlens_k, int b, in
                   });
     }
     return n;
+}
+
+bool plan_args_ok(const void *q, const void *k, const void *out, int b, int h, int h_kv, int ctas, int max_ranges) {
+    return q && k && out && b >= 1 && h >= 1 && h_kv >= 1 && h % h_kv == 0 && h / h_kv <= 128 && ctas >= 1 &&
+           max_ranges >= 1;
+}
+
+LineShape plan_shape(int h, int h_kv, int one_tile, int causal, int by_key, const LineBound &bound) {
+    return by_key ? bwd_key_line(h_kv, h / h_kv, causal != 0, bound)
+                  : pack_line(h_kv, h / h_kv, one_tile != 0, causal != 0, bound);
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_debug_packed_plan(const int *seqlens_q, const int *seqlens_k, int b, int h, int h_kv, int one_tile,
+                           int causal, int by_key, int ctas, int max_ranges, int *out) try {
+    if (!plan_args_ok(seqlens_q, seqlens_k, out, b, h, h_kv, ctas, max_ranges)) return -1;
+    int64_t all_q = 0, all_k = 0;
+    std::vector<SeqLen> seqs(b);
+    for (int i = 0; i < b; ++i) {
+        if (seqlens_q[i] < 0 || seqlens_k[i] < 0) return -1;
+        seqs[i] = SeqLen{seqlens_q[i], seqlens_k[i]};
+        all_q += seqlens_q[i];
+        all_k += seqlens_k[i];
+    }
+    if (all_q > kMaxRows || all_k > kMaxRows) return -1;
+    const LineBound bound{b, static_cast<int>(all_q), all_k, all_k};
+    return plan_on_host(plan_shape(h, h_kv, one_tile, causal, by_key, bound), seqs, true, ctas, max_ranges, out);
+} catch (...) {  // no exception leaves the library
+    return -1;
+}
+
+int attn_debug_packed_starts(const int *cu_seqlens_q, const int *cu_seqlens_k, int b, int total_q, int total_k,
+                             int h, int h_kv, int one_tile, int causal, int by_key, int ctas, int max_ranges,
+                             int *out) try {
+    if (!plan_args_ok(cu_seqlens_q, cu_seqlens_k, out, b, h, h_kv, ctas, max_ranges) || total_q < 1 || total_k < 1 ||
+        total_q > kMaxRows || total_k > kMaxRows)
+        return -1;
+    std::vector<SeqLen> seqs(b);
+    bool in_order = true;
+    for (int i = 0; i < b; ++i) {
+        int first = 0;
+        in_order &= clamp_rows(cu_seqlens_q[i], cu_seqlens_q[i + 1], total_q, &first, &seqs[i].sq);
+        in_order &= clamp_rows(cu_seqlens_k[i], cu_seqlens_k[i + 1], total_k, &first, &seqs[i].sk);
+    }
+    const LineBound bound{b, total_q, total_k, total_k};
+    return plan_on_host(plan_shape(h, h_kv, one_tile, causal, by_key, bound), seqs, in_order, ctas, max_ranges, out);
+} catch (...) {
+    return -1;
 }
 
 attn_status_t attn_fwd_packed(const void *q, const void *k, const void *v, const int32_t *cu_seqlens_q,
@@ -429,6 +471,7 @@ attn_status_t attn_bwd_packed(const void *q, const void *k, const void *v, const
     if (total_k < 1) return ATTN_ERR_INVALID_ARG;
     attn_status_t st = check_packed(b, total_q, h, h_kv, d, scale, dtype);
     if (st == ATTN_OK && total_k > kMaxRows) st = ATTN_ERR_UNSUPPORTED;
+    if (st == ATTN_OK) st = check_units(b, total_k, 128, h_kv);
     const int64_t qrow = static_cast<int64_t>(h) * d, krow = static_cast<int64_t>(h_kv) * d;
     for (int64_t s : {q_stride, dq_stride})
         if (st == ATTN_OK) st = check_stride(s, qrow);

@@ -48,17 +48,16 @@ struct SeqInfo {
     int q0, sq, k0, sk;
 };
 
-__device__ __forceinline__ SeqInfo seq_info(const SeqArrays &s, int i) {
+__device__ __forceinline__ SeqInfo seq_info(const SeqArrays &s, int i, bool *ordered = nullptr) {
     SeqInfo x;
-    x.q0 = min(max(__ldg(s.cu_q + i), 0), s.total_q);
-    x.sq = min(max(__ldg(s.cu_q + i + 1), x.q0), s.total_q) - x.q0;
+    bool in_order = clamp_rows(__ldg(s.cu_q + i), __ldg(s.cu_q + i + 1), s.total_q, &x.q0, &x.sq);
     if (s.cu_k != nullptr) {
-        x.k0 = min(max(__ldg(s.cu_k + i), 0), s.max_k);
-        x.sk = min(max(__ldg(s.cu_k + i + 1), x.k0), s.max_k) - x.k0;
+        in_order &= clamp_rows(__ldg(s.cu_k + i), __ldg(s.cu_k + i + 1), s.max_k, &x.k0, &x.sk);
     } else {
         x.k0 = 0;
         x.sk = min(max(__ldg(s.seqlens + i), 0), s.max_k);
     }
+    if (ordered != nullptr) *ordered = in_order;
     return x;
 }
 
@@ -102,8 +101,9 @@ __device__ __forceinline__ void line_sum_warps(const SeqArrays &s, LineShape sha
     LineSum t{0, 0, 0};
 #pragma unroll 1
     for (int i = threadIdx.x; i < s.b; i += blockDim.x) {
-        const SeqInfo x = seq_info(s, i);
-        line_add(&t, shape, x.sq, x.sk);
+        bool ordered;
+        const SeqInfo x = seq_info(s, i, &ordered);
+        line_add(&t, shape, x.sq, x.sk, ordered);
     }
     t.cost = __reduce_add_sync(0xffffffffu, t.cost);
     t.units = __reduce_add_sync(0xffffffffu, t.units);
@@ -133,14 +133,16 @@ __device__ __forceinline__ void post_units(const SeqArrays &seqs, LineShape shap
     const int lane = threadIdx.x & 31;
     known_shape<BY_KEY>(&shape);
     SeqInfo x{0, 0, 0, 0};
-    if (lane < seqs.b) x = seq_info(seqs, lane);
+    bool ordered = true;
+    if (lane < seqs.b) x = seq_info(seqs, lane, &ordered);
     int n = line_units(shape, x.sq, x.sk);         // units of a head
     int per = line_before(shape, x.sq, x.sk, n);   // and their cost
     LineSum sum;
     if (seqs.b <= 32) {
         sum.cost = __reduce_add_sync(0xffffffffu, shape.heads * per);
         sum.units = __reduce_add_sync(0xffffffffu, shape.heads * n);
-        const int longest = n == 0 ? 0
+        const int longest = !ordered ? kOutOfOrder
+                            : n == 0 ? 0
                             : BY_KEY ? line_before(shape, x.sq, x.sk, 1)
                                      : per - line_before(shape, x.sq, x.sk, n - 1);
         sum.longest = __reduce_max_sync(0xffffffffu, longest);

@@ -106,19 +106,35 @@ EXATTN_HD int line_before(const LineShape &s, int sq, int sk, int n) {
     return n * s.unit_cost + static_cast<int>((sum * s.weight) >> s.shift);
 }
 
-// Sums over the sequences.
+// Rows [a, z) of a sequence whose starts come from the device, moved into [0,
+// total): whatever the array holds, they stay inside the tensor. False: the
+// starts are out of order.
+EXATTN_HD bool clamp_rows(int a, int z, int total, int *first, int *rows) {
+    *first = smin(smax(a, 0), total);
+    *rows = smin(smax(z, *first), total) - *first;
+    return a <= z;
+}
+
+// Sums over the sequences. Starts in order give sequences that do not overlap,
+// so that the sums stay below the bound that the host fitted the shape to;
+// out of order, sequences could overlap and the 32-bit sums wrap, and with
+// them every place on the line. kOutOfOrder as `longest` then says so (no unit
+// is that long), and nothing is dealt out.
+constexpr int kOutOfOrder = 0x7fffffff;
 struct LineSum {
     int cost;     // with the heads
     int units;    // with the heads
     int longest;  // unit: the last one over query tokens, the first one over keys
 };
 
-EXATTN_HD void line_add(LineSum *t, const LineShape &s, int sq, int sk) {
+EXATTN_HD void line_add(LineSum *t, const LineShape &s, int sq, int sk, bool ordered) {
+    if (!ordered) t->longest = kOutOfOrder;
     const int n = line_units(s, sq, sk);
     if (n == 0) return;
     const int all = line_before(s, sq, sk, n);
-    t->cost += s.heads * all;
-    t->units += s.heads * n;
+    // (unsigned: out of order, they may wrap)
+    t->cost = static_cast<int>(static_cast<uint32_t>(t->cost) + static_cast<uint32_t>(s.heads) * all);
+    t->units = static_cast<int>(static_cast<uint32_t>(t->units) + static_cast<uint32_t>(s.heads) * n);
     t->longest = smax(t->longest, s.by_key ? line_before(s, sq, sk, 1) : all - line_before(s, sq, sk, n - 1));
 }
 
@@ -134,7 +150,8 @@ EXATTN_HD bool line_whole(const LineShape &s, const LineSum &t, int ctas) {
 }
 
 EXATTN_HD LineDeal line_deal(LineShape *s, const LineSum &t, int ctas) {
-    LineDeal d;
+    LineDeal d{0, 0, 0, 0};
+    if (t.longest == kOutOfOrder) return d;
     d.length = t.cost;
     d.parts = smin(ctas, smax(1, static_cast<int>(static_cast<uint32_t>(t.cost) / static_cast<uint32_t>(s->min_part))));
     if (line_whole(*s, t, ctas)) {
@@ -200,8 +217,10 @@ inline Place place_in_seq(const LineShape &s, int seq, int sq, int sk, int rem) 
 
 // Whether part c begins inside a unit that begins at x0, costs `cost` and has n
 // steps, away from its ends: where it cuts it. The parts that share a unit are
-// the one before the first cut, and one per cut.
+// the one before the first cut, and one per cut (part 0 begins the line and
+// cuts nothing, so there is one before).
 EXATTN_HD bool part_cuts(const LineShape &s, const LineDeal &d, int c, int x0, int cost, int n) {
+    if (c == 0) return false;
     const int x = part_begin(d, c) - x0;
     if (x <= 0 || x >= cost) return false;
     const int t = place_step(s, x, cost, n);

@@ -242,9 +242,10 @@ attn_status_t attn_decode_paged(const void *q, const void *k_pages, const void *
  * Sequences of different lengths lie one behind the other in one tensor of
  * rows: sequence i holds rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1 (int32
  * [b + 1], on the device, ascending; a sequence may be empty). Rows that
- * belong to no sequence are neither used nor written. Starts that are out of
- * order or past the tensor are clamped: the results then mean nothing, but
- * no other memory is touched.
+ * belong to no sequence are neither used nor written. Starts past the tensor
+ * are clamped to its end, and a call whose starts are out of order may leave
+ * its results unwritten: they then mean nothing, but no other memory is
+ * touched.
  *
  * Grouped heads: h query heads share h_kv K/V heads, h a multiple of h_kv
  * and at most 128 h_kv (ATTN_ERR_UNSUPPORTED above); query head x uses K/V
@@ -506,7 +507,16 @@ int attn_debug_short_plan(int sq, int sk, int h, int d, int grouped_ok, int *out
 int attn_debug_packed_plan(const int *seqlens_q, const int *seqlens_k, int b, int h, int h_kv,
                            int one_tile, int causal, int by_key, int ctas, int max_ranges, int *out);
 
-/* Library ABI version (major * 100 + minor): 102. */
+/*
+ * Test hook, host-side only: attn_debug_packed_plan from starts as the kernels
+ * read them (int32 [b + 1], whatever they hold) in tensors of total_q and
+ * total_k rows: clamped, and nothing dealt out (0) where they are out of order.
+ */
+int attn_debug_packed_starts(const int *cu_seqlens_q, const int *cu_seqlens_k, int b, int total_q,
+                             int total_k, int h, int h_kv, int one_tile, int causal, int by_key,
+                             int ctas, int max_ranges, int *out);
+
+/* Library ABI version (major * 100 + minor): 103. */
 int attn_version(void);
 
 #ifdef __cplusplus
