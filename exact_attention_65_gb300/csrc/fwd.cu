@@ -489,7 +489,10 @@ __device__ __forceinline__ void fwd_mma(uint32_t sbase, uint32_t tmem, int nqb, 
                 if (j + 2 < x.nkv) ok = issue_s(j + 2);
             }
             if (!ok) break;
-            if (x.nkv == 0) {  // causal: a unit that sees no key
+            if (x.nkv == 0) {  // a unit that sees no key
+                // O full may not run two phases ahead of the epilogue: its
+                // wait could not tell them apart by the parity
+                if (!mbar_wait(bar(G::BAR_OE), (o_cnt[0] & 1) ^ 1, g, 7)) break;
                 mma_commit(bar(G::BAR_QE + qbuf));
                 mma_commit(bar(G::BAR_OF));
             }
@@ -561,6 +564,14 @@ __device__ __forceinline__ void fwd_mma(uint32_t sbase, uint32_t tmem, int nqb, 
                         if (j == x.nkv - 1) mma_commit(bar(G::BAR_QE + qbuf));  // ... and of this Q
                     }
                 } else {
+                    // a unit that sees no key waited for nothing so far: O full
+                    // may not run two phases ahead of the epilogue
+                    if constexpr (SPLIT != 0) {
+                        if (x.nkv == 0 && !mbar_wait(bar(G::BAR_OE + t), (o_cnt[t] & 1) ^ 1, g, 7)) {
+                            ok = false;
+                            break;
+                        }
+                    }
                     mma_commit(bar(G::BAR_OF + t));
                 }
             }
