@@ -342,6 +342,9 @@ __device__ __forceinline__ void bwd_mma(uint32_t sbase, uint32_t tmem, int ntile
         int first, count;
         unit_steps<MODE, CAUSAL>(bunit_of<MODE, CAUSAL>(u, ntiles, a), nsteps, a, first, count);
         if (count == 0) {  // nothing to accumulate: free the fixed tiles, hand over
+            // (accumulators full may not run two phases ahead of the epilogue:
+            // its wait could not tell them apart by the parity)
+            if (!mbar_wait(bar(G::BAR_AE), (it_u & 1) ^ 1, g, 7)) break;
             mma_commit(bar(G::BAR_FE));
             mma_commit(bar(G::BAR_AF));
             continue;

@@ -79,3 +79,27 @@ def test_key_ranges_past_the_end(gpu, oracle_mod):
             o_ref, lse_ref = oracle_mod.attention(q[i:i + 1], keys, values, 1 / math.sqrt(d), rows=list(range(sq)),
                                                   causal=causal)
             compare_masked(o[i:i + 1], lse[i:i + 1], o_ref, lse_ref, rows=list(range(sq)))
+
+
+@pytest.mark.parametrize("b,sq,sk,h", [
+    (2, 1024, 10, 60),   # seven of eight query tiles see no key
+    (1, 10, 3000, 60),   # all keys are seen
+    (1, 2000, 200, 60),
+])
+def test_backward_with_many_more_rows_than_keys(gpu, oracle_mod, b, sq, sk, h):
+    """dQ = 0 in the rows that see no key; the gradients of two heads against the oracle."""
+    d = 128
+    q, k, v = workloads.make_qkv(b, sq, sk, h, d, torch.bfloat16, seed=103)
+    g = torch.randn(q.shape, generator=torch.Generator().manual_seed(104)).bfloat16()
+    dev = [t.cuda() for t in (q, k, v)]
+    o, lse = gpu.attn_fwd(*dev, causal=True)
+    grads = gpu.attn_bwd(*dev, o, lse, g.cuda(), causal=True)
+    assert gpu.attn_get_device_status() == gpu.ATTN_OK
+    assert torch.all(grads[0][:, :max(sq - sk, 0)] == 0)
+    for head in (0, h - 1):
+        part = [x[:, :, head:head + 1].contiguous() for x in (q, k, v, g)]
+        refs = oracle_mod.attention_backward(*part, 1 / math.sqrt(d), causal=True)
+        for x, ref in zip(grads, refs):
+            got = x[:, :, head:head + 1].double().cpu().numpy()
+            assert np.isfinite(got).all()
+            assert np.abs(got - ref).max() <= 2e-2 * (1 + np.abs(ref).max())
