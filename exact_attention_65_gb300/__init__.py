@@ -95,6 +95,8 @@ def load_library() -> ctypes.CDLL:
         lib.attn_debug_packed_plan.argtypes = [vp, vp] + [i32] * 8 + [vp]
         lib.attn_debug_packed_starts.restype = i32
         lib.attn_debug_packed_starts.argtypes = [vp, vp] + [i32] * 10 + [vp]
+        lib.attn_debug_packed_shares.restype = i32
+        lib.attn_debug_packed_shares.argtypes = [vp, vp] + [i32] * 5 + [vp]
         lib.attn_decode_splitkv_noalloc.restype = i32
         lib.attn_decode_splitkv_noalloc.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
                                                     f32, i32, i32, vp]

@@ -534,7 +534,7 @@ int dec_num_splits(int b, int sq, int sk, int h, int d, int num_sms) {
 
 extern "C" {
 
-int attn_version(void) { return 103; }
+int attn_version(void) { return 104; }
 
 const char *attn_status_string(attn_status_t s) {
     switch (s) {

@@ -47,7 +47,7 @@ LineShape pack_line(int heads, int group, bool one_tile, bool causal, const Line
     s.by_key = 0;
     s.weight = 1;
     s.shift = 7;
-    s.unit_cost = 2;
+    s.unit_cost = kUnitSteps;
     s.min_steps = one_tile ? 2 : 6;
     s.min_part = one_tile ? 4 : 16;
     fit_line(&s, bound);
@@ -70,7 +70,7 @@ LineShape bwd_key_line(int heads, int group, bool causal, const LineBound &bound
     s.by_key = 1;
     s.weight = group;
     s.shift = 7;
-    s.unit_cost = 2;
+    s.unit_cost = kUnitSteps;
     s.min_steps = 2;
     s.min_part = 8;
     fit_line(&s, bound);
@@ -378,6 +378,29 @@ int attn_debug_packed_starts(const int *cu_seqlens_q, const int *cu_seqlens_k, i
     return plan_on_host(plan_shape(h, h_kv, one_tile, causal, by_key, bound), seqs, in_order, ctas, max_ranges, out);
 } catch (...) {
     return -1;
+}
+
+int attn_debug_packed_shares(const int *seqlens_q, const int *seqlens_k, int b, int h, int h_kv, int causal,
+                             int ctas, int *out) {
+    if (!plan_args_ok(seqlens_q, seqlens_k, out, b, h, h_kv, ctas, 1) || ctas < 2) return -1;
+    LineBound bound{b, 0, 0, 0};
+    for (int i = 0; i < b; ++i) {
+        if (seqlens_q[i] < 0 || seqlens_k[i] < 0 || seqlens_q[i] > kMaxRows - bound.total_q) return -1;
+        bound.total_q += seqlens_q[i];
+        bound.total_k += seqlens_k[i];
+    }
+    if (bound.total_k > kMaxRows) return -1;
+    bound.max_k = bound.total_k;
+    const LineShape q = bwd_query_line(h_kv, h / h_kv, causal != 0, bound),
+                    kv = bwd_key_line(h_kv, h / h_kv, causal != 0, bound);
+    LineSum qs{0, 0, 0}, kvs{0, 0, 0};
+    for (int i = 0; i < b; ++i) {
+        line_add(&qs, q, seqlens_q[i], seqlens_k[i], true);
+        line_add(&kvs, kv, seqlens_q[i], seqlens_k[i], true);
+    }
+    out[0] = q.shift;
+    out[1] = kv.shift;
+    return key_ctas(q, qs, kv, kvs, ctas);
 }
 
 attn_status_t attn_fwd_packed(const void *q, const void *k, const void *v, const int32_t *cu_seqlens_q,

@@ -857,18 +857,6 @@ __device__ __forceinline__ void pbwd_compute(uint8_t *smem, uint32_t sbase, uint
     }
 }
 
-// CTAs of the key-tile kind, of ctas in all. A key-tile step (four products)
-// takes 1.15 times a query-tile step (three); with the units' fixed costs,
-// short sequences have more of their time in query tiles (b1 s8192 h32/8 d128
-// causal: 1581 us with 80 of 152 for keys whatever the lengths, 1542 so).
-// Where every unit can have a CTA to itself, each kind gets at least its units.
-__device__ __forceinline__ int key_ctas(const LineSum &q, const LineSum &kv, int ctas) {
-    const float wq = static_cast<float>(q.cost), wkv = 1.15f * static_cast<float>(kv.cost);
-    int n = static_cast<int>(__fdividef(static_cast<float>(ctas) * wkv, fmaxf(wq + wkv, 1.f)) + 0.5f);
-    if (q.units + kv.units <= ctas) n = min(max(n, kv.units), ctas - q.units);
-    return min(max(n, 1), ctas - 1);
-}
-
 template <int D, int MODE, bool BF16>
 __device__ __forceinline__ void pbwd_run(const CUtensorMap *tq, const CUtensorMap *tk, const CUtensorMap *tv,
                                          const CUtensorMap *tdo, uint8_t *smem, uint32_t sbase, uint32_t tmem,
@@ -951,8 +939,9 @@ __global__ void __launch_bounds__(kPBwdThreads, 1)
     tc_fence_after();
     const uint32_t tmem = uniform(*tmem_slot);
     const WaitGuard g{abort_flag, a.status, kKernBwd};
-    const int ctas_kv = key_ctas(line_total(sums, kPBwdThreads / 32),
-                                 line_total(sums + kPBwdThreads / 32, kPBwdThreads / 32), gridDim.x);
+    const int ctas_kv =
+        key_ctas(a.line[kModeDQ], line_total(sums, kPBwdThreads / 32), a.line[kModeDKV],
+                 line_total(sums + kPBwdThreads / 32, kPBwdThreads / 32), gridDim.x);
     if (static_cast<int>(blockIdx.x) < ctas_kv)
         pbwd_run<D, kModeDKV, BF16>(&tq, &tk, &tv, &tdo, smem, sbase, tmem, blockIdx.x, ctas_kv, a, g);
     else

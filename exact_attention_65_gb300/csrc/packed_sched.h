@@ -50,6 +50,9 @@ struct LineShape {
     int unit_div, step_div;       //   (the shifts)
 };
 
+// A unit's fixed cost, in steps.
+constexpr int kUnitSteps = 2;
+
 // mul and shift of a division by len (1 .. 256): with 2^k >= len, mul =
 // ceil(2^(31 + k) / len) fits 32 bits, and x * mul >> (31 + k) is exact for x <
 // 2^31, as mul errs by less than 1 and x / 2^(31 + k) < 1 / len.
@@ -172,6 +175,28 @@ EXATTN_HD int part_begin(const LineDeal &d, int c) {
 #else
     return d.q * c + d.r * c / d.parts;
 #endif
+}
+
+// CTAs of the backward's key-tile kind, of ctas in all, from both kinds' lines.
+// A key-tile step (four products) takes 1.15 times a query-tile step (three);
+// with the units' fixed costs, short sequences have more of their time in query
+// tiles (b1 s8192 h32/8 d128 causal: 1581 us with 80 of 152 for keys whatever
+// the lengths, 1542 so). Each line counts 2^(shift - 7) steps as one, the two
+// shifts can differ, and a unit's fixed cost then is a rounded one. Where every
+// unit can have a CTA to itself, each kind gets at least its units.
+EXATTN_HD float line_steps_of(const LineShape &s, const LineSum &t) {
+    return static_cast<float>(t.cost - t.units * s.unit_cost) * static_cast<float>(1u << (s.shift - 7)) +
+           static_cast<float>(kUnitSteps) * static_cast<float>(t.units);
+}
+EXATTN_HD int key_ctas(const LineShape &q, const LineSum &qs, const LineShape &kv, const LineSum &kvs, int ctas) {
+    const float wq = line_steps_of(q, qs), wkv = 1.15f * line_steps_of(kv, kvs), all = wq + wkv > 1.f ? wq + wkv : 1.f;
+#if defined(__CUDA_ARCH__)
+    int n = static_cast<int>(__fdividef(static_cast<float>(ctas) * wkv, all) + 0.5f);
+#else
+    int n = static_cast<int>(static_cast<float>(ctas) * wkv / all + 0.5f);
+#endif
+    if (qs.units + kvs.units <= ctas) n = smin(smax(n, kvs.units), ctas - qs.units);
+    return smin(smax(n, 1), ctas - 1);
 }
 
 // A place x (counted from the unit's beginning) as a step of a unit of n

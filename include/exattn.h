@@ -516,7 +516,16 @@ int attn_debug_packed_starts(const int *cu_seqlens_q, const int *cu_seqlens_k, i
                              int total_k, int h, int h_kv, int one_tile, int causal, int by_key,
                              int ctas, int max_ranges, int *out);
 
-/* Library ABI version (major * 100 + minor): 103. */
+/*
+ * Test hook, host-side only: how many of ctas CTAs (at least 2) the packed
+ * backward gives to its key tiles; out[0], out[1]: the logarithms of the units
+ * in which the costs of its query-tile and key-tile work are counted (7: one
+ * step). -1 on invalid arguments.
+ */
+int attn_debug_packed_shares(const int *seqlens_q, const int *seqlens_k, int b, int h, int h_kv,
+                             int causal, int ctas, int *out);
+
+/* Library ABI version (major * 100 + minor): 104. */
 int attn_version(void);
 
 #ifdef __cplusplus
