@@ -101,8 +101,11 @@ struct DeviceState {
     // The split decode's workspace, one per stream: arrival counters of the
     // in-kernel reduce (all zero whenever a call starts) and the per-split
     // partials. Calls on one stream are ordered, so each call may reuse them.
+    // (A handle may come back for another stream once its stream is destroyed,
+    // even with work of that one still to do; the id is unique.)
     struct StreamWs {
         cudaStream_t stream;
+        unsigned long long id;
         uint32_t *counters;
         int64_t n_counters;
         void *part;
@@ -189,24 +192,32 @@ cudaStream_t side_stream(DeviceState *ds, cudaStream_t stream) {
 // counters and part_bytes of partials, grown stream-ordered on `stream`
 // (what is replaced is freed after the work already queued there). False
 // while the stream is being captured into a graph, whose replays could run
-// concurrently: the caller then takes a workspace per call and the separate
-// reduce kernel.
+// concurrently, on the per-thread default stream (one handle, many streams),
+// and on a stream whose handle was another stream's before (what that one
+// still has to do is not ordered with it): the caller then takes a workspace
+// per call and the separate reduce kernel.
 bool stream_workspace(DeviceState *ds, cudaStream_t stream, int64_t n, size_t part_bytes,
                       uint32_t **counters, void **part) {
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
     if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) {
         cudaGetLastError();
         return false;
     }
-    if (cs != cudaStreamCaptureStatusNone) return false;
+    if (cs != cudaStreamCaptureStatusNone || stream == cudaStreamPerThread) return false;
+    if (cudaStreamGetId(stream, &id) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
     std::lock_guard<std::mutex> lock(g_mu);
     DeviceState::StreamWs *e = nullptr;
     for (auto &x : ds->stream_ws)
         if (x.stream == stream) e = &x;
     if (e == nullptr) {
-        ds->stream_ws.push_back(DeviceState::StreamWs{stream, nullptr, 0, nullptr, 0});
+        ds->stream_ws.push_back(DeviceState::StreamWs{stream, id, nullptr, 0, nullptr, 0});
         e = &ds->stream_ws.back();
     }
+    if (e->id != id) return false;
     if (e->n_counters < n) {
         const int64_t cap = n < 1024 ? 1024 : n;
         uint32_t *p = nullptr;

@@ -91,9 +91,12 @@ bool misaligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>
 // What the cut units of a call leave for one another, kept per stream: calls
 // on a stream are ordered, so each call reuses it. The lock is held until the
 // call is enqueued, so that another host thread cannot replace the buffers in
-// between.
+// between. A handle may come back for another stream once its stream is
+// destroyed, even with work of that one still to do, so an entry also holds
+// the stream's id, which is unique.
 struct PackWs {
     cudaStream_t stream;
+    unsigned long long id;
     uint32_t *arrivals = nullptr;
     int n_arrivals = 0;
     char *part = nullptr;
@@ -111,10 +114,31 @@ struct Workspace {
     void *owned = nullptr;  // a workspace of this call's own, to be freed stream-ordered
 };
 
-// n arrival counters and part_bytes of partial results. A stream that is
-// being captured (its replays are not ordered with the stream's other calls),
-// or the per-thread default stream (one handle, many streams), gets them from
-// the memory pool for this call alone.
+// n arrival counters and part_bytes of partial results of one call's own, from
+// the memory pool.
+attn_status_t own_workspace(cudaStream_t stream, size_t count_bytes, size_t part_bytes, Workspace *w) {
+    void *p = nullptr;
+    if (cudaMallocAsync(&p, count_bytes + part_bytes, stream) != cudaSuccess) {
+        cudaGetLastError();
+        return ATTN_ERR_NO_MEMORY;
+    }
+    if (cudaMemsetAsync(p, 0, count_bytes, stream) != cudaSuccess) {
+        cudaFreeAsync(p, stream);
+        return ATTN_ERR_CUDA;
+    }
+    w->owned = p;
+    w->arrivals = static_cast<uint32_t *>(p);
+    w->part = static_cast<char *>(p) + count_bytes;
+    w->call = 1;
+    return ATTN_OK;
+}
+
+// The stream's workspace, grown where it is too small. Streams that cannot have
+// one of their own get it for the call alone: one that is being captured (its
+// replays are not ordered with the stream's other calls), the per-thread
+// default stream (one handle, many streams), and one whose handle was another
+// stream's before (what that one still has to do is not ordered with it; its
+// entry stays until packed_release()).
 attn_status_t get_workspace(int dev, cudaStream_t stream, int n, size_t part_bytes, Workspace *w) {
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) {
@@ -122,21 +146,12 @@ attn_status_t get_workspace(int dev, cudaStream_t stream, int n, size_t part_byt
         return ATTN_ERR_CUDA;
     }
     const size_t count_bytes = (static_cast<size_t>(n) * sizeof(uint32_t) + 255) / 256 * 256;
-    if (cs != cudaStreamCaptureStatusNone || stream == cudaStreamPerThread) {
-        void *p = nullptr;
-        if (cudaMallocAsync(&p, count_bytes + part_bytes, stream) != cudaSuccess) {
-            cudaGetLastError();
-            return ATTN_ERR_NO_MEMORY;
-        }
-        if (cudaMemsetAsync(p, 0, count_bytes, stream) != cudaSuccess) {
-            cudaFreeAsync(p, stream);
-            return ATTN_ERR_CUDA;
-        }
-        w->owned = p;
-        w->arrivals = static_cast<uint32_t *>(p);
-        w->part = static_cast<char *>(p) + count_bytes;
-        w->call = 1;
-        return ATTN_OK;
+    if (cs != cudaStreamCaptureStatusNone || stream == cudaStreamPerThread)
+        return own_workspace(stream, count_bytes, part_bytes, w);
+    unsigned long long id = 0;
+    if (cudaStreamGetId(stream, &id) != cudaSuccess) {
+        cudaGetLastError();
+        return ATTN_ERR_CUDA;
     }
     w->lock = std::unique_lock<std::mutex>(g_ws_mu);
     PackWs *e = nullptr;
@@ -145,12 +160,17 @@ attn_status_t get_workspace(int dev, cudaStream_t stream, int n, size_t part_byt
     if (e == nullptr) {
         PackWs x;
         x.stream = stream;
+        x.id = id;
         try {
             g_ws[dev].push_back(x);
         } catch (...) {  // no exception leaves the library
             return ATTN_ERR_NO_MEMORY;
         }
         e = &g_ws[dev].back();
+    }
+    if (e->id != id) {
+        w->lock.unlock();
+        return own_workspace(stream, count_bytes, part_bytes, w);
     }
     if (e->n_arrivals < n) {
         void *p = nullptr;

@@ -154,8 +154,10 @@ attn_status_t attn_bwd_causal(const void *q, const void *k, const void *v, const
  * with the partials (calls on a stream are ordered, so each reuses them;
  * grown stream-ordered on demand, freed by attn_release_workspace). With
  * sq > 1 the partials come from the same per-stream workspace and a second
- * kernel reduces them. While the stream is being captured into a graph, the
- * partials are taken per call as below and the second kernel reduces.
+ * kernel reduces them. While the stream is being captured into a graph, on
+ * cudaStreamPerThread, and on a stream whose handle was a destroyed stream's
+ * before, the partials are taken per call as below and the second kernel
+ * reduces.
  * num_splits = 0 lets attn_decode_num_splits() choose; a positive value is
  * clamped to the number of key blocks. With one split the first kernel
  * writes O and LSE directly and no workspace is used. Any sq >= 1 is
@@ -164,7 +166,7 @@ attn_status_t attn_bwd_causal(const void *q, const void *k, const void *v, const
  * forward kernel, so each K/V byte is read once for all query rows of a
  * head (the issue's case of 1 to 10 new tokens); its key blocks are tiles of
  * 128 keys and a requested count is lowered so that no split is empty.
- * Under graph capture the per-call workspace is taken stream-ordered from
+ * The per-call workspace is taken stream-ordered from
  * the device's default memory pool and returned after the reduce; it is
  * kept cached in the pool until attn_release_workspace().
  */
@@ -274,9 +276,10 @@ attn_status_t attn_decode_paged(const void *q, const void *k_pages, const void *
  * of a row tile's keys that went to several SMs are joined in a fixed order,
  * so the same call gives the same bits. Workspace (fp32 partial results, at
  * most 80 MB) and arrival counters are kept per stream and freed by
- * attn_release_workspace(); while the stream is being captured into a graph
- * (and on cudaStreamPerThread) they are taken from the device's memory pool
- * for the call alone. Errors as attn_fwd.
+ * attn_release_workspace(); while the stream is being captured into a graph,
+ * on cudaStreamPerThread, and on a stream whose handle was a destroyed
+ * stream's before, they are taken from the device's memory pool for the call
+ * alone. Errors as attn_fwd.
  */
 attn_status_t attn_fwd_packed(const void *q, const void *k, const void *v, const int32_t *cu_seqlens_q,
                               const int32_t *cu_seqlens_k, void *o, float *lse, int b, int total_q,
@@ -449,9 +452,10 @@ unsigned int attn_last_timeout_site(void);
 const char *attn_status_string(attn_status_t status);
 
 /*
- * Waits for the current device to finish its work, frees the split
- * decode's per-stream workspaces (counters and partials; the next split
- * decode on a stream makes them again) and returns the memory the device's
+ * Waits for the current device to finish its work, frees the per-stream
+ * workspaces of the split decode and of the packed and paged attention
+ * (counters and partials; the next call on a stream makes them again; those
+ * of destroyed streams go here too) and returns the memory the device's
  * default pool keeps cached to the system. No other call of this library
  * may run on the device meanwhile (from another host thread).
  */
