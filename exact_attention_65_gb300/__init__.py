@@ -177,14 +177,25 @@ def _check(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor):
     return b, sq, sk, h, d, code, idx
 
 
-def _outputs(q, out, lse, b, h, sq, idx):
+def _empty(shape, dtype, device, stream):
+    """A result made by the call, in memory of the stream that writes it: what
+    the current stream gave back may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):  # (anything with a cuda_stream will do for a call)
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _outputs(q, out, lse, b, h, sq, idx, stream):
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     elif (out.shape != q.shape or out.dtype is not q.dtype or not out.is_contiguous()
           or out.get_device() != idx):
         raise ValueError("out must be a contiguous tensor like q")
     if lse is None:
-        lse = torch.empty((b, h, sq), dtype=torch.float32, device=q.device)
+        lse = _empty((b, h, sq), torch.float32, q.device, stream)
     elif (lse.shape != (b, h, sq) or lse.dtype is not torch.float32 or not lse.is_contiguous()
           or lse.get_device() != idx):
         raise ValueError("lse must be a contiguous float32 tensor [b, h, sq]")
@@ -215,11 +226,12 @@ def attn_fwd(q, k, v, scale: float | None = None, out=None, lse=None, stream=Non
 
     q: [b, sq, h, d], k/v: [b, sk, h, d], fp16 or bf16, contiguous CUDA
     tensors; default scale 1/sqrt(d). Runs on ``stream`` (default: the
-    current stream of q's device). ``causal``: bottom-right-aligned mask
+    current stream of q's device); results that are not given are made on
+    that stream, as if it were current. ``causal``: bottom-right-aligned mask
     (query row i sees key j only if j <= i + sk - sq)."""
     b, sq, sk, h, d, dt, idx = _check(q, k, v)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    out, lse = _outputs(q, out, lse, b, h, sq, idx)
+    out, lse = _outputs(q, out, lse, b, h, sq, idx, stream)
     lib = _lib or load_library()
     fn = lib.attn_fwd_causal if causal else lib.attn_fwd
     rc = _call(fn, idx, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
@@ -282,7 +294,7 @@ def attn_decode_splitkv(q, k, v, scale: float | None = None, num_splits: int = 0
     per-split (O_i, LSE_i) with the log-sum-exp combine."""
     b, sq, sk, h, d, dt, idx = _check(q, k, v)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    out, lse = _outputs(q, out, lse, b, h, sq, idx)
+    out, lse = _outputs(q, out, lse, b, h, sq, idx, stream)
     lib = _lib or load_library()
     fn = lib.attn_decode_splitkv_causal if causal else lib.attn_decode_splitkv_ex
     rc = _call(fn, idx, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
@@ -325,7 +337,7 @@ def attn_decode_paged(q, k_pages, v_pages, block_table, seqlens_k, scale: float 
     dt = _dtype_code(q)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     idx = q.get_device()
-    out, lse = _outputs(q, out, lse, b, h, sq, idx)
+    out, lse = _outputs(q, out, lse, b, h, sq, idx, stream)
     lib = _lib or load_library()
     rc = _call(lib.attn_decode_paged_ex, idx, stream, q.data_ptr(), k_pages.data_ptr(),
                v_pages.data_ptr(), block_table.data_ptr(), seqlens_k.data_ptr(), out.data_ptr(),
@@ -352,9 +364,8 @@ def attn_bwd(q, k, v, o, lse, dout, scale: float | None = None, dq=None, dk=None
             or lse.device != q.device):
         raise ValueError("lse must be a contiguous float32 tensor [b, h, sq]")
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq, dk, dv = (_empty(x.shape, x.dtype, x.device, stream) if t is None else t
+                  for t, x in ((dq, q), (dk, k), (dv, v)))
     for name, t, ref in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         if t.shape != ref.shape or t.dtype != ref.dtype or not t.is_contiguous() or t.device != q.device:
             raise ValueError(f"{name} must be a contiguous tensor like {name[1]}")
@@ -397,7 +408,7 @@ def _array(name, t, shape, idx, dtype):
         raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor {list(shape)} on the same device")
 
 
-def _packed_q(q, cu_seqlens_q, out, lse):
+def _packed_q(q, cu_seqlens_q, out, lse, stream):
     """Sizes, dtype code, device index and token stride of packed query rows,
     with their outputs. (Kept lean: short batches issue in a few microseconds,
     and this runs on every call.)"""
@@ -426,11 +437,11 @@ def _packed_q(q, cu_seqlens_q, out, lse):
     if code is None:
         raise TypeError(f"exattn takes float16 or bfloat16 tensors, got {dt}")
     if out is None:
-        out = torch.empty((t, h, d), dtype=dt, device=q.device)
+        out = _empty((t, h, d), dt, q.device, stream)
     elif out.shape != q.shape or out.dtype is not dt or not out.is_contiguous() or out.get_device() != idx:
         raise ValueError("out must be a contiguous tensor with q's shape and dtype")
     if lse is None:
-        lse = torch.empty((h, t), dtype=_F32, device=q.device)
+        lse = _empty((h, t), _F32, q.device, stream)
     elif (lse.shape != (h, t) or lse.dtype is not _F32 or not lse.is_contiguous()
           or lse.get_device() != idx):
         raise ValueError("lse must be a contiguous float32 tensor [h, total_q]")
@@ -474,7 +485,7 @@ def attn_fwd_packed(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int = 0,
     bottom-right-aligned mask of each sequence's own lengths. Returns out
     [total_q, h, d] and lse [h, total_q]; rows of no sequence are left as
     they were."""
-    b, t, h, d, dt, idx, qs, out, lse = _packed_q(q, cu_seqlens_q, out, lse)
+    b, t, h, d, dt, idx, qs, out, lse = _packed_q(q, cu_seqlens_q, out, lse, stream)
     tk, hk, ks, vs = _packed_kv(q, k, v, cu_seqlens_k, b, h, d, idx)
     lib = _lib or load_library()
     rc = _call(lib.attn_fwd_packed, idx, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
@@ -496,7 +507,7 @@ def attn_bwd_packed(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, scale: fl
     not given); rows of no sequence are left as they were."""
     if o is None or lse is None:
         raise ValueError("o and lse must be the forward's results")
-    b, t, h, d, dt, idx, qs, o, lse = _packed_q(q, cu_seqlens_q, o, lse)
+    b, t, h, d, dt, idx, qs, o, lse = _packed_q(q, cu_seqlens_q, o, lse, stream)
     tk, hk, ks, vs = _packed_kv(q, k, v, cu_seqlens_k, b, h, d, idx)
     if not isinstance(dout, torch.Tensor) or dout.shape != q.shape or dout.dtype is not q.dtype \
             or not dout.is_contiguous() or dout.get_device() != idx:
@@ -504,7 +515,7 @@ def attn_bwd_packed(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, scale: fl
     grads, strides = [], []
     for name, x, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         if x is None:
-            x = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+            x = _empty(like.shape, like.dtype, like.device, stream)
         strides.append(_rows(name, x, idx, q.dtype))
         if x.shape != like.shape:
             raise ValueError(f"{name} must have {name[1]}'s shape")
@@ -549,7 +560,7 @@ def attn_chunk_paged(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens_k, 
     seqlens_k: int32 [b] keys per request with the new ones. ``causal``: the
     bottom-right-aligned mask against each request's own key count. Other
     arguments and results as attn_fwd_packed."""
-    b, t, h, d, dt, idx, qs, out, lse = _packed_q(q, cu_seqlens_q, out, lse)
+    b, t, h, d, dt, idx, qs, out, lse = _packed_q(q, cu_seqlens_q, out, lse, stream)
     num_pages, page_size, hk, dk = _pools(k_pages, v_pages, idx, q.dtype)
     if dk != d or hk < 1 or h % hk:
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, pages {tuple(k_pages.shape)}")
@@ -586,15 +597,15 @@ def attn_paged_plan(seqlens_k, new_lens, block_table, free_pages, free_count, pa
         raise ValueError("seqlens_k must be an int32 CUDA tensor [b] (there is no CPU path)")
     b, idx = seqlens_k.shape[0], seqlens_k.get_device()
     if cu_seqlens_q is None:
-        cu_seqlens_q = torch.empty(b + 1, dtype=_I32, device=seqlens_k.device)
+        cu_seqlens_q = _empty(b + 1, _I32, seqlens_k.device, stream)
     if seqlens_out is None:
-        seqlens_out = torch.empty(b, dtype=_I32, device=seqlens_k.device)
+        seqlens_out = _empty(b, _I32, seqlens_k.device, stream)
     if free_left is None:
-        free_left = torch.empty(1, dtype=_I32, device=seqlens_k.device)
+        free_left = _empty(1, _I32, seqlens_k.device, stream)
     if slot_map is None:
         if max_tokens is None:
             raise ValueError("give max_tokens or slot_map")
-        slot_map = torch.empty(int(max_tokens), dtype=_I64, device=seqlens_k.device)
+        slot_map = _empty(int(max_tokens), _I64, seqlens_k.device, stream)
     elif max_tokens is not None and int(max_tokens) != slot_map.numel():
         raise ValueError("slot_map must have max_tokens entries")
     for name, t, n in (("block_table", block_table, 2), ("free_pages", free_pages, 1), ("slot_map", slot_map, 1)):
@@ -657,7 +668,7 @@ def attn_decode_splitkv_noalloc(q, k, v, out, lse, scale: float | None = None,
     if out is None or lse is None:
         raise ValueError("out and lse must be given: this entry point allocates nothing")
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    out, lse = _outputs(q, out, lse, b, h, sq, idx)
+    out, lse = _outputs(q, out, lse, b, h, sq, idx, stream)
     lib = _lib or load_library()
     rc = _call(lib.attn_decode_splitkv_noalloc, idx, stream, q.data_ptr(), k.data_ptr(),
                v.data_ptr(), out.data_ptr(), lse.data_ptr(), b, sq, sk, h, d, scale,
