@@ -272,11 +272,6 @@ attn_status_t device_info(int *dev, uint32_t **status, int *num_sms) {
     return ATTN_OK;
 }
 
-cudaStream_t device_side_stream(cudaStream_t stream) {
-    DeviceState *ds = nullptr;
-    return device_state(&ds) == ATTN_OK ? side_stream(ds, stream) : nullptr;
-}
-
 }  // namespace exattn
 
 namespace {

@@ -326,8 +326,6 @@ bool encode_dims(CUtensorMap *map, const void *base, bool bf16, const uint64_t (
 CUtensorMapSwizzle fwd_swizzle(int d);
 // The current device: its status word and SM count (made ready on first use).
 attn_status_t device_info(int *dev, uint32_t **status, int *num_sms);
-// The backward's second compute stream; nullptr while `stream` is captured.
-cudaStream_t device_side_stream(cudaStream_t stream);
 // Frees what the packed entry points keep per stream on device `dev`.
 void packed_release(int dev);
 
