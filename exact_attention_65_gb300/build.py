@@ -26,7 +26,7 @@ LIB = os.path.join(PKG, "libexattn.so")
 SOURCES = ["fwd.cu", "fwd_packed.cu", "chunk_paged.cu", "bwd.cu", "fwd_short.cu", "bwd_packed.cu",
            "bwd_short.cu", "decode.cu", "api.cu", "api_packed.cu", "paged_tables.cu",
            "decode_noalloc.cu"]
-HEADERS = [os.path.join(CSRC, h) for h in ("internal.h", "ptx.cuh", "packed_sched.h", "packed_dev.cuh",
+HEADERS = [os.path.join(CSRC, h) for h in ("internal.h", "ptx.cuh", "packed.h", "packed_sched.h", "packed_dev.cuh",
                                            "fwd_packed.cuh")] + [os.path.join(INCLUDE, "exattn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC]

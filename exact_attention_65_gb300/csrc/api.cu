@@ -11,6 +11,7 @@
 
 #include "exattn.h"
 #include "internal.h"
+#include "packed.h"
 
 using namespace exattn;
 

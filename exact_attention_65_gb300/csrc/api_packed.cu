@@ -7,7 +7,7 @@
 #include <vector>
 
 #include "exattn.h"
-#include "internal.h"
+#include "packed.h"
 
 using namespace exattn;
 

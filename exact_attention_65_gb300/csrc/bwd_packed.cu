@@ -43,7 +43,7 @@
 
 #include <type_traits>
 
-#include "internal.h"
+#include "packed.h"
 #include "packed_dev.cuh"
 #include "ptx.cuh"
 

@@ -46,7 +46,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "internal.h"
+#include "packed.h"
 #include "packed_dev.cuh"
 #include "ptx.cuh"
 

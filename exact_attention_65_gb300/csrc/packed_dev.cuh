@@ -4,7 +4,7 @@
 // next.
 #pragma once
 
-#include "internal.h"
+#include "packed.h"
 #include "packed_sched.h"
 #include "ptx.cuh"
 

@@ -3,7 +3,7 @@
 // (attn_paged_write).
 #include <cuda_runtime.h>
 
-#include "internal.h"
+#include "packed.h"
 
 namespace exattn {
 namespace {
