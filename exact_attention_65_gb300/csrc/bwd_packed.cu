@@ -139,10 +139,14 @@ __device__ __forceinline__ int sequence_of(const SeqArrays &s, int tok) {
 // pass over both, bound by HBM.
 //
 // D = sum_j P_j dP_j = sum_t dO O. O was rounded to 16 bits, which puts an error
-// of up to u |dO| |O| (u = eps / 2) into every dS = P (dP - D) of the row. For a
-// row that sees many keys |O| is small beside |dP|; for one that sees few it
-// is not (with one key dS is 0, and the error would be all that is left), so
-// rows that see at most kFewKeys keys form the sum over the keys, in fp32.
+// of up to u |dO| |O| (u = eps / 2) into every dS = P (dP - D) of the row. Where a
+// row's weights are spread over many keys |O| is small beside |dP|; where most
+// of the weight lies on few keys it is not, and dS itself is small (with all of
+// it on one key dS is 0, and the error would be all that is left). Rows that
+// see at most kFewKeys keys, which are always of the second kind, form the sum
+// over the keys, in fp32. Longer rows that put their weight on one key keep the
+// error, as attn_bwd does for every row: telling them apart would take P, which
+// only the main kernel has.
 constexpr int kFewKeys = 16;
 
 template <int D, bool BF16>
