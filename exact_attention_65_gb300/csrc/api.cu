@@ -117,6 +117,7 @@ struct DeviceState {
 
 DeviceState g_dev[kMaxDevices];
 std::mutex g_mu;
+std::mutex g_ws_mu;  // of the stream_ws lists, and of the calls that use one
 unsigned int g_last_site = 0;
 
 }  // namespace
@@ -196,9 +197,11 @@ cudaStream_t side_stream(DeviceState *ds, cudaStream_t stream) {
 // concurrently, on the per-thread default stream (one handle, many streams),
 // and on a stream whose handle was another stream's before (what that one
 // still has to do is not ordered with it): the caller then takes a workspace
-// per call and the separate reduce kernel.
+// per call and the separate reduce kernel. Where there is one, *lock is held
+// until the caller has enqueued its kernels: another host thread's call on the
+// stream may neither replace the buffers nor come between them.
 bool stream_workspace(DeviceState *ds, cudaStream_t stream, int64_t n, size_t part_bytes,
-                      uint32_t **counters, void **part) {
+                      uint32_t **counters, void **part, std::unique_lock<std::mutex> *lock) {
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     unsigned long long id = 0;
     if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) {
@@ -210,12 +213,16 @@ bool stream_workspace(DeviceState *ds, cudaStream_t stream, int64_t n, size_t pa
         cudaGetLastError();
         return false;
     }
-    std::lock_guard<std::mutex> lock(g_mu);
+    std::unique_lock<std::mutex> held(g_ws_mu);
     DeviceState::StreamWs *e = nullptr;
     for (auto &x : ds->stream_ws)
         if (x.stream == stream) e = &x;
     if (e == nullptr) {
-        ds->stream_ws.push_back(DeviceState::StreamWs{stream, id, nullptr, 0, nullptr, 0});
+        try {
+            ds->stream_ws.push_back(DeviceState::StreamWs{stream, id, nullptr, 0, nullptr, 0});
+        } catch (...) {  // no exception leaves the library
+            return false;
+        }
         e = &ds->stream_ws.back();
     }
     if (e->id != id) return false;
@@ -248,6 +255,7 @@ bool stream_workspace(DeviceState *ds, cudaStream_t stream, int64_t n, size_t pa
     }
     *counters = e->counters;
     *part = e->part;
+    *lock = std::move(held);
     return true;
 }
 
@@ -298,16 +306,17 @@ attn_status_t alloc_partials(int64_t splits, int b, int sq, int h, int d, cudaSt
 // Partials of the tensor-core kernel over key ranges: the stream's own
 // workspace (kept per stream: no allocation per call), or, while the stream
 // is being captured into a graph, a workspace of the call's own, returned in
-// *owned for the caller to free after the reduce.
+// *owned for the caller to free after the reduce. *lock: as stream_workspace().
 attn_status_t range_partials(DeviceState *ds, int64_t splits, int b, int sq, int h, int d,
-                             cudaStream_t stream, void **owned, float **o_part, float **lse_part) {
+                             cudaStream_t stream, void **owned, float **o_part, float **lse_part,
+                             std::unique_lock<std::mutex> *lock) {
     const int64_t rows = static_cast<int64_t>(b) * sq * h;
     const size_t o_bytes = static_cast<size_t>(splits * rows * d) * sizeof(float);
     const size_t l_bytes = static_cast<size_t>(splits * rows) * sizeof(float);
     uint32_t *counters = nullptr;
     void *part = nullptr;
     *owned = nullptr;
-    if (stream_workspace(ds, stream, 1, o_bytes + l_bytes, &counters, &part)) {
+    if (stream_workspace(ds, stream, 1, o_bytes + l_bytes, &counters, &part, lock)) {
         *o_part = static_cast<float *>(part);
         *lse_part = reinterpret_cast<float *>(static_cast<char *>(part) + o_bytes);
         return ATTN_OK;
@@ -325,8 +334,9 @@ attn_status_t run_split_decode(DeviceState *ds, int d, bool bf16, const CUtensor
     const size_t l_bytes = static_cast<size_t>(a.splits * rows) * sizeof(float);
     uint32_t *counters = nullptr;
     void *part = nullptr;
+    std::unique_lock<std::mutex> lock;
     if (stream_workspace(ds, stream, static_cast<int64_t>(a.b) * cdiv(a.sq, dec_rows_per_cta(a.sq)) * a.h,
-                         o_bytes + l_bytes, &counters, &part)) {
+                         o_bytes + l_bytes, &counters, &part, &lock)) {
         a.arrivals = counters;
         a.o_part = static_cast<float *>(part);
         a.lse_part = reinterpret_cast<float *>(static_cast<char *>(part) + o_bytes);
@@ -440,7 +450,8 @@ attn_status_t run_fwd(const void *q, const void *k, const void *v, void *o, floa
     if (splits == 1)
         return launch_fwd(d, bf16, tq, tk, tv, a, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
     void *ws = nullptr;
-    attn_status_t st = range_partials(ds, splits, b, sq, h, d, stream, &ws, &a.o_part, &a.lse_part);
+    std::unique_lock<std::mutex> lock;
+    attn_status_t st = range_partials(ds, splits, b, sq, h, d, stream, &ws, &a.o_part, &a.lse_part, &lock);
     if (st != ATTN_OK) return st;
     cudaError_t e = launch_fwd(d, bf16, tq, tk, tv, a, stream);
     if (e == cudaSuccess)
@@ -508,7 +519,8 @@ attn_status_t run_fwd_paged(const void *q, const void *k_pages, const void *v_pa
     if (splits == 1)
         return launch_fwd(d, bf16, tq, tk, tv, a, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
     void *ws = nullptr;
-    attn_status_t st = range_partials(ds, splits, b, sq, h, d, stream, &ws, &a.o_part, &a.lse_part);
+    std::unique_lock<std::mutex> lock;
+    attn_status_t st = range_partials(ds, splits, b, sq, h, d, stream, &ws, &a.o_part, &a.lse_part, &lock);
     if (st != ATTN_OK) return st;
     cudaError_t e = launch_fwd(d, bf16, tq, tk, tv, a, stream);
     if (e == cudaSuccess)
@@ -1012,7 +1024,7 @@ void attn_release_workspace(void) {
     if (cudaGetDevice(&dev) != cudaSuccess) return;
     cudaDeviceSynchronize();
     if (dev < kMaxDevices) {
-        std::lock_guard<std::mutex> lock(g_mu);
+        std::lock_guard<std::mutex> lock(g_ws_mu);
         for (auto &x : g_dev[dev].stream_ws) {
             if (x.counters) cudaFree(x.counters);
             if (x.part) cudaFree(x.part);
