@@ -242,10 +242,9 @@ inline Place place_in_seq(const LineShape &s, int seq, int sq, int sk, int rem) 
 
 // Whether part c begins inside a unit that begins at x0, costs `cost` and has n
 // steps, away from its ends: where it cuts it. The parts that share a unit are
-// the one before the first cut, and one per cut (part 0 begins the line and
-// cuts nothing, so there is one before).
+// the one before the first cut, and one per cut (part 0 begins at 0, where the
+// line begins: it cuts nothing, so there is one before).
 EXATTN_HD bool part_cuts(const LineShape &s, const LineDeal &d, int c, int x0, int cost, int n) {
-    if (c == 0) return false;
     const int x = part_begin(d, c) - x0;
     if (x <= 0 || x >= cost) return false;
     const int t = place_step(s, x, cost, n);
