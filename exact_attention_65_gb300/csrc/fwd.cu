@@ -416,6 +416,20 @@ __device__ __forceinline__ void fwd_mma(uint32_t sbase, uint32_t tmem, int nqb, 
         const Unit x = unit_of<SPLIT, PAGED>(u, nqb, nkv, a);
         const int qbuf = it_u % G::QBUF;
         if (!mbar_wait(bar(G::BAR_QF + qbuf), (it_u / G::QBUF) & 1, g, 4)) break;
+        if constexpr (SPLIT != 0) {
+            // A unit that sees no key has nothing to wait for below and hands over
+            // at once. But O full may not run two phases ahead of the epilogue,
+            // whose wait could not tell them apart by the parity. (Here rather
+            // than at the hand-over, where the wait made the issuer's loop
+            // slower: b4 s512 h32 causal 26.6 -> 28.7 us, b1 s8192 420 -> 430;
+            // here 26.6 and 424.)
+            if (x.nkv == 0) {
+#pragma unroll
+                for (int t = 0; t < G::QT; ++t)
+                    if (t < x.n_qt && !mbar_wait(bar(G::BAR_OE + t), (o_cnt[t] & 1) ^ 1, g, 7)) ok = false;
+                if (!ok) break;
+            }
+        }
         if constexpr (ONE) {
             // One live query tile: S of key tile j goes to the S columns of
             // tile (j & 1), so S_{j+1} is made while the softmax works on
@@ -489,10 +503,7 @@ __device__ __forceinline__ void fwd_mma(uint32_t sbase, uint32_t tmem, int nqb, 
                 if (j + 2 < x.nkv) ok = issue_s(j + 2);
             }
             if (!ok) break;
-            if (x.nkv == 0) {  // a unit that sees no key
-                // O full may not run two phases ahead of the epilogue: its
-                // wait could not tell them apart by the parity
-                if (!mbar_wait(bar(G::BAR_OE), (o_cnt[0] & 1) ^ 1, g, 7)) break;
+            if (x.nkv == 0) {  // causal: a unit that sees no key
                 mma_commit(bar(G::BAR_QE + qbuf));
                 mma_commit(bar(G::BAR_OF));
             }
@@ -564,14 +575,6 @@ __device__ __forceinline__ void fwd_mma(uint32_t sbase, uint32_t tmem, int nqb, 
                         if (j == x.nkv - 1) mma_commit(bar(G::BAR_QE + qbuf));  // ... and of this Q
                     }
                 } else {
-                    // a unit that sees no key waited for nothing so far: O full
-                    // may not run two phases ahead of the epilogue
-                    if constexpr (SPLIT != 0) {
-                        if (x.nkv == 0 && !mbar_wait(bar(G::BAR_OE + t), (o_cnt[t] & 1) ^ 1, g, 7)) {
-                            ok = false;
-                            break;
-                        }
-                    }
                     mma_commit(bar(G::BAR_OF + t));
                 }
             }
