@@ -259,7 +259,7 @@ attn_status_t attn_decode_paged(const void *q, const void *k_pages, const void *
  * dout and the page pools are contiguous. lse is fp32 [h, total_q].
  * Values of another sequence, of rows behind the last sequence, and stale
  * values in a page never reach a result, whatever they are; a row's own keys
- * are taken to be finite.
+ * are taken to be finite. Outputs may not overlap inputs or each other.
  */
 
 /*
@@ -267,11 +267,16 @@ attn_status_t attn_decode_paged(const void *q, const void *k_pages, const void *
  * (causal != 0: attn_fwd_causal, aligned to the sequence's own lengths) over
  * its own rows.
  *   q, o    [total_q, h, d]    k, v  [total_k, h_kv, d]
- *   max_seqlen_q  the most rows a sequence has, or 0 if not known. It only
- *                 picks the kernel's form (results are right whatever it
- *                 is): units of one 128-row tile where every sequence fits
- *                 one, else of two.
- * A row that sees no key gets O = 0 and LSE = -inf. total_q, total_k >= 1.
+ *   max_seqlen_q  the most rows a sequence has, or 0 if not known (then
+ *                 taken to be total_q). It only picks the kernel's form
+ *                 (results are right whatever it is): units of one 128-row
+ *                 tile where every sequence fits one (has at most floor(128
+ *                 / (h / h_kv)) rows), else of two. Give it where it is
+ *                 known: 64 requests with a token each over up to 8192 keys,
+ *                 h32 on 8, take 150 us with it and 221 without.
+ * A row that sees no key gets O = 0 and LSE = -inf. total_q, total_k >= 1. More
+ * than 2^29 units (rows of a K/V head, floor(128 / (h / h_kv)) at a time in each
+ * sequence) are ATTN_ERR_UNSUPPORTED.
  * How the work is dealt out is decided on the device from the lengths; ranges
  * of a row tile's keys that went to several SMs are joined in a fixed order,
  * so the same call gives the same bits. Workspace (fp32 partial results, at
@@ -355,6 +360,13 @@ attn_status_t attn_chunk_paged(const void *q, const void *k_pages, const void *v
  *                slot_map, and the step must not be run as it is
  * Outputs may not overlap inputs or each other (the inputs stay as they are,
  * so a call can be repeated). Errors as attn_fwd.
+ * Two things only the caller can see, and such a step must not be run as it is
+ * either: a request with more keys than its table row holds (seqlens_out below
+ * seqlens_k + new_lens) has no slot for those past it, and tokens past
+ * max_tokens are in cu_seqlens_q but not in slot_map. free_left counts neither.
+ * Pages only leave the stack here. A finished request's go back by the caller,
+ * on the device too: its table's entries behind the first free_count, and the
+ * count raised by as many (free_pages needs room for every page of the pool).
  */
 attn_status_t attn_paged_plan(const int32_t *seqlens_k, const int32_t *new_lens, int32_t *block_table,
                               const int32_t *free_pages, const int32_t *free_count, int32_t *cu_seqlens_q,
@@ -367,7 +379,9 @@ attn_status_t attn_paged_plan(const int32_t *seqlens_k, const int32_t *new_lens,
  * and v_stride, as above) goes to row slot_map[t] of the pools seen as
  * [num_pages * page_size, h_kv, d]. Slots outside the pools (-1: a padding
  * token) are skipped. The same slot twice leaves each 16 bytes of it from one
- * of the two rows. tokens >= 1; errors as attn_fwd.
+ * of the two rows. k and v may lie in the pools (rows that move), but not in
+ * slots that the call writes, and the two pools may not overlap. tokens >= 1;
+ * errors as attn_fwd.
  */
 attn_status_t attn_paged_write(const void *k, const void *v, const int64_t *slot_map, void *k_pages,
                                void *v_pages, int64_t tokens, int h_kv, int d, int num_pages,
