@@ -33,11 +33,14 @@ void fit_line(LineShape *s, const LineBound &x) {
 
 // Where the forward's work is cut (packed_sched.h). A unit's fixed cost (Q,
 // first S, epilogue) counts as two steps of 128 keys (one: b2 s8192 h32/8 d128
-// 783 us, two: 740). Joining a cut unit costs as much as several steps of two
-// tiles, so these are cut only where a CTA's share is 16 steps, six away from
-// a unit's ends (16 prompts of 64 to 1500 tokens: 145 us with 4 and 2, 132
-// with 16 and 6); units of one tile, where a long cache has to be spread over
-// many CTAs and few rows are joined, from 4 steps on, two from the ends.
+// causal 783 us, two: 740; measured, it is one and a half). Joining a cut unit
+// costs as much as several steps of two tiles, so these are cut only where a
+// CTA's share is 16 steps, six away from a unit's ends (16 prompts of 64 to
+// 1500 tokens: 145 us with 4 and 2, 132 with 16 and 6); units of one tile, where
+// a long cache has to be spread over many CTAs and few rows are joined, from 4
+// steps on, two from the ends. These numbers come from calls with work for every
+// CTA; a small one is spread too thinly by them (one token over 900 keys on 8
+// K/V heads: 64 steps on 16 CTAs, the longest chain 6).
 LineShape pack_line(int heads, int group, bool one_tile, bool causal, const LineBound &bound) {
     LineShape s;
     s.heads = heads;

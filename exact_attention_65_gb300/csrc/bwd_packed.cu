@@ -29,10 +29,11 @@
 // that slice in the streamed tile.
 //
 // What bounds it: the chain of a step (S and dP products, P and dS, the sums),
-// which the tensor pipe and the elementwise warps share in turns: 3,950 cycles
-// per key-tile step and 3,430 per query-tile step at d = 128 in a trace of an
-// earlier form, against 2,048 and 1,536 of products (b1 s8192 h32/8 d128: 2962 us, 928 TFLOP/s on the
-// five products of the chain rule; causal 1540 us, 893 TFLOP/s).
+// which the tensor pipe and the elementwise warps share in turns: 1.82 us per
+// key-tile step and 1.59 per query-tile step at d = 128 (from s4096 to s8192 by
+// the difference, no mask, 2070 MHz), some 3,770 and 3,300 cycles against 2,048
+// and 1,536 of products (b1 s8192 h32/8 d128: 2950 us, 932 TFLOP/s on the five
+// products of the chain rule; causal 1525 us, 901 TFLOP/s).
 //
 // Roles (384 threads): warp 0 TMA producer, warp 1 MMA issuer, warp 2 stages
 // the steps' (LSE, D) and zeroes tails, warp 3 deals out units, warps 4-11
@@ -976,10 +977,16 @@ cudaError_t launch_bwd_packed_t(const CUtensorMap &tq, const CUtensorMap &tk, co
     bwd_prep_kernel<D, BF16><<<grid, 256, 0, stream>>>(a, geom);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // A short batch's main kernel starts while the first one runs: its set-up
-    // and first copies need nothing from it (5 sequences of up to 301 tokens,
-    // h16 d64, forward and backward: 47 -> 39 us). A long one's CTAs would be
-    // placed as SMs come free, neighbours on the work line far apart (b1 s8192
-    // h32/8 d128: 1550 -> 1759 us), so it waits.
+    // and first copies need nothing from it. A long one's CTAs would be placed as
+    // SMs come free, neighbours on the work line far apart, so it waits. Waiting
+    // against not, causal, us:
+    //   2 Mi values of q   h32/8 d128 b2 s256 36.2 30.9, b1 s512 45.3 42.3;
+    //                      h16 d64 b8 s256 37.1 31.6, b1 s2048 73.9 73.8
+    //   4 Mi               b4 s256 39.1 35.8, b1 s1024 65.8 66.5;
+    //                      b16 s256 52.4 55.3, b2 s2048 126.0 138.6
+    //   8 Mi               b8 s256 65.1 60.7, b1 s2048 149.6 159.5;
+    //                      b32 s256 98.2 114.1, b1 s8192 657 801
+    //   32 Mi              b32 s256 194.5 223.5, b1 s8192 1522 1730
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;

@@ -26,21 +26,24 @@
 // issue the MMAs of tile 0 and 1 (ONE: warp 1 S, warp 8 P V), warp 3 deals
 // out units, warps 4-7 and 8-11 softmax and epilogue of tile 0 and 1. The two
 // issuers take turns: with one thread for both tiles the tensor pipe stood
-// still while it waited and counted (b1 s8192 h32 d128, no mask: 888 us, now
-// 754).
+// still while it waited and counted (b1 s8192 h32 d128, no mask: 888 us with one,
+// 754 with two when they came in).
 //
 // V rows of a unit's last tile that lie past the sequence belong to the next
 // sequence or are stale; P is 0 there, and 0 * NaN is NaN: the issuers zero
 // those below the next multiple of 16, where the P V product stops.
 //
-// What bounds it: long prompts, the tensor pipe, whose products took about 100
-// cycles instead of 64 in a trace, probably because the softmax warps use TMEM
-// at the same time (7777 and 8192 tokens h32/8 d128 causal: 743 to 788 us, 1380
-// to 1460 TFLOP/s, 72 to 77% of the measured peak); single tokens, HBM and the
-// change from unit to unit (64 requests of up to 8192 keys, h32/8, 16-key pages:
-// 154 to 160 us, 5.8 to 6.1 TB/s, 86 to 90%); batches of short sequences, that
-// change (an estimate of 4.5 us: the epilogue, and code that the instruction
-// cache no longer holds; 16 prompts of 64 to 1500 tokens: 128 us, 830 TFLOP/s).
+// What bounds it: long prompts, the tensor pipe beside the softmax warps' use of
+// TMEM: a step of two tiles takes 1.50 us (b1 h32/8 d128 without mask, s4096 to
+// s8192 to s16384 by differences: 205, 689, 2647 us, 1341 to 1662 TFLOP/s), some
+// 3,000 cycles, of which its products need 2,048 (7777 and 8192 tokens causal:
+// 743 to 803 us, 1350 to 1460 TFLOP/s, 71 to 77% of the measured peak); single
+// tokens, HBM and the change from unit to unit (64 requests of up to 8192 keys,
+// h32/8, 16-key pages: 148 to 160 us, 5.8 to 6.3 TB/s, 86 to 93%); batches of
+// short sequences, three things about equally: a unit costs 2.2 to 2.7 us besides
+// its steps (units of 1 to 8 steps, 8 and 16 to a CTA), the call some 11 us, and
+// the shares are uneven where units are short (16 prompts of 64 to 1500 tokens:
+// 80 on the fullest CTA against 70 on average; 127 us, 830 TFLOP/s).
 #pragma once
 
 #include <cuda_bf16.h>
