@@ -7,6 +7,7 @@ import ctypes
 import random
 
 import pytest
+import torch
 
 import exact_attention_65_gb300 as ea
 from test_packed_abi import BWD, BWD_OK, CHUNK, CHUNK_OK, FWD, FWD_OK, call
@@ -82,3 +83,54 @@ def test_refuses_more_units_than_are_counted(exattn_lib, fn, order, ok, kw):
     wide = {x: 65535 * 16 for x in ("qs", "ks", "vs", "dqs", "dks", "dvs")}
     args = dict(ok, b=65535, h=65535, hk=65535, d=16, **wide, **kw)
     assert call(getattr(exattn_lib, fn), order, **args) == ea.ATTN_ERR_UNSUPPORTED
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def guarded(rows, *tail, dtype=torch.float16):
+    """Room for `rows` rows between two rows of 7.0."""
+    x = torch.full((rows + 2, *tail), 7.0, dtype=dtype, device="cuda")
+    return x, x[1:rows + 1]
+
+
+def untouched(x):
+    return bool(torch.all(x[0] == 7.0) and torch.all(x[-1] == 7.0))
+
+
+OUT_OF_ORDER = [
+    (64, [0, 64, 0, 64]),
+    (64, [64, 10, 64, 64]),
+    (300, [0] + [300, 0] * 35 + [300]),                    # more than 32 sequences
+    (1 << 20, [(1 << 20) * (i % 2) for i in range(65)]),   # costs that wrap
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cu", OUT_OF_ORDER, ids=["three", "descending", "many", "wrapping"])
+@pytest.mark.parametrize("hint", [0, 1])
+def test_nothing_outside_the_tensors_is_touched(gpu, rows, cu, hint):
+    h, h_kv, d = 4, 1, 16
+    q, k, v = (torch.randn(rows, n, d, device="cuda").half() for n in (h, h_kv, h_kv))
+    starts = ints(cu)
+    frame, out = guarded(rows, h, d)
+    lse_frame = torch.full((h * rows + 2,), 7.0, device="cuda")
+    lse = lse_frame[1:-1].view(h, rows)
+    gpu.attn_fwd_packed(q, k, v, starts, starts, max_seqlen_q=hint, out=out, lse=lse, causal=True)
+    frames = [guarded(rows, n, d) for n in (h, h_kv, h_kv)]
+    gpu.attn_bwd_packed(q, k, v, torch.zeros_like(q), torch.zeros(h, rows, device="cuda"), torch.randn_like(q), starts,
+                        starts, dq=frames[0][1], dk=frames[1][1], dv=frames[2][1], causal=True)
+    b = len(cu) - 1
+    pages = torch.randn(8, 16, h_kv, d, device="cuda").half()
+    table = torch.zeros(b, 2, dtype=torch.int32, device="cuda")
+    paged_frame, paged = guarded(rows, h, d)
+    gpu.attn_chunk_paged(q, pages, pages.clone(), table, starts, ints([20] * b), max_seqlen_q=hint, out=paged, causal=True)
+    assert gpu.attn_get_device_status() == gpu.ATTN_OK
+    assert all(untouched(x) for x in (frame, paged_frame, *(x for x, _ in frames)))
+    assert lse_frame[0] == 7.0 and lse_frame[-1] == 7.0
+    # and the next call is as ever
+    good = ints([0, rows // 2, rows])
+    first = gpu.attn_fwd_packed(q, k, v, good, good, causal=True)
+    again = gpu.attn_fwd_packed(q, k, v, good, good, causal=True)
+    assert all(torch.equal(x, y) for x, y in zip(first, again)) and torch.isfinite(first[0].float()).all()
