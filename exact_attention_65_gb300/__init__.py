@@ -91,6 +91,14 @@ def load_library() -> ctypes.CDLL:
         lib.attn_paged_plan.argtypes = [vp] * 9 + [i32] * 4 + [i64, vp]
         lib.attn_paged_write.restype = i32
         lib.attn_paged_write.argtypes = [vp] * 5 + [i64] + [i32] * 4 + [i64] * 2 + [i32, vp]
+        lib.attn_paged_append.restype = i32
+        lib.attn_paged_append.argtypes = [vp] * 9 + [i64] * 2 + [i32] * 7 + [i64] * 4 + [i32, vp]
+        lib.attn_paged_append_q4.restype = i32
+        lib.attn_paged_append_q4.argtypes = [vp] * 9 + [i64] * 2 + [i32] * 7 + [i64] * 4 + [f32] * 2 + [i32, vp]
+        lib.attn_paged_read_q4.restype = i32
+        lib.attn_paged_read_q4.argtypes = [vp] * 5 + [i64] + [i32] * 4 + [f32] * 2 + [i64] * 2 + [i32, vp]
+        lib.attn_q4_page_bytes.restype = i64
+        lib.attn_q4_page_bytes.argtypes = [i32] * 2
         lib.attn_debug_packed_plan.restype = i32
         lib.attn_debug_packed_plan.argtypes = [vp, vp] + [i32] * 8 + [vp]
         lib.attn_debug_packed_starts.restype = i32
@@ -668,6 +676,142 @@ def attn_paged_write(k, v, slot_map, k_pages, v_pages, stream=None):
         raise AttnError(rc, "attn_paged_write")
 
 
+def _append_args(q, k, v, cos_sin, positions, slot_map, q_out, stream):
+    """Sizes, strides, dtype code and device index of an append's rows, with
+    its output. (Kept lean: a decode step's append issues in a few microseconds.)"""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
+        raise ValueError("q must be a CUDA tensor [tokens, h, d] (there is no CPU path)")
+    idx, dt = q.get_device(), q.dtype
+    code = _dtype_code(q)
+    qs, ks, vs = _rows("q", q, idx, dt), _rows("k", k, idx, dt), _rows("v", v, idx, dt)
+    t, h, d = q.shape
+    if k.shape != v.shape or k.shape[0] != t or k.shape[2] != d:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
+    if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be a float32 tensor [max_positions, rot]")
+    _array("cos_sin", cos_sin, tuple(cos_sin.shape), idx, _F32)
+    _array("positions", positions, (t,), idx, _I64)
+    _array("slot_map", slot_map, (t,), idx, _I64)
+    if q_out is None:
+        q_out = _empty((t, h, d), dt, q.device, stream)
+    os = _rows("q_out", q_out, idx, dt)
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    return t, h, k.shape[1], d, qs, ks, vs, os, code, idx, q_out
+
+
+def attn_paged_append(q, k, v, cos_sin, positions, slot_map, k_pages, v_pages, q_out=None,
+                      interleaved: bool = False, stream=None):
+    """A step's queries and keys rotated by their positions, keys and values
+    into the pages of a paged cache; returns the rotated queries.
+
+    q: [tokens, h, d], k, v: [tokens, h_kv, d] (each may be a slice of wider
+    rows); cos_sin: float32 [max_positions, rot], row p the cosines of the rot /
+    2 angles of position p and then their sines; the first rot channels of a
+    head turn (a multiple of 16); positions: int64 [tokens]; slot_map: int64
+    [tokens] as in attn_paged_write (a token with a slot outside the pools is
+    not stored, but its queries are rotated; for a position that cos_sin does
+    not have nothing is written). ``interleaved``: channels 2 i and 2 i + 1 are
+    a pair, instead of i and i + rot / 2. q_out: [tokens, h, d], also a slice
+    of wider rows, or q itself. k_pages, v_pages: [num_pages, page_size, h_kv,
+    d], written in place; they may not overlap the rows."""
+    t, h, hk, d, qs, ks, vs, os, code, idx, q_out = _append_args(q, k, v, cos_sin, positions, slot_map, q_out, stream)
+    num_pages, page_size, ph, pd = _pools(k_pages, v_pages, idx, q.dtype)
+    if ph != hk or pd != d:
+        raise ValueError(f"shape mismatch: k {tuple(k.shape)}, pages {tuple(k_pages.shape)}")
+    lib = _lib or load_library()
+    rc = _call(lib.attn_paged_append, idx, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), cos_sin.data_ptr(),
+               positions.data_ptr(), slot_map.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+               t, cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0, h, hk, d, num_pages, page_size, qs,
+               ks, vs, os, code)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_paged_append")
+    return q_out
+
+
+def attn_q4_page_bytes(page_size: int, d: int) -> int:
+    """Bytes of a page of one head of a 4-bit cache (0: not supported)."""
+    return load_library().attn_q4_page_bytes(page_size, d)
+
+
+def _pools_q4(k_pages, v_pages, d, idx):
+    """(num_pages, h_kv, page_size) of a pair of 4-bit pools of head dim d."""
+    try:
+        shape = k_pages.shape
+        num_pages, h, block = shape
+        fine = (k_pages.dtype is torch.uint8 and v_pages.dtype is torch.uint8 and v_pages.shape == shape
+                and k_pages.get_device() == idx and v_pages.get_device() == idx and k_pages.is_contiguous()
+                and v_pages.is_contiguous())
+    except (AttributeError, ValueError, TypeError):
+        fine = False
+    if not fine:
+        raise ValueError("k_pages and v_pages must be contiguous uint8 tensors [num_pages, h_kv, page_size * 9 d / 16] "
+                         "of one shape on the rows' device")
+    # 9 d / 16 bytes of a row and head
+    if d < 16 or block % (9 * d // 16):
+        raise ValueError(f"pages {tuple(shape)} do not hold whole rows of head dim {d}")
+    return num_pages, h, block // (9 * d // 16)
+
+
+def attn_paged_append_q4(q, k, v, cos_sin, positions, slot_map, k_pages, v_pages, k_scale: float = 1.0,
+                         v_scale: float = 1.0, q_out=None, interleaved: bool = False, stream=None):
+    """attn_paged_append into a cache held in 4 bits; returns the rotated queries.
+
+    k_pages, v_pages: uint8 [num_pages, h_kv, page_size * 9 d / 16]
+    (attn_q4_page_bytes(page_size, d)), page_size a multiple of 16: per page
+    and head, rows of e2m1 codes (two to a byte) and then rows of e4m3 scales,
+    one for 16 channels. A value is code * scale * k_scale (v_scale); every
+    call on a pool gets the same scales."""
+    t, h, hk, d, qs, ks, vs, os, code, idx, q_out = _append_args(q, k, v, cos_sin, positions, slot_map, q_out, stream)
+    num_pages, ph, page_size = _pools_q4(k_pages, v_pages, d, idx)
+    if ph != hk:
+        raise ValueError(f"shape mismatch: k {tuple(k.shape)}, pages {tuple(k_pages.shape)}")
+    lib = _lib or load_library()
+    rc = _call(lib.attn_paged_append_q4, idx, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), cos_sin.data_ptr(),
+               positions.data_ptr(), slot_map.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+               t, cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0, h, hk, d, num_pages, page_size, qs,
+               ks, vs, os, k_scale, v_scale, code)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_paged_append_q4")
+    return q_out
+
+
+def attn_paged_read_q4(k_pages, v_pages, slot_map, d: int, dtype=torch.bfloat16, k_scale: float = 1.0,
+                       v_scale: float = 1.0, k=None, v=None, stream=None):
+    """Rows of a 4-bit cache in 16 bits: returns k, v [tokens, h_kv, d].
+
+    k_pages, v_pages, k_scale, v_scale: as in attn_paged_append_q4; slot_map:
+    int64 [tokens], the slot of each row (zeros come back for one outside the
+    pools). k, v may be given (then dtype is theirs), also as slices of wider
+    rows."""
+    if not isinstance(slot_map, torch.Tensor) or not slot_map.is_cuda or slot_map.dim() != 1:
+        raise ValueError("slot_map must be an int64 CUDA tensor [tokens] (there is no CPU path)")
+    idx, t = slot_map.get_device(), slot_map.shape[0]
+    _array("slot_map", slot_map, (t,), idx, _I64)
+    num_pages, h, page_size = _pools_q4(k_pages, v_pages, d, idx)
+    given = k if k is not None else v
+    if given is not None:
+        if not isinstance(given, torch.Tensor):
+            raise ValueError("k and v must be CUDA tensors [tokens, h_kv, d]")
+        dtype = given.dtype
+    code = _DTYPE_CODE.get(dtype)
+    if code is None:
+        raise TypeError(f"exattn takes float16 or bfloat16 tensors, got {dtype}")
+    if k is None:
+        k = _empty((t, h, d), dtype, slot_map.device, stream)
+    if v is None:
+        v = _empty((t, h, d), dtype, slot_map.device, stream)
+    ks, vs = _rows("k", k, idx, dtype), _rows("v", v, idx, dtype)
+    if tuple(k.shape) != (t, h, d) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [{t}, {h}, {d}]")
+    lib = _lib or load_library()
+    rc = _call(lib.attn_paged_read_q4, idx, stream, k_pages.data_ptr(), v_pages.data_ptr(), slot_map.data_ptr(),
+               k.data_ptr(), v.data_ptr(), t, h, d, num_pages, page_size, k_scale, v_scale, ks, vs, code)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_paged_read_q4")
+    return k, v
+
+
 def attn_decode_splitkv_noalloc(q, k, v, out, lse, scale: float | None = None,
                                 num_splits: int = 0, stream=None):
     """attn_decode_splitkv for callers that cannot allocate device memory:
@@ -728,6 +872,7 @@ def attn_debug_set_flags(flags: int) -> None:
 __all__ = [
     "AttnError", "attn_fwd", "attn_fwd_host", "attn_bwd", "attn_decode_splitkv",
     "attn_decode_paged", "attn_fwd_packed", "attn_bwd_packed", "attn_chunk_paged", "attn_paged_plan", "attn_paged_write",
+    "attn_paged_append", "attn_paged_append_q4", "attn_paged_read_q4", "attn_q4_page_bytes",
     "attn_decode_splitkv_noalloc", "attn_get_noalloc_status",
     "attn_decode_num_splits",
     "attn_decode_num_splits_for_sms", "attn_get_device_status", "attn_last_timeout_site",

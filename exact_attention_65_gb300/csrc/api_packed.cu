@@ -8,6 +8,7 @@
 
 #include "exattn.h"
 #include "packed.h"
+#include "q4.cuh"
 
 using namespace exattn;
 
@@ -362,6 +363,78 @@ LineShape plan_shape(int h, int h_kv, int one_tile, int causal, int by_key, cons
                   : pack_line(h_kv, h / h_kv, one_tile != 0, causal != 0, bound);
 }
 
+// Rows of h_kv heads: 16-byte words (32-byte groups) of a call, so that a grid's
+// blocks of them fit 31 bits.
+constexpr int64_t kMaxAppend = 1ll << 38;
+
+// What the calls on 4-bit pages check besides. The scales' range keeps every
+// unit, 2^-9 .. 448 times a scale, and its reciprocal normal numbers.
+attn_status_t check_q4(int page_size, float k_scale, float v_scale) {
+    for (float s : {k_scale, v_scale})
+        if (!(s >= 0x1p-64f && s <= 0x1p64f)) return ATTN_ERR_INVALID_ARG;
+    return page_size % 16 == 0 ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
+}
+
+attn_status_t fill_append(AppendArgs *a, const void *q, const void *k, const void *v, const float *cos_sin,
+                          const int64_t *positions, const int64_t *slot_map, void *q_out, void *k_pages,
+                          void *v_pages, int64_t tokens, int64_t max_positions, int rot, int interleaved, int h,
+                          int h_kv, int d, int num_pages, int page_size, int64_t q_stride, int64_t k_stride,
+                          int64_t v_stride, int64_t q_out_stride, int dtype) {
+    for (const void *p : {q, k, v, static_cast<const void *>(cos_sin), static_cast<const void *>(q_out),
+                          static_cast<const void *>(k_pages), static_cast<const void *>(v_pages)})
+        if (!p || misaligned(p, 16)) return ATTN_ERR_INVALID_ARG;
+    for (const void *p : {positions, slot_map})
+        if (!p || misaligned(p, 8)) return ATTN_ERR_INVALID_ARG;
+    if (tokens < 1 || max_positions < 1 || h < 1 || h_kv < 1 || num_pages < 1 || page_size < 1)
+        return ATTN_ERR_INVALID_ARG;
+    if (dtype != ATTN_FP16 && dtype != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+    if (d != 16 && d != 32 && d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+    // halves of the rotated part are whole 16-byte words
+    if (rot < 16 || rot > d || rot % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+    if (h > 65535 || h_kv > 65535 || tokens > 0x7fffffffLL || max_positions > 0x7fffffffLL)
+        return ATTN_ERR_UNSUPPORTED;
+    const int64_t qrow = static_cast<int64_t>(h) * d, krow = static_cast<int64_t>(h_kv) * d;
+    attn_status_t st = check_stride(q_stride, qrow);
+    if (st == ATTN_OK) st = check_stride(q_out_stride, qrow);
+    if (st == ATTN_OK) st = check_stride(k_stride, krow);
+    if (st == ATTN_OK) st = check_stride(v_stride, krow);
+    if (st != ATTN_OK) return st;
+    a->q = static_cast<const uint4 *>(q);
+    a->k = static_cast<const uint4 *>(k);
+    a->v = static_cast<const uint4 *>(v);
+    a->q_out = static_cast<uint4 *>(q_out);
+    a->cos_sin = cos_sin;
+    a->positions = positions;
+    a->slot_map = slot_map;
+    a->k_pages = k_pages;
+    a->v_pages = v_pages;
+    a->tokens = tokens;
+    a->max_positions = max_positions;
+    a->slots = static_cast<int64_t>(num_pages) * page_size;
+    a->q_stride = q_stride / 8;
+    a->k_stride = k_stride / 8;
+    a->v_stride = v_stride / 8;
+    a->q_out_stride = q_out_stride / 8;
+    a->h = h;
+    a->h_kv = h_kv;
+    a->d = d;
+    a->rot = rot;
+    a->interleaved = interleaved ? 1 : 0;
+    a->page_size = page_size;
+    a->k_scale = a->v_scale = 1.0f;
+    a->k_six = a->v_six = 6.0f;
+    a->block = a->codes = 0;
+    return ATTN_OK;
+}
+
+attn_status_t run_append(const AppendArgs &a, int dtype, bool q4, cudaStream_t stream) {
+    int dev = 0, sms = 0;
+    uint32_t *status = nullptr;
+    const attn_status_t st = device_info(&dev, &status, &sms);
+    if (st != ATTN_OK) return st;
+    return launch_append(a, dtype == ATTN_BF16, q4, sms, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -676,6 +749,85 @@ attn_status_t attn_paged_write(const void *k, const void *v, const int64_t *slot
     a.slots = static_cast<int64_t>(num_pages) * page_size;
     if (a.tokens * a.words > (1ll << 40)) return ATTN_ERR_UNSUPPORTED;
     return launch_paged_write(a, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int64_t attn_q4_page_bytes(int page_size, int d) {
+    if ((d != 16 && d != 32 && d != 64 && d != 128) || page_size < 16 || page_size % 16 != 0) return 0;
+    return q4_block_bytes(page_size, d);
+}
+
+attn_status_t attn_paged_append(const void *q, const void *k, const void *v, const float *cos_sin,
+                                const int64_t *positions, const int64_t *slot_map, void *q_out, void *k_pages,
+                                void *v_pages, int64_t tokens, int64_t max_positions, int rot, int interleaved,
+                                int h, int h_kv, int d, int num_pages, int page_size, int64_t q_stride,
+                                int64_t k_stride, int64_t v_stride, int64_t q_out_stride, attn_dtype_t dtype,
+                                cudaStream_t stream) {
+    AppendArgs a;
+    const attn_status_t st =
+        fill_append(&a, q, k, v, cos_sin, positions, slot_map, q_out, k_pages, v_pages, tokens, max_positions, rot,
+                    interleaved, h, h_kv, d, num_pages, page_size, q_stride, k_stride, v_stride, q_out_stride, dtype);
+    return st == ATTN_OK ? run_append(a, dtype, false, stream) : st;
+}
+
+attn_status_t attn_paged_append_q4(const void *q, const void *k, const void *v, const float *cos_sin,
+                                   const int64_t *positions, const int64_t *slot_map, void *q_out, void *k_pages,
+                                   void *v_pages, int64_t tokens, int64_t max_positions, int rot, int interleaved,
+                                   int h, int h_kv, int d, int num_pages, int page_size, int64_t q_stride,
+                                   int64_t k_stride, int64_t v_stride, int64_t q_out_stride, float k_scale,
+                                   float v_scale, attn_dtype_t dtype, cudaStream_t stream) {
+    AppendArgs a;
+    attn_status_t st =
+        fill_append(&a, q, k, v, cos_sin, positions, slot_map, q_out, k_pages, v_pages, tokens, max_positions, rot,
+                    interleaved, h, h_kv, d, num_pages, page_size, q_stride, k_stride, v_stride, q_out_stride, dtype);
+    if (st == ATTN_OK) st = check_q4(page_size, k_scale, v_scale);
+    if (st != ATTN_OK) return st;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.k_six = 6.0f * k_scale;
+    a.v_six = 6.0f * v_scale;
+    a.block = q4_block_bytes(page_size, d);
+    a.codes = static_cast<int64_t>(page_size) * q4_code_bytes(d);
+    return run_append(a, dtype, true, stream);
+}
+
+attn_status_t attn_paged_read_q4(const void *k_pages, const void *v_pages, const int64_t *slot_map, void *k, void *v,
+                                 int64_t tokens, int h_kv, int d, int num_pages, int page_size, float k_scale,
+                                 float v_scale, int64_t k_stride, int64_t v_stride, attn_dtype_t dtype,
+                                 cudaStream_t stream) {
+    for (const void *p : {k_pages, v_pages, static_cast<const void *>(k), static_cast<const void *>(v)})
+        if (!p || misaligned(p, 16)) return ATTN_ERR_INVALID_ARG;
+    if (!slot_map || misaligned(slot_map, 8)) return ATTN_ERR_INVALID_ARG;
+    if (tokens < 1 || h_kv < 1 || num_pages < 1 || page_size < 1) return ATTN_ERR_INVALID_ARG;
+    if (dtype != ATTN_FP16 && dtype != ATTN_BF16) return ATTN_ERR_INVALID_ARG;
+    if (d != 16 && d != 32 && d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+    if (h_kv > 65535 || tokens > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+    const int64_t row = static_cast<int64_t>(h_kv) * d;
+    attn_status_t st = check_q4(page_size, k_scale, v_scale);
+    if (st == ATTN_OK) st = check_stride(k_stride, row);
+    if (st == ATTN_OK) st = check_stride(v_stride, row);
+    if (st != ATTN_OK) return st;
+    if (tokens * (row / 16) > kMaxAppend) return ATTN_ERR_UNSUPPORTED;
+    int dev = 0, sms = 0;
+    uint32_t *status = nullptr;
+    if ((st = device_info(&dev, &status, &sms)) != ATTN_OK) return st;
+    ReadQ4Args a;
+    a.k_pages = static_cast<const uint8_t *>(k_pages);
+    a.v_pages = static_cast<const uint8_t *>(v_pages);
+    a.slot_map = slot_map;
+    a.k = static_cast<uint4 *>(k);
+    a.v = static_cast<uint4 *>(v);
+    a.tokens = tokens;
+    a.slots = static_cast<int64_t>(num_pages) * page_size;
+    a.k_stride = k_stride / 8;
+    a.v_stride = v_stride / 8;
+    a.block = q4_block_bytes(page_size, d);
+    a.codes = static_cast<int64_t>(page_size) * q4_code_bytes(d);
+    a.h_kv = h_kv;
+    a.d = d;
+    a.page_size = page_size;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    return launch_read_q4(a, dtype == ATTN_BF16, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -389,6 +389,82 @@ attn_status_t attn_paged_write(const void *k, const void *v, const int64_t *slot
                                cudaStream_t stream);
 
 /*
+ * ---------------------------------------------------------------------
+ * Rotating appends and the 4-bit cache
+ *
+ * attn_paged_write with the position rotation on the way: a step's queries and
+ * keys are rotated by their positions, the keys and values go into the pages,
+ * the queries to q_out.
+ *   q, q_out     [tokens, h, d]    k, v  [tokens, h_kv, d] (token strides as
+ *                above; q_out may be q itself with q's stride)
+ *   cos_sin      fp32 [max_positions, rot], 16-byte aligned: row p holds the
+ *                cosines of the rot / 2 angles of position p, then their sines
+ *   positions    int64 [tokens]; slot_map int64 [tokens] as in attn_paged_write
+ *   rot          channels of a head that turn, from the first on: a multiple of
+ *                16, at most d (ATTN_ERR_UNSUPPORTED otherwise); the others pass
+ *   interleaved  0: channel i < rot / 2 is paired with i + rot / 2; otherwise
+ *                channels 2 i and 2 i + 1 are a pair. Pair i, (x, y), becomes
+ *                (x cos_i - y sin_i, y cos_i + x sin_i), in fp32, rounded once.
+ * A slot outside the pools (-1: a padding token) gets no key and value, but the
+ * token's queries are rotated. For a token whose position is outside 0 ..
+ * max_positions - 1 nothing is written. Channels that do not turn, and v, are
+ * copied bit by bit. Outputs may not overlap inputs (but for q_out) or each
+ * other; the same slot twice leaves each 16 bytes of it from one of the two
+ * rows. h need not be a multiple of h_kv. Errors as attn_fwd.
+ */
+attn_status_t attn_paged_append(const void *q, const void *k, const void *v, const float *cos_sin,
+                                const int64_t *positions, const int64_t *slot_map, void *q_out,
+                                void *k_pages, void *v_pages, int64_t tokens, int64_t max_positions,
+                                int rot, int interleaved, int h, int h_kv, int d, int num_pages,
+                                int page_size, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                int64_t q_out_stride, attn_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * A cache held in 4 bits. A pool is uint8 [num_pages, h_kv, page_bytes],
+ * 16-byte aligned, page_bytes = page_size * 9 d / 16 (attn_q4_page_bytes()): a
+ * page of a head holds page_size rows of d / 2 bytes of codes (channel 2 i of
+ * the row in the low half of byte i), then page_size rows of d / 16 scales.
+ *   code   e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6, and 8 more with the sign
+ *   scale  e4m3, one for 16 neighbouring channels of a row
+ *   value  code * scale * (the tensor's scale, k_scale or v_scale)
+ * page_size is a multiple of 16 (ATTN_ERR_UNSUPPORTED otherwise), k_scale and
+ * v_scale lie within 2^-64 .. 2^64 (ATTN_ERR_INVALID_ARG otherwise), and every
+ * call on a pool gets the same ones. Choose them so that the largest value of
+ * the tensor is at most 2688 times, and typical ones some 0.1 to 1000 times,
+ * its scale: a group's scale is exact to 4 bits from 2^-6 on.
+ */
+/* Bytes of a page of one head; 0 for a page size or head dim that is not supported. */
+int64_t attn_q4_page_bytes(int page_size, int d);
+
+/*
+ * attn_paged_append into 4-bit pages. Keys (rotated, not rounded before) and
+ * values: a group of 16 channels with largest magnitude m gets the scale s =
+ * e4m3(m / (6 k_scale)), a channel x the code e2m1(x / (s k_scale)), each
+ * rounded to the nearest with ties to even and limited to the largest value; s =
+ * 0 has codes 0. A group that holds an infinity or a NaN gets the scale NaN, so
+ * that what reads it gets NaN. The same slot twice leaves codes and scales of
+ * both rows side by side. Other arguments and errors as attn_paged_append.
+ */
+attn_status_t attn_paged_append_q4(const void *q, const void *k, const void *v, const float *cos_sin,
+                                   const int64_t *positions, const int64_t *slot_map, void *q_out,
+                                   void *k_pages, void *v_pages, int64_t tokens, int64_t max_positions,
+                                   int rot, int interleaved, int h, int h_kv, int d, int num_pages,
+                                   int page_size, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                   int64_t q_out_stride, float k_scale, float v_scale,
+                                   attn_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * Rows of a 4-bit cache back in 16 bits: row slot_map[t] of the pools, rounded
+ * once, to row t of k and v [tokens, h_kv, d] (token strides as above); zeros
+ * where the slot is outside the pools. A slot may come up several times. Errors
+ * as attn_fwd.
+ */
+attn_status_t attn_paged_read_q4(const void *k_pages, const void *v_pages, const int64_t *slot_map,
+                                 void *k, void *v, int64_t tokens, int h_kv, int d, int num_pages,
+                                 int page_size, float k_scale, float v_scale, int64_t k_stride,
+                                 int64_t v_stride, attn_dtype_t dtype, cudaStream_t stream);
+
+/*
  * Split-KV decode that allocates no device memory. The pages have no
  * counterpart: this is a library convenience, not part of the method.
  *

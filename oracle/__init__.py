@@ -349,3 +349,71 @@ def paged_plan(seqlens, new_lens, block_table, free_pages, free_count, page_size
         cu.append(cu[-1] + new)
         lens.append(min(old + new, width * page_size))
     return table, np.array(cu), np.array(lens), slots, left
+
+
+# ---------------------------------------------------------------- rotation and the 4-bit cache
+def rotate(x, cos_sin, positions, interleaved=False):
+    """x [t, heads, d] in float64 with the first rot channels of each head
+    turned in pairs by the angles of the token's position (cos_sin [max, rot]:
+    cosines, then sines)."""
+    x, table = _f64(x).copy(), _f64(cos_sin)[np.asarray(positions)]
+    half = table.shape[1] // 2
+    for i in range(half):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+        c, s = table[:, i, None], table[:, half + i, None]
+        x[:, :, a], x[:, :, b] = x[:, :, a] * c - x[:, :, b] * s, x[:, :, b] * c + x[:, :, a] * s
+    return x
+
+
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+E4M3 = np.array([m * 2.0 ** -9 if e == 0 else (1 + m / 8) * 2.0 ** (e - 7)
+                 for e in range(16) for m in range(8)][:127])  # (127 is NaN)
+
+
+def nearest(grid, x):
+    """Index of the grid's value nearest to each |x|; a tie goes to the even index, what is above to the last."""
+    x = np.abs(x)
+    hi = np.clip(np.searchsorted(grid, x), 1, len(grid) - 1)
+    lo = hi - 1
+    below, above = x - grid[lo], grid[hi] - x
+    return np.where((below < above) | ((below == above) & (lo % 2 == 0)), lo, hi)
+
+
+def q4_quantise(x, scale):
+    """Codes (0 .. 15) [..., d] and scale bytes [..., d / 16] of x, in float64."""
+    x = _f64(x)
+    g = x.reshape(*x.shape[:-1], -1, 16)
+    with np.errstate(invalid="ignore"):
+        m = np.abs(g).max(axis=-1)
+        fine = np.isfinite(m)
+        s = np.where(fine, nearest(E4M3, np.where(fine, m, 0.0) / (6.0 * scale)), 127)
+        unit = E4M3[np.minimum(s, 126)] * scale
+        y = np.where((unit > 0)[..., None], g / np.where(unit > 0, unit, 1.0)[..., None], 0.0)
+        code = np.where(fine[..., None], nearest(E2M1, y) + 8 * np.signbit(y), 0)
+    return code.reshape(x.shape).astype(np.uint8), s.astype(np.uint8)
+
+
+def q4_values(code, s, scale):
+    """Values of codes [..., d] with scale bytes [..., d / 16], in float64."""
+    s = np.where(s == 127, np.nan, E4M3[np.minimum(s, 126)])
+    v = E2M1[code & 7] * np.where(code & 8, -1.0, 1.0)
+    return v * np.repeat(s, 16, axis=-1) * scale
+
+
+def q4_rows(pool, d):
+    """A 4-bit pool [num_pages, h_kv, page * 9 d / 16] (uint8) as codes
+    [num_pages * page, h_kv, d] and scale bytes [num_pages * page, h_kv, d / 16]."""
+    pool = np.asarray(pool)
+    n, h, block = pool.shape
+    page = block // (9 * d // 16)
+    code = pool[:, :, :page * d // 2].reshape(n, h, page, d // 2)
+    s = pool[:, :, page * d // 2:].reshape(n, h, page, d // 16)
+    code = np.stack([code & 15, code >> 4], axis=-1).reshape(n, h, page, d)
+    return [x.transpose(0, 2, 1, 3).reshape(n * page, h, -1) for x in (code, s)]
+
+
+def q4_pool(code, s, num_pages, page):
+    """The pool of codes [num_pages * page, h_kv, d] and scale bytes: q4_rows() the other way round."""
+    code, s = (x.reshape(num_pages, page, x.shape[1], -1).transpose(0, 2, 1, 3) for x in (code, s))
+    code = code[..., 0::2] | code[..., 1::2] << 4
+    return np.concatenate([x.reshape(num_pages, x.shape[1], -1) for x in (code, s)], axis=-1).astype(np.uint8)
