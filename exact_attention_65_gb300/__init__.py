@@ -97,6 +97,8 @@ def load_library() -> ctypes.CDLL:
         lib.attn_paged_append_q4.argtypes = [vp] * 9 + [i64] * 2 + [i32] * 7 + [i64] * 4 + [f32] * 2 + [i32, vp]
         lib.attn_paged_read_q4.restype = i32
         lib.attn_paged_read_q4.argtypes = [vp] * 5 + [i64] + [i32] * 4 + [f32] * 2 + [i64] * 2 + [i32, vp]
+        lib.attn_chunk_paged_q4.restype = i32
+        lib.attn_chunk_paged_q4.argtypes = [vp] * 8 + [i32] * 9 + [i64] + [f32] * 3 + [i32, i32, vp]
         lib.attn_q4_page_bytes.restype = i64
         lib.attn_q4_page_bytes.argtypes = [i32] * 2
         lib.attn_debug_packed_plan.restype = i32
@@ -776,6 +778,34 @@ def attn_paged_append_q4(q, k, v, cos_sin, positions, slot_map, k_pages, v_pages
     return q_out
 
 
+def attn_chunk_paged_q4(q, k_pages, v_pages, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q: int = 0,
+                        scale: float | None = None, k_scale: float = 1.0, v_scale: float = 1.0, out=None, lse=None,
+                        stream=None, causal: bool = False):
+    """attn_chunk_paged over a cache held in 4 bits: attention of each
+    request's new tokens over the values that its pages hold, with grouped heads.
+
+    k_pages, v_pages, k_scale, v_scale: as in attn_paged_append_q4, which put
+    the new tokens' own rows there. Other arguments and results as
+    attn_chunk_paged."""
+    b, t, h, d, dt, idx, qs, out, lse = _packed_q(q, cu_seqlens_q, out, lse, stream)
+    num_pages, hk, page_size = _pools_q4(k_pages, v_pages, d, idx)
+    if hk < 1 or h % hk:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, pages {tuple(k_pages.shape)}")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be an int32 tensor [b, max_pages]")
+    max_pages = block_table.shape[1]
+    _array("block_table", block_table, (b, max_pages), idx, _I32)
+    _array("seqlens_k", seqlens_k, (b,), idx, _I32)
+    lib = _lib or load_library()
+    rc = _call(lib.attn_chunk_paged_q4, idx, stream, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+               block_table.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), out.data_ptr(),
+               lse.data_ptr(), b, t, max_seqlen_q, h, hk, d, num_pages, page_size, max_pages, qs,
+               1.0 / math.sqrt(d) if scale is None else float(scale), k_scale, v_scale, 1 if causal else 0, dt)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_chunk_paged_q4")
+    return out, lse
+
+
 def attn_paged_read_q4(k_pages, v_pages, slot_map, d: int, dtype=torch.bfloat16, k_scale: float = 1.0,
                        v_scale: float = 1.0, k=None, v=None, stream=None):
     """Rows of a 4-bit cache in 16 bits: returns k, v [tokens, h_kv, d].
@@ -872,7 +902,8 @@ def attn_debug_set_flags(flags: int) -> None:
 __all__ = [
     "AttnError", "attn_fwd", "attn_fwd_host", "attn_bwd", "attn_decode_splitkv",
     "attn_decode_paged", "attn_fwd_packed", "attn_bwd_packed", "attn_chunk_paged", "attn_paged_plan", "attn_paged_write",
-    "attn_paged_append", "attn_paged_append_q4", "attn_paged_read_q4", "attn_q4_page_bytes",
+    "attn_paged_append", "attn_paged_append_q4", "attn_paged_read_q4", "attn_chunk_paged_q4",
+    "attn_q4_page_bytes",
     "attn_decode_splitkv_noalloc", "attn_get_noalloc_status",
     "attn_decode_num_splits",
     "attn_decode_num_splits_for_sms", "attn_get_device_status", "attn_last_timeout_site",

@@ -257,7 +257,7 @@ bool encode_keys(CUtensorMap *map, const void *base, bool bf16, int d, int h_kv,
 
 // Common part of the two forwards: everything but K and V.
 void fill_pack(PackArgs *a, void *o, float *lse, int b, int total_q, int max_seqlen_q, int h, int h_kv,
-               int64_t max_k, float scale, bool causal, uint32_t *status, int num_sms) {
+               int64_t max_k, float scale, bool causal, uint32_t *status, int num_sms, bool may_be_one = true) {
     a->o = o;
     a->lse = lse;
     a->h = h;
@@ -271,13 +271,16 @@ void fill_pack(PackArgs *a, void *o, float *lse, int b, int total_q, int max_seq
     a->ctas = num_sms;
     // Units of one query tile where no sequence is known to hold more.
     const int longest = max_seqlen_q > 0 && max_seqlen_q < total_q ? max_seqlen_q : total_q;
-    a->one_tile = longest <= a->tile_tokens ? 1 : 0;
+    a->one_tile = may_be_one && longest <= a->tile_tokens ? 1 : 0;
     a->group_inv = pack_group_inv(a->group);
     a->line = pack_line(h_kv, a->group, a->one_tile != 0, causal, LineBound{b, total_q, max_k, max_k});
     a->seqs.b = b;
     a->seqs.total_q = total_q;
     a->block_table = nullptr;
     a->page_size = a->max_pages = a->num_pages = a->box_rows = 0;
+    a->k4 = a->v4 = nullptr;
+    a->block4 = 0;
+    a->v_scale4 = 1.0f;
 }
 
 template <class Launch>
@@ -788,6 +791,47 @@ attn_status_t attn_paged_append_q4(const void *q, const void *k, const void *v, 
     a.block = q4_block_bytes(page_size, d);
     a.codes = static_cast<int64_t>(page_size) * q4_code_bytes(d);
     return run_append(a, dtype, true, stream);
+}
+
+attn_status_t attn_chunk_paged_q4(const void *q, const void *k_pages, const void *v_pages,
+                                  const int32_t *block_table, const int32_t *cu_seqlens_q, const int32_t *seqlens_k,
+                                  void *o, float *lse, int b, int total_q, int max_seqlen_q, int h, int h_kv, int d,
+                                  int num_pages, int page_size, int max_pages_per_seq, int64_t q_stride, float scale,
+                                  float k_scale, float v_scale, int causal, attn_dtype_t dtype, cudaStream_t stream) {
+    for (const void *p : {q, k_pages, v_pages, static_cast<const void *>(o)})
+        if (!p || misaligned(p, 16)) return ATTN_ERR_INVALID_ARG;
+    for (const void *p : {static_cast<const void *>(lse), static_cast<const void *>(block_table),
+                          static_cast<const void *>(cu_seqlens_q), static_cast<const void *>(seqlens_k)})
+        if (!p || misaligned(p, 4)) return ATTN_ERR_INVALID_ARG;
+    if (num_pages < 1 || page_size < 1 || max_pages_per_seq < 1) return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = check_packed(b, total_q, h, h_kv, d, scale, dtype);
+    if (st == ATTN_OK) st = check_stride(q_stride, static_cast<int64_t>(h) * d);
+    if (st == ATTN_OK) st = check_q4(page_size, k_scale, v_scale);
+    if (st != ATTN_OK) return st;
+    if (!std::isfinite(scale * k_scale * kLog2e)) return ATTN_ERR_INVALID_ARG;
+    const int64_t max_k = static_cast<int64_t>(max_pages_per_seq) * page_size;
+    if (max_k > kMaxRows) return ATTN_ERR_UNSUPPORTED;
+    int dev = 0, sms = 0;
+    uint32_t *status = nullptr;
+    if ((st = device_info(&dev, &status, &sms)) != ATTN_OK) return st;
+    const bool bf16 = dtype == ATTN_BF16;
+    PackArgs a;
+    fill_pack(&a, o, lse, b, total_q, max_seqlen_q, h, h_kv, max_k, scale * k_scale, causal != 0, status, sms, false);
+    a.seqs.cu_q = cu_seqlens_q;
+    a.seqs.cu_k = nullptr;
+    a.seqs.seqlens = seqlens_k;
+    a.seqs.max_k = static_cast<int>(max_k);
+    a.block_table = block_table;
+    a.page_size = page_size;
+    a.max_pages = max_pages_per_seq;
+    a.num_pages = num_pages;
+    a.k4 = static_cast<const uint8_t *>(k_pages);
+    a.v4 = static_cast<const uint8_t *>(v_pages);
+    a.block4 = q4_block_bytes(page_size, d);
+    a.v_scale4 = v_scale;
+    CUtensorMap tq;
+    if (!encode_rows(&tq, q, bf16, d, h, h_kv, total_q, q_stride, a.tile_tokens)) return ATTN_ERR_CUDA;
+    return run_pack(&a, dev, d, stream, [&] { return launch_chunk_q4(d, bf16, tq, a, stream); });
 }
 
 attn_status_t attn_paged_read_q4(const void *k_pages, const void *v_pages, const int64_t *slot_map, void *k, void *v,

@@ -52,6 +52,7 @@
 #include "packed.h"
 #include "packed_dev.cuh"
 #include "ptx.cuh"
+#include "q4.cuh"
 
 namespace exattn {
 namespace {
@@ -103,18 +104,25 @@ struct PackGeom {
     static constexpr int NUM_BARS = BAR_WG + 2;
     static constexpr int OFF_MSG = (OFF_BAR + NUM_BARS * 8 + 15) & ~15;
     static constexpr int OFF_SUM = OFF_MSG + kMsgSlots * 64;  // a LineSum per warp
-    static constexpr int OFF_MISC = OFF_SUM + 12 * 12;        // TMEM base, abort, joiner[2]
+    static constexpr int OFF_MISC = OFF_SUM + 16 * 12;        // TMEM base, abort, joiner[2]
     static constexpr int USED = OFF_MISC + 16;
     static constexpr int MIN_SMEM = 120 * 1024;  // one CTA per SM: it owns all of TMEM
     static constexpr int SMEM_BYTES = (USED > MIN_SMEM ? USED : MIN_SMEM) + 1024;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
 
-constexpr int kPackThreads = 384;
-constexpr int kPackRegsLaunch = 168;
-constexpr int kPackRegsControl = 96;
-constexpr int kPackRegsSoftmax = 200;
-static_assert(4 * kPackRegsControl + 8 * kPackRegsSoftmax <= 12 * kPackRegsLaunch, "register split");
+// Threads and registers of a CTA. Over a 4-bit cache four more warps widen its
+// rows to 16 bits.
+template <bool Q4>
+struct PackThreads {
+    static constexpr int COUNT = Q4 ? 512 : 384;
+    static constexpr int REGS_LAUNCH = Q4 ? 128 : 168;
+    static constexpr int REGS_CONTROL = Q4 ? 72 : 96;
+    static constexpr int REGS_SOFTMAX = Q4 ? 184 : 200;
+    static constexpr int REGS_WIDEN = 72;
+    static_assert(4 * REGS_CONTROL + 8 * REGS_SOFTMAX + (Q4 ? 4 * REGS_WIDEN : 0) <= COUNT / 32 * REGS_LAUNCH,
+                  "register split");
+};
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2p(float lo, float hi) {
@@ -260,14 +268,159 @@ __device__ __forceinline__ void pack_producer(const CUtensorMap *tq, const CUten
     }
 }
 
+// The 4-bit form's producers. Q comes by TMA, one lane issuing.
+template <int D>
+__device__ __forceinline__ void pack_q_producer(const CUtensorMap *tq, uint32_t sbase, const UnitMsg *msgs,
+                                                const PackArgs &a, const WaitGuard &g) {
+    using G = PackGeom<D, false>;
+    auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
+    const uint32_t q_box = a.tile_tokens * a.group * G::ROW_BYTES;
+    int qb = 0, q_issued = 0;
+    uint32_t q_phase = 1;
+    UnitMsg x;
+#pragma unroll 1
+    for (int n = 0; take_unit<false>(&x, n, msgs, bar(G::BAR_MF), bar(G::BAR_ME), g, 17); ++n) {
+        if (!await(bar(G::BAR_QE + qb), q_phase, g, 1)) break;
+        const int n_qt = live_tiles<2>(x, a);
+        mbar_arrive_expect_tx(bar(G::BAR_QF + qb), n_qt * G::PANELS * q_box);
+#pragma unroll 1
+        for (int t = 0; t < n_qt; ++t)
+#pragma unroll
+            for (int p = 0; p < G::PANELS; ++p)
+                tma_load_4d(sbase + G::OFF_Q + qb * G::Q_BUF_BYTES + t * G::TILE_BYTES + p * G::PANEL_BYTES, tq,
+                            bar(G::BAR_QF + qb), p * G::PANEL_ELEMS, 0, x.head, x.q0 + x.tok0 + t * a.tile_tokens);
+        ++q_issued;
+        if (++qb == G::QBUF) {
+            qb = 0;
+            q_phase ^= 1u;
+        }
+    }
+    // never leave the CTA with a copy still landing (as in pack_producer)
+    WaitGuard drain = g;
+    uint32_t no_abort = 0;
+    drain.abort = &no_abort;
+#pragma unroll 1
+    for (int i = (q_issued > G::QBUF ? q_issued - G::QBUF : 0); i < q_issued; ++i)
+        await(bar(G::BAR_QF + i % G::QBUF), (i / G::QBUF) & 1, drain, 9);
+}
+
+// A row of codes and scales of one head, as a thread holds it on its way.
+template <int D>
+struct Q4Row {
+    static constexpr int WORDS = D / 8;  // a word of codes is 8 channels
+    uint32_t code[WORDS];
+    uint32_t scale[(D + 63) / 64];  // a byte for 16 channels
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) code[i] = 0u;
+#pragma unroll
+        for (int i = 0; i < (D + 63) / 64; ++i) scale[i] = 0u;
+    }
+    __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales) {
+        if constexpr (D >= 32) {
+#pragma unroll
+            for (int i = 0; i < WORDS / 4; ++i) {
+                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(codes) + i);
+                code[4 * i] = x.x, code[4 * i + 1] = x.y, code[4 * i + 2] = x.z, code[4 * i + 3] = x.w;
+            }
+        } else {
+            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(codes));
+            code[0] = x.x, code[1] = x.y;
+        }
+        if constexpr (D == 128) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(scales));
+            scale[0] = x.x, scale[1] = x.y;
+        } else if constexpr (D == 64) {
+            scale[0] = __ldg(reinterpret_cast<const uint32_t *>(scales));
+        } else if constexpr (D == 32) {
+            scale[0] = __ldg(reinterpret_cast<const uint16_t *>(scales));
+        } else {
+            scale[0] = __ldg(scales);
+        }
+    }
+};
+
+// Four warps widen K and V: thread r takes key r of each step, from the pages
+// through registers (both rows a step ahead) into row r of the ring's tile,
+// swizzled as TMA would leave it. Values are exact in either type; K takes Q's
+// type, V is fp16. Rows past the sequence's end are zeros.
+template <int D, bool BF16>
+__device__ __forceinline__ void pack_widen(uint32_t sbase, const UnitMsg *msgs, const PackArgs &a,
+                                           const WaitGuard &g) {
+    using G = PackGeom<D, false>;
+    auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
+    const int r = threadIdx.x & 127;
+    const uint32_t row = r * G::ROW_BYTES;
+    constexpr int CPR = G::ROW_BYTES / 16;  // 16-byte chunks of a swizzled row: 8, 4 or 2
+    const uint32_t swz = CPR == 8 ? r & 7 : CPR == 4 ? (r >> 1) & 3 : (r >> 2) & 1;
+    Ring<G::SLOTS> ring;
+    ring.phase = 1;
+    bool ok = true;
+    UnitMsg x;
+#pragma unroll 1
+    for (int n = 0; ok && take_unit<true>(&x, n, msgs, bar(G::BAR_MF), bar(G::BAR_ME), g, 17); ++n) {
+        const int32_t *table = a.block_table + static_cast<int64_t>(x.seq) * a.max_pages;
+        Q4Row<D> buf[2];
+        // this thread's row of K and V of step j
+        auto fetch = [&](int j, int kv) {
+            const int key = j * G::BN + r;
+            buf[kv].clear();
+            if (j < x.step0 + x.nstep && key < x.sk) {
+                const int p = static_cast<int>(static_cast<uint32_t>(key) / static_cast<uint32_t>(a.page_size));
+                const int page = min(max(__ldg(table + p), 0), a.num_pages - 1);
+                const int at = key - p * a.page_size;
+                const uint8_t *block =
+                    (kv ? a.v4 : a.k4) + (static_cast<int64_t>(page) * (a.h / a.group) + x.head) * a.block4;
+                buf[kv].load(block + static_cast<int64_t>(at) * q4_code_bytes(D),
+                             block + static_cast<int64_t>(a.page_size) * q4_code_bytes(D) +
+                                 static_cast<int64_t>(at) * q4_scale_bytes(D));
+            }
+        };
+        fetch(x.step0, 0);
+        fetch(x.step0, 1);
+#pragma unroll 1
+        for (int j = x.step0; ok && j < x.step0 + x.nstep; ++j) {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                ok = ok && await(bar(G::BAR_KVE + ring.slot), ring.phase, g, 2);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                const uint32_t dst = sbase + G::OFF_KV + ring.slot * G::TILE_BYTES + row;
+#pragma unroll
+                for (int i = 0; i < Q4Row<D>::WORDS; ++i) {
+                    const uint32_t pair = q4_scales_f16(buf[kv].scale[i / 8] >> (16 * (i / 4 % 2)));
+                    const uint32_t s2 = __byte_perm(pair, 0, i / 2 % 2 ? 0x3232 : 0x1010);
+                    uint32_t w[4];
+                    q4_codes_f16(buf[kv].code[i], w);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        w[e] = h2_mul(w[e], s2);
+                        if (BF16 && kv == 0) {
+                            const float2 f = h2_float2(w[e]);
+                            w[e] = cvt_pack_bf16(f.x, f.y);
+                        }
+                    }
+                    st_shared_v4(dst + i / CPR * G::PANEL_BYTES + ((i % CPR) ^ swz) * 16, w);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if ((threadIdx.x & 31) == 0) mbar_arrive(bar(G::BAR_KVF + ring.slot));
+                ring.next();
+                fetch(j + 1, kv);
+            }
+        }
+    }
+}
+
 // The products of a tile and the zeroing of its V tail, as the issuers use
 // them: one lane issues, a whole warp zeroes.
-template <int D, bool BF16, bool ONE>
+template <int D, bool BF16, bool ONE, bool Q4 = false>
 struct TileMma {
     using G = PackGeom<D, ONE>;
     uint32_t sbase, idesc_s;
     uint64_t dq, dk, dv;
-    static constexpr uint32_t idesc_o = mma_idesc_f16(G::BM, D, BF16, false, true);
+    // (values of a 4-bit cache are exact in fp16, and P is rounded less there than in bf16)
+    static constexpr uint32_t idesc_o = mma_idesc_f16(G::BM, D, BF16 && !Q4, false, true);
     static constexpr uint32_t tile16 = G::TILE_BYTES >> 4;
     static_assert(G::PANELS <= 2, "panels of a tile");
 
@@ -430,12 +583,12 @@ __device__ __forceinline__ void issue_one_pv(uint32_t sbase, uint32_t tmem, cons
 }
 
 // The MMAs of tile t of two.
-template <int D, bool BF16>
+template <int D, bool BF16, bool Q4>
 __device__ __forceinline__ void pack_issue(uint32_t sbase, uint32_t tmem, const UnitMsg *msgs, int t,
                                            const PackArgs &a, const WaitGuard &g) {
     using G = PackGeom<D, false>;
     auto bar = [&](int i) { return sbase + G::OFF_BAR + 8u * i; };
-    const TileMma<D, BF16, false> mma(sbase, t, a);
+    const TileMma<D, BF16, false, Q4> mma(sbase, t, a);
     Ring<G::SLOTS> ring;
     int qbuf = 0;
     uint32_t q_phase = 0;         // of the Q buffers
@@ -472,7 +625,7 @@ __device__ __forceinline__ void pack_issue(uint32_t sbase, uint32_t tmem, const 
             // everything the turn needs: V_{j-1} (its tail zeroed), K_j, P_{j-1}
             if (j > 0) {
                 ok = await(bar(G::BAR_KVF + vr.slot), vr.phase, g, 6);
-                if (live && (keys & 15)) {
+                if (!Q4 && live && (keys & 15)) {  // (rows past the end are widened as zeros)
                     if (!__all_sync(0xffffffffu, ok)) break;
                     mma.zero_tail(vr.slot, keys);
                 }
@@ -609,7 +762,7 @@ __device__ __forceinline__ void pack_join(int first_part, int nparts, int t, int
         join_rows<D, BF16, 4, 2>(first_part, nparts, t, tiles, tok0, head0, rows, a);
 }
 
-template <int D, bool BF16, bool ONE>
+template <int D, bool BF16, bool ONE, bool Q4>
 __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint32_t tmem, const UnitMsg *msgs,
                                              int t, int q4, const PackArgs &a, const WaitGuard &g) {
     using G = PackGeom<D, ONE>;
@@ -621,6 +774,10 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
     const uint32_t tS0 = tmem + t * G::TMEM_TILE_STRIDE + (static_cast<uint32_t>(q4 * 32) << 16);
     const uint32_t tO = tS0 + G::TMEM_O_OFF;
     const float c = fabsf(a.scale_log2);
+    // over a 4-bit cache P is fp16 whatever the type, and 2^6 times as large (at
+    // most 2^14): its least values are 2^-30 of the reference max
+    constexpr bool P_BF16 = BF16 && !Q4;
+    constexpr float P_SHIFT = Q4 ? 6.0f : 0.0f;
     int s_cnt = 0, s2_cnt = 0, o_cnt = 0;
     int met = 0;      // meetings of the tile's warps
     volatile int *joiner = reinterpret_cast<volatile int *>(smem + G::OFF_MISC + 8);
@@ -699,7 +856,7 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
                             mx[i & 3] = max3f(mx[i & 3], s[2 * i], s[2 * i + 1]);
                     }
                     step(fmaxf(max3f(mx[0], mx[1], mx[2]), mx[3]));
-                    const float neg_m = -m_ref;
+                    const float neg_m = P_SHIFT - m_ref;
                     const uint64_t c2 = f2_make(c, c), nm2 = f2_make(neg_m, neg_m);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
@@ -712,7 +869,7 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
                             const float p0 = fast_exp2(x0);
                             const float p1 = fast_exp2(x1);
                             acc2[i & 1] = f2_add(acc2[i & 1], f2_make(p0, p1));
-                            pk[i] = pack2p<BF16>(p0, p1);
+                            pk[i] = pack2p<P_BF16>(p0, p1);
                         }
                         tmem_st32(tS + half * (G::BN / 4), pk);
                     }
@@ -733,7 +890,7 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
                             if (c0 + i < valid) mx[i & 1] = fmaxf(mx[i & 1], __uint_as_float(sr[i]));
                     }
                     step(fmaxf(mx[0], mx[1]));
-                    const float neg_m = -m_ref;
+                    const float neg_m = P_SHIFT - m_ref;
                     const uint64_t c2 = f2_make(c, c), nm2 = f2_make(neg_m, neg_m);
 #pragma unroll 1
                     for (int c0 = 0; c0 < G::BN; c0 += 32) {
@@ -753,7 +910,7 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
                                 const float p0 = fast_exp2(c0 + 2 * i < valid ? x0 : -INFINITY);
                                 const float p1 = fast_exp2(c0 + 2 * i + 1 < valid ? x1 : -INFINITY);
                                 acc2[i & 1] = f2_add(acc2[i & 1], f2_make(p0, p1));
-                                pk[i] = pack2p<BF16>(p0, p1);
+                                pk[i] = pack2p<P_BF16>(p0, p1);
                             }
                         }
                         tmem_st16(tS + c0 / 2, pk);
@@ -804,7 +961,7 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
         // A row that saw no key of the range: O = 0, LSE = -inf. (Not told by
         // l > 0: a NaN among the row's inputs has to come out as NaN.)
         const bool empty_row = nstep == 0 || sees <= 0;
-        const float inv_l = empty_row ? 0.0f : 1.0f / l;
+        const float inv_l = empty_row ? 0.0f : (Q4 ? a.v_scale4 : 1.0f) / l;
         const int slot = x->slot;
         const bool part = slot >= 0;
         const int64_t grow = x->q0 + (row_out ? tok : 0);
@@ -861,7 +1018,7 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(G::BAR_OE + t));
-        const float lse2 = empty_row ? -INFINITY : m_ref + __log2f(l);
+        const float lse2 = empty_row ? -INFINITY : m_ref + __log2f(l) - P_SHIFT;
         if (!part) {
             if (row_out) a.lse[static_cast<int64_t>(head) * a.total_q + grow] = lse2 * 0.69314718055994530942f;
             free_unit(n, bar(G::BAR_ME));
@@ -891,11 +1048,13 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
     }
 }
 
-template <int D, bool BF16, bool PAGED, bool ONE>
-__global__ void __launch_bounds__(kPackThreads, 1)
+template <int D, bool BF16, bool PAGED, bool ONE, bool Q4>
+__global__ void __launch_bounds__(PackThreads<Q4>::COUNT, 1)
     pack_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                 const __grid_constant__ CUtensorMap tv, const PackArgs a) {
     using G = PackGeom<D, ONE>;
+    using T = PackThreads<Q4>;
+    static_assert(!Q4 || (PAGED && !ONE), "the 4-bit cache has the two-tile form");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -915,16 +1074,19 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             if ((i >= G::BAR_PF && i < G::BAR_PF + 2) || (i >= G::BAR_OE && i < G::BAR_OE + 2))
                 count = 4;  // the tile's softmax warps
             if (i >= G::BAR_WG) count = 4;
-            if (i >= G::BAR_ME && i < G::BAR_MS) count = ONE ? 7 + (PAGED ? 1 : 0) : 11;  // producers, issuers, softmax warps
+            if (i >= G::BAR_ME && i < G::BAR_MS) count = ONE ? 7 + (PAGED ? 1 : 0) : Q4 ? 15 : 11;  // producers, issuers, softmax warps
             // released by each tile's issuer
             if ((i >= G::BAR_QE && i < G::BAR_KVF) || (i >= G::BAR_KVE && i < G::BAR_SF)) count = G::QT;
+            if (Q4 && i >= G::BAR_KVF && i < G::BAR_KVE) count = 4;  // the widening warps
             mbar_init(bar(i), count);
         }
         *abort_flag = 0u;
         fence_mbar_init();
         tma_prefetch_desc(&tq);
-        tma_prefetch_desc(&tk);
-        tma_prefetch_desc(&tv);
+        if (!Q4) {
+            tma_prefetch_desc(&tk);
+            tma_prefetch_desc(&tv);
+        }
     }
     if (warp == 1) {
         tmem_alloc(smem_u32(tmem_slot), G::TMEM_COLS);
@@ -938,13 +1100,15 @@ __global__ void __launch_bounds__(kPackThreads, 1)
     const WaitGuard g{abort_flag, a.status, kKernFwd};
 
     if (warp < 4) {
-        reg_dealloc<kPackRegsControl>();
-        if (warp == 0) {
+        reg_dealloc<T::REGS_CONTROL>();
+        if (Q4 && warp == 0) {
+            if (lane == 0 && !(a.flags & kFlagSkipLoads)) pack_q_producer<D>(&tq, sbase, msgs, a, g);
+        } else if (warp == 0) {
             if ((PAGED || lane == 0) && !(a.flags & kFlagSkipLoads))
                 pack_producer<D, PAGED, ONE, PAGED && ONE ? 0 : 2>(&tq, &tk, &tv, sbase, msgs, a, g);
         } else if (warp < 3) {
             if constexpr (!ONE) {
-                pack_issue<D, BF16>(sbase, tmem, msgs, warp - 1, a, g);
+                pack_issue<D, BF16, Q4>(sbase, tmem, msgs, warp - 1, a, g);
             } else {
                 if (warp == 1)
                     issue_one_s<D, BF16>(sbase, tmem, msgs, a, g);
@@ -954,15 +1118,19 @@ __global__ void __launch_bounds__(kPackThreads, 1)
             }
         } else {
             post_units<0>(
-                a.seqs, a.line, [&] { return line_total(sums, kPackThreads / 32); }, msgs, bar(G::BAR_MF),
+                a.seqs, a.line, [&] { return line_total(sums, T::COUNT / 32); }, msgs, bar(G::BAR_MF),
                 bar(G::BAR_ME), bar(G::BAR_MS), g, 18, blockIdx.x, gridDim.x);
         }
+    } else if (Q4 && warp >= 12) {
+        reg_dealloc<T::REGS_WIDEN>();
+        if constexpr (Q4)
+            if (!(a.flags & kFlagSkipLoads)) pack_widen<D, BF16>(sbase, msgs, a, g);
     } else {
-        reg_alloc<kPackRegsSoftmax>();
+        reg_alloc<T::REGS_SOFTMAX>();
         if (ONE && warp == 8)
             issue_one_pv<D, BF16>(sbase, tmem, msgs, a, g);
         if (warp < 4 + 4 * G::QT)
-            pack_softmax<D, BF16, ONE>(smem, sbase, tmem, msgs, (warp - 4) >> 2, warp & 3, a, g);
+            pack_softmax<D, BF16, ONE, Q4>(smem, sbase, tmem, msgs, (warp - 4) >> 2, warp & 3, a, g);
     }
 
     tc_fence_before();
@@ -971,7 +1139,7 @@ __global__ void __launch_bounds__(kPackThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, G::TMEM_COLS);
 }
 
-template <int D, bool BF16, bool PAGED, bool ONE>
+template <int D, bool BF16, bool PAGED, bool ONE, bool Q4 = false>
 cudaError_t launch_pack_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const PackArgs &a,
                           cudaStream_t stream) {
     using G = PackGeom<D, ONE>;
@@ -980,12 +1148,13 @@ cudaError_t launch_pack_t(const CUtensorMap &tq, const CUtensorMap &tk, const CU
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 64 && !attr_set[dev]) {
-        e = cudaFuncSetAttribute(pack_kernel<D, BF16, PAGED, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(pack_kernel<D, BF16, PAGED, ONE, Q4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  G::SMEM_BYTES);
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    pack_kernel<D, BF16, PAGED, ONE><<<a.ctas, kPackThreads, G::SMEM_BYTES, stream>>>(tq, tk, tv, a);
+    pack_kernel<D, BF16, PAGED, ONE, Q4>
+        <<<a.ctas, PackThreads<Q4>::COUNT, G::SMEM_BYTES, stream>>>(tq, tk, tv, a);
     return cudaGetLastError();
 }
 

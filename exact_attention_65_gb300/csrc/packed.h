@@ -47,6 +47,10 @@ struct PackArgs {
     // paged K/V
     const int32_t *block_table;
     int page_size, max_pages, num_pages, box_rows;
+    // a 4-bit cache (q4.cuh): its pools, bytes of a page of a head, V's scale
+    const uint8_t *k4, *v4;
+    int64_t block4;
+    float v_scale4;
 };
 // Query tokens of a 128-row tile, and where work is cut.
 inline int pack_tile_tokens(int group) { return 128 / group; }
@@ -64,6 +68,7 @@ cudaError_t launch_fwd_packed(int d, bool bf16, const CUtensorMap &tq, const CUt
                               const CUtensorMap &tv, const PackArgs &a, cudaStream_t stream);
 cudaError_t launch_chunk_paged(int d, bool bf16, const CUtensorMap &tq, const CUtensorMap &tk,
                                const CUtensorMap &tv, const PackArgs &a, cudaStream_t stream);
+cudaError_t launch_chunk_q4(int d, bool bf16, const CUtensorMap &tq, const PackArgs &a, cudaStream_t stream);
 
 // Backward of the packed forward (bwd_packed.cu). Index 0: query-tile units
 // (dQ), 1: key-tile units (dK, dV).

@@ -454,6 +454,24 @@ attn_status_t attn_paged_append_q4(const void *q, const void *k, const void *v, 
                                    attn_dtype_t dtype, cudaStream_t stream);
 
 /*
+ * attn_chunk_paged over a 4-bit cache: the new tokens of each request (one, a
+ * few, or a chunk of a prompt) over its pages. A cached value enters the
+ * products as it stands (code * scale is exact in 16 bits, the tensor's scale
+ * goes into the softmax's scale and into O), so results are those of exact
+ * attention over the cache's values.
+ *   k_pages, v_pages  4-bit pools [num_pages, h_kv, page_bytes]; k_scale, v_scale
+ *                     as attn_paged_append_q4 got them; scale * k_scale finite
+ * Rows of a page past a request's end may hold anything. Other arguments,
+ * results, workspace and errors as attn_chunk_paged.
+ */
+attn_status_t attn_chunk_paged_q4(const void *q, const void *k_pages, const void *v_pages,
+                                  const int32_t *block_table, const int32_t *cu_seqlens_q,
+                                  const int32_t *seqlens_k, void *o, float *lse, int b, int total_q,
+                                  int max_seqlen_q, int h, int h_kv, int d, int num_pages, int page_size,
+                                  int max_pages_per_seq, int64_t q_stride, float scale, float k_scale,
+                                  float v_scale, int causal, attn_dtype_t dtype, cudaStream_t stream);
+
+/*
  * Rows of a 4-bit cache back in 16 bits: row slot_map[t] of the pools, rounded
  * once, to row t of k and v [tokens, h_kv, d] (token strides as above); zeros
  * where the slot is outside the pools. A slot may come up several times. Errors

@@ -60,6 +60,23 @@ def test_read_q4_refuses(exattn_lib, kw, expect):
     assert call(exattn_lib.attn_paged_read_q4, READ, **{**READ_OK, **kw}) == expect
 
 
+CHUNK = "q kp vp table cq lens o lse b tq mq h hk d pages page width qs scale k_scale v_scale causal dtype stream"
+CHUNK_OK = dict(q=A, kp=A, vp=A, table=A, cq=A, lens=A, o=A, lse=A, b=2, tq=10, mq=0, h=4, hk=2, d=64, pages=9, page=16,
+                width=4, qs=256, scale=0.1, k_scale=1.0, v_scale=1.0, causal=1, dtype=ea.ATTN_BF16, stream=None)
+
+
+@pytest.mark.parametrize("kw,expect", SCALES + [
+    (dict(q=None), INV), (dict(kp=None), INV), (dict(table=None), INV), (dict(lens=None), INV), (dict(lse=None), INV),
+    (dict(vp=A + 8), INV), (dict(o=A + 8), INV), (dict(table=A + 2), INV), (dict(cq=A + 1), INV), (dict(b=0), INV),
+    (dict(tq=0), INV), (dict(pages=0), INV), (dict(page=0), INV), (dict(width=0), INV), (dict(h=6, hk=4), INV),
+    (dict(qs=64), INV), (dict(dtype=2), INV), (dict(scale=float("inf")), INV), (dict(scale=1e38, k_scale=1e10), INV),
+    (dict(d=96), UNS), (dict(h=258, hk=2, qs=1 << 15), UNS), (dict(page=1 << 20, width=1 << 12), UNS),
+    (dict(tq=0x7fffffff), UNS), (dict(b=70000), UNS),
+])
+def test_chunk_q4_refuses(exattn_lib, kw, expect):
+    assert call(exattn_lib.attn_chunk_paged_q4, CHUNK, **{**CHUNK_OK, **kw}) == expect
+
+
 def test_page_bytes(exattn_lib):
     assert [ea.attn_q4_page_bytes(16, d) for d in (16, 32, 64, 128)] == [144, 288, 576, 1152]
     assert ea.attn_q4_page_bytes(48, 128) == 3456
@@ -74,6 +91,8 @@ def test_binding_refuses_host_tensors(exattn_lib):
             fn(q, q, q, torch.zeros(9, 64), n, n, q, q)
     with pytest.raises(ValueError, match="CUDA tensor"):
         ea.attn_paged_read_q4(q, q, n, 64)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        ea.attn_chunk_paged_q4(q, q, q, n, n, n)
 
 
 # ---------------------------------------------------------------- the oracle's own pins
