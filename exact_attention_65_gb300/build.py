@@ -25,7 +25,7 @@ LIB = os.path.join(PKG, "libexattn.so")
 
 SOURCES = ["fwd.cu", "fwd_packed.cu", "chunk_paged.cu", "bwd.cu", "fwd_short.cu", "bwd_packed.cu",
            "bwd_short.cu", "decode.cu", "api.cu", "api_packed.cu", "paged_tables.cu",
-           "append_paged.cu", "chunk_q4.cu", "decode_noalloc.cu"]
+           "append_paged.cu", "chunk_q4.cu", "decode_q4.cu", "decode_noalloc.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("internal.h", "ptx.cuh", "packed.h", "packed_sched.h", "packed_dev.cuh",
                                            "fwd_packed.cuh", "q4.cuh")] + [os.path.join(INCLUDE, "exattn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -58,6 +58,23 @@ LineShape pack_line(int heads, int group, bool one_tile, bool causal, const Line
     return s;
 }
 
+// Few rows over a 4-bit cache: units of `tokens` tokens, cut as those of one tile.
+LineShape decode_q4_line(int heads, int tokens, bool causal, const LineBound &bound) {
+    LineShape s;
+    s.heads = heads;
+    s.unit_len = tokens;
+    s.step_len = 128;
+    s.causal = causal ? 1 : 0;
+    s.by_key = 0;
+    s.weight = 1;
+    s.shift = 7;
+    s.unit_cost = kUnitSteps;
+    s.min_steps = 2;
+    s.min_part = 4;
+    fit_line(&s, bound);
+    return s;
+}
+
 // The backward's query-tile units: one tile against steps of 128 keys.
 LineShape bwd_query_line(int heads, int group, bool causal, const LineBound &bound) {
     return pack_line(heads, group, true, causal, bound);
@@ -281,22 +298,34 @@ void fill_pack(PackArgs *a, void *o, float *lse, int b, int total_q, int max_seq
     a->k4 = a->v4 = nullptr;
     a->block4 = 0;
     a->v_scale4 = 1.0f;
+    a->q = nullptr;
+    a->q_stride = 0;
+    a->page_mul = 0;
+    a->page_div = 0;
 }
 
+// Takes the workspace (`rows` rows of partial results for each CTA, counters
+// counters from number `from` on) and launches.
 template <class Launch>
-attn_status_t run_pack(PackArgs *a, int dev, int d, cudaStream_t stream, Launch launch) {
-    const size_t rows = static_cast<size_t>(a->ctas) * 2 * (a->one_tile ? 1 : 2) * 128;
+attn_status_t run_with(PackArgs *a, int dev, int d, size_t rows, int from, int counters, cudaStream_t stream,
+                       Launch launch) {
+    rows *= a->ctas;
     Workspace w;
     const attn_status_t st =
-        get_workspace(dev, stream, 2 * a->ctas, rows * (static_cast<size_t>(d) + 1) * sizeof(float), &w);
+        get_workspace(dev, stream, from + counters, rows * (static_cast<size_t>(d) + 1) * sizeof(float), &w);
     if (st != ATTN_OK) return st;
-    a->arrivals = w.arrivals;
+    a->arrivals = w.arrivals + from;
     a->call = w.call;
     a->o_part = reinterpret_cast<float *>(w.part);
     a->lse_part = a->o_part + rows * d;
     const cudaError_t e = launch();
     const cudaError_t ef = w.owned ? cudaFreeAsync(w.owned, stream) : cudaSuccess;
     return (e == cudaSuccess && ef == cudaSuccess) ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+template <class Launch>
+attn_status_t run_pack(PackArgs *a, int dev, int d, cudaStream_t stream, Launch launch) {
+    return run_with(a, dev, d, 2 * (a->one_tile ? 1 : 2) * 128, 0, 2 * a->ctas, stream, launch);
 }
 
 bool overlap(const void *p, size_t np, const void *q, size_t nq) {
@@ -829,6 +858,21 @@ attn_status_t attn_chunk_paged_q4(const void *q, const void *k_pages, const void
     a.v4 = static_cast<const uint8_t *>(v_pages);
     a.block4 = q4_block_bytes(page_size, d);
     a.v_scale4 = v_scale;
+    // Few rows: a kernel that widens the codes in registers (64 requests of a
+    // token over up to 8192 keys, h32/8 d128: 92 us, on the two-tile form 199)
+    const int64_t longest = max_seqlen_q > 0 && max_seqlen_q < total_q ? max_seqlen_q : total_q;
+    const int rows = decode_q4_rows(longest * a.group);
+    if (rows > 0 && check_units(b, total_q, rows / a.group, h_kv) == ATTN_OK) {
+        a.q = q;
+        a.q_stride = q_stride;
+        a.tile_tokens = rows / a.group;
+        a.line = decode_q4_line(h_kv, a.tile_tokens, causal != 0, LineBound{b, total_q, max_k, max_k});
+        a.ctas = sms * decode_q4_ctas(rows);
+        fast_division(page_size / 16, &a.page_mul, &a.page_div);
+        // (counters of its own: it counts further than the other kernels)
+        return run_with(&a, dev, d, 2 * rows, 2 * sms, a.ctas, stream,
+                        [&] { return launch_decode_q4(d, bf16, rows, a, stream); });
+    }
     CUtensorMap tq;
     if (!encode_rows(&tq, q, bf16, d, h, h_kv, total_q, q_stride, a.tile_tokens)) return ATTN_ERR_CUDA;
     return run_pack(&a, dev, d, stream, [&] { return launch_chunk_q4(d, bf16, tq, a, stream); });

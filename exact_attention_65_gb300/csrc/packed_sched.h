@@ -167,8 +167,9 @@ EXATTN_HD LineDeal line_deal(LineShape *s, const LineSum &t, int ctas) {
     return d;
 }
 
-// (r c and parts are below 2^16 and 2^8: the quotient of floats, half a unit
-// up, has the integer quotient's floor)
+// (r c and parts are below 2^17 and 2^9: the quotient of floats, half a unit
+// up, has the integer quotient's floor: it errs by 2^-13 at most, half a unit of
+// the numerator is more than 2^-10)
 EXATTN_HD int part_begin(const LineDeal &d, int c) {
 #if defined(__CUDA_ARCH__)
     return d.q * c + static_cast<int>(__fdividef(static_cast<float>(d.r * c) + 0.5f, static_cast<float>(d.parts)));

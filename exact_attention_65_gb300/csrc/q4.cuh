@@ -78,4 +78,10 @@ __device__ __forceinline__ uint32_t q4_code_byte(float lo, float hi) {
     return r;
 }
 
+// 16 bytes at a 16-byte-aligned shared-memory address.
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
 }  // namespace exattn
