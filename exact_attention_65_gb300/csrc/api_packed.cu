@@ -58,7 +58,8 @@ LineShape pack_line(int heads, int group, bool one_tile, bool causal, const Line
     return s;
 }
 
-// Few rows over a 4-bit cache: units of `tokens` tokens, cut as those of one tile.
+// Few rows over a 4-bit cache: units of `tokens` tokens, dealt to warps: cut
+// wherever a warp's share ends, of two steps at least.
 LineShape decode_q4_line(int heads, int tokens, bool causal, const LineBound &bound) {
     LineShape s;
     s.heads = heads;
@@ -68,9 +69,9 @@ LineShape decode_q4_line(int heads, int tokens, bool causal, const LineBound &bo
     s.by_key = 0;
     s.weight = 1;
     s.shift = 7;
-    s.unit_cost = kUnitSteps;
-    s.min_steps = 2;
-    s.min_part = 4;
+    s.unit_cost = 1;
+    s.min_steps = 1;
+    s.min_part = 2;
     fit_line(&s, bound);
     return s;
 }
@@ -300,21 +301,19 @@ void fill_pack(PackArgs *a, void *o, float *lse, int b, int total_q, int max_seq
     a->v_scale4 = 1.0f;
     a->q = nullptr;
     a->q_stride = 0;
-    a->page_mul = 0;
+    a->page_bytes = a->page_mul = 0;
     a->page_div = 0;
 }
 
-// Takes the workspace (`rows` rows of partial results for each CTA, counters
-// counters from number `from` on) and launches.
+// Takes the workspace (`rows` rows of partial results, `counters` counters) and
+// launches.
 template <class Launch>
-attn_status_t run_with(PackArgs *a, int dev, int d, size_t rows, int from, int counters, cudaStream_t stream,
-                       Launch launch) {
-    rows *= a->ctas;
+attn_status_t run_with(PackArgs *a, int dev, int d, size_t rows, int counters, cudaStream_t stream, Launch launch) {
     Workspace w;
     const attn_status_t st =
-        get_workspace(dev, stream, from + counters, rows * (static_cast<size_t>(d) + 1) * sizeof(float), &w);
+        get_workspace(dev, stream, counters, rows * (static_cast<size_t>(d) + 1) * sizeof(float), &w);
     if (st != ATTN_OK) return st;
-    a->arrivals = w.arrivals + from;
+    a->arrivals = w.arrivals;
     a->call = w.call;
     a->o_part = reinterpret_cast<float *>(w.part);
     a->lse_part = a->o_part + rows * d;
@@ -325,7 +324,8 @@ attn_status_t run_with(PackArgs *a, int dev, int d, size_t rows, int from, int c
 
 template <class Launch>
 attn_status_t run_pack(PackArgs *a, int dev, int d, cudaStream_t stream, Launch launch) {
-    return run_with(a, dev, d, 2 * (a->one_tile ? 1 : 2) * 128, 0, 2 * a->ctas, stream, launch);
+    const size_t rows = static_cast<size_t>(a->ctas) * 2 * (a->one_tile ? 1 : 2) * 128;
+    return run_with(a, dev, d, rows, 2 * a->ctas, stream, launch);
 }
 
 bool overlap(const void *p, size_t np, const void *q, size_t nq) {
@@ -862,15 +862,16 @@ attn_status_t attn_chunk_paged_q4(const void *q, const void *k_pages, const void
     // token over up to 8192 keys, h32/8 d128: 92 us, on the two-tile form 199)
     const int64_t longest = max_seqlen_q > 0 && max_seqlen_q < total_q ? max_seqlen_q : total_q;
     const int rows = decode_q4_rows(longest * a.group);
-    if (rows > 0 && check_units(b, total_q, rows / a.group, h_kv) == ATTN_OK) {
+    if (rows > 0 && check_units(b, total_q, rows / a.group, h_kv) == ATTN_OK && h_kv * a.block4 <= 0xffffffffLL) {
         a.q = q;
         a.q_stride = q_stride;
         a.tile_tokens = rows / a.group;
         a.line = decode_q4_line(h_kv, a.tile_tokens, causal != 0, LineBound{b, total_q, max_k, max_k});
         a.ctas = sms * decode_q4_ctas(rows);
+        a.page_bytes = static_cast<uint32_t>(h_kv * a.block4);
         fast_division(page_size / 16, &a.page_mul, &a.page_div);
-        // (counters of its own: it counts further than the other kernels)
-        return run_with(&a, dev, d, 2 * rows, 2 * sms, a.ctas, stream,
+        const int warps = a.ctas * kDecodeQ4Warps;
+        return run_with(&a, dev, d, static_cast<size_t>(warps) * 2 * rows, 3 * warps, stream,
                         [&] { return launch_decode_q4(d, bf16, rows, a, stream); });
     }
     CUtensorMap tq;

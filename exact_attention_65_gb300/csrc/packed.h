@@ -51,10 +51,11 @@ struct PackArgs {
     const uint8_t *k4, *v4;
     int64_t block4;
     float v_scale4;
-    // few rows over a 4-bit cache (decode_q4.cu): q itself, and tile / (tiles of
-    // 16 keys in a page) = tile * page_mul >> page_div
+    // few rows over a 4-bit cache (decode_q4.cu): q itself, bytes of a page of all
+    // heads, and tile / (tiles of 16 keys in a page) = tile * page_mul >> page_div
     const void *q;
     int64_t q_stride;
+    uint32_t page_bytes;
     uint32_t page_mul;
     int page_div;
 };
@@ -76,10 +77,12 @@ cudaError_t launch_chunk_paged(int d, bool bf16, const CUtensorMap &tq, const CU
                                const CUtensorMap &tv, const PackArgs &a, cudaStream_t stream);
 cudaError_t launch_chunk_q4(int d, bool bf16, const CUtensorMap &tq, const PackArgs &a, cudaStream_t stream);
 // The most rows (tokens times a group's heads) of a unit of launch_decode_q4()
-// with so many rows to a request: 8 or 16, 0 where it has more. CTAs it takes of
-// an SM; its cut units leave O_i [ctas, 2, rows, d] and LSE_i [ctas, 2, rows].
+// with so many rows to a request: 8 or 16, 0 where it has more. Its work is dealt
+// to four warps of each CTA; each leaves up to two ranges' O_i and LSE_i [warps, 2,
+// rows], with three counters.
 inline int decode_q4_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 0; }
-inline int decode_q4_ctas(int rows) { return rows == 8 ? 2 : 1; }
+inline int decode_q4_ctas(int rows) { return rows == 8 ? 4 : 3; }
+constexpr int kDecodeQ4Warps = 4;
 LineShape decode_q4_line(int heads, int tokens, bool causal, const LineBound &bound);
 cudaError_t launch_decode_q4(int d, bool bf16, int rows, const PackArgs &a, cudaStream_t stream);
 

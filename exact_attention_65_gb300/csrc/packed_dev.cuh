@@ -122,14 +122,20 @@ __device__ __forceinline__ LineSum line_total(const LineSum *sums, int warps) {
     return t;
 }
 
-// Run by one warp: finds part `part` of the line dealt to `ctas` CTAs and
-// posts its units. total(): the line's sums where there are more than 32
-// sequences. `full` / `empty` / `shared`: kMsgSlots barriers each; `site`:
-// where a timeout of the wait for a free message slot is recorded.
-template <int BY_KEY, class Total>
-__device__ __forceinline__ void post_units(const SeqArrays &seqs, LineShape shape, Total total, UnitMsg *msgs,
-                                           uint32_t full, uint32_t empty, uint32_t shared, const WaitGuard &g,
-                                           uint32_t site, int part, int ctas) {
+// A part of the line as the warp that walks it knows it.
+struct PartPlace {
+    Place p, e;      // where it begins and ends
+    SeqLen p_len;    // of p's sequence: lengths, units of a head, what lies before it on the line
+    int p_units, p_x0;
+    SeqInfo cur;     // p's sequence
+};
+
+// Run by one warp: finds part `part` of the line dealt to `ctas` CTAs (or warps:
+// MANY, more than 512). total(): the line's sums where there are more than 32
+// sequences. Fits `shape` to the deal.
+template <int BY_KEY, bool MANY, class Total>
+__device__ __forceinline__ PartPlace find_part(const SeqArrays &seqs, LineShape &shape, Total total, int part, int ctas,
+                                               LineDeal *dealt) {
     const int lane = threadIdx.x & 31;
     known_shape<BY_KEY>(&shape);
     SeqInfo x{0, 0, 0, 0};
@@ -152,6 +158,8 @@ __device__ __forceinline__ void post_units(const SeqArrays &seqs, LineShape shap
     const LineDeal deal = line_deal(&shape, sum, ctas);
     if (shape.weight == 0) per = n;
 
+    *dealt = deal;
+
     // The part's begin (lanes 0-15 look for it) and end (lanes 16-31): 32
     // sequences at a time, by a prefix sum
     Place p{seqs.b, 0, 0, 0}, e = p;
@@ -159,7 +167,7 @@ __device__ __forceinline__ void post_units(const SeqArrays &seqs, LineShape shap
     int p_units = 0, p_x0 = 0;
     SeqInfo cur{0, 0, 0, 0};
     if (part < deal.parts) {
-        const int want0 = part_begin(deal, part), want1 = part_begin(deal, part + 1);
+        const int want0 = part_begin<MANY>(deal, part), want1 = part_begin<MANY>(deal, part + 1);
         int before = 0;
 #pragma unroll 1
         for (int i0 = 0;;) {
@@ -234,6 +242,21 @@ __device__ __forceinline__ void post_units(const SeqArrays &seqs, LineShape shap
             per = line_before(shape, x.sq, x.sk, n);
         }
     }
+    return PartPlace{p, e, p_len, p_units, p_x0, cur};
+}
+
+// Run by one warp: finds part `part` of the line dealt to `ctas` CTAs and
+// posts its units. total(): the line's sums where there are more than 32
+// sequences. `full` / `empty` / `shared`: kMsgSlots barriers each; `site`:
+// where a timeout of the wait for a free message slot is recorded.
+template <int BY_KEY, class Total>
+__device__ __forceinline__ void post_units(const SeqArrays &seqs, LineShape shape, Total total, UnitMsg *msgs,
+                                           uint32_t full, uint32_t empty, uint32_t shared, const WaitGuard &g,
+                                           uint32_t site, int part, int ctas) {
+    const int lane = threadIdx.x & 31;
+    LineDeal deal;
+    PartPlace at = find_part<BY_KEY, false>(seqs, shape, total, part, ctas, &deal);
+    SeqInfo &cur = at.cur;
 
     int posted = 0;
     auto post = [&](const UnitMsg &m) {
@@ -252,7 +275,7 @@ __device__ __forceinline__ void post_units(const SeqArrays &seqs, LineShape shap
     };
     bool ok = true;
     walk_part(
-        shape, seqs.b, p, e, p_len, p_units, p_x0,
+        shape, seqs.b, at.p, at.e, at.p_len, at.p_units, at.p_x0,
         [&](int i) {
             cur = seq_info(seqs, i);
             return SeqLen{cur.sq, cur.sk};

@@ -167,11 +167,13 @@ EXATTN_HD LineDeal line_deal(LineShape *s, const LineSum &t, int ctas) {
     return d;
 }
 
-// (r c and parts are below 2^17 and 2^9: the quotient of floats, half a unit
-// up, has the integer quotient's floor: it errs by 2^-13 at most, half a unit of
-// the numerator is more than 2^-10)
+// (r c and parts are below 2^16 and 2^8: the quotient of floats, half a unit
+// up, has the integer quotient's floor; MANY, for more parts: up to 2^15)
+template <bool MANY = false>
 EXATTN_HD int part_begin(const LineDeal &d, int c) {
 #if defined(__CUDA_ARCH__)
+    if (MANY)
+        return d.q * c + static_cast<int>(static_cast<uint32_t>(d.r * c) / static_cast<uint32_t>(smax(d.parts, 1)));
     return d.q * c + static_cast<int>(__fdividef(static_cast<float>(d.r * c) + 0.5f, static_cast<float>(d.parts)));
 #else
     return d.q * c + d.r * c / d.parts;
@@ -247,8 +249,9 @@ inline Place place_in_seq(const LineShape &s, int seq, int sq, int sk, int rem) 
 // steps, away from its ends: where it cuts it. The parts that share a unit are
 // the one before the first cut, and one per cut (part 0 begins at 0, where the
 // line begins: it cuts nothing, so there is one before).
+template <bool MANY = false>
 EXATTN_HD bool part_cuts(const LineShape &s, const LineDeal &d, int c, int x0, int cost, int n) {
-    const int x = part_begin(d, c) - x0;
+    const int x = part_begin<MANY>(d, c) - x0;
     if (x <= 0 || x >= cost) return false;
     const int t = place_step(s, x, cost, n);
     return t > 0 && t < n;
