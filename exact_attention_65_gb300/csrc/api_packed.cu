@@ -58,20 +58,22 @@ LineShape pack_line(int heads, int group, bool one_tile, bool causal, const Line
     return s;
 }
 
-// Few rows over a 4-bit cache: units of `tokens` tokens, dealt to warps: cut
-// wherever a warp's share ends, of two steps at least.
+// Few rows over a 4-bit cache: units of `tokens` tokens in steps of two tiles of
+// 16 keys, dealt to warps and cut wherever a warp's share ends. (Steps of 128 keys
+// left shares of 3 or 4 for one long sequence: TODO us against TODO.) A unit's fixed cost
+// counts as two steps; a share is four steps at least, for the join's sake.
 LineShape decode_q4_line(int heads, int tokens, bool causal, const LineBound &bound) {
     LineShape s;
     s.heads = heads;
     s.unit_len = tokens;
-    s.step_len = 128;
+    s.step_len = 32;
     s.causal = causal ? 1 : 0;
     s.by_key = 0;
     s.weight = 1;
-    s.shift = 7;
-    s.unit_cost = 1;
+    s.shift = 5;
+    s.unit_cost = 2;
     s.min_steps = 1;
-    s.min_part = 2;
+    s.min_part = 4;
     fit_line(&s, bound);
     return s;
 }

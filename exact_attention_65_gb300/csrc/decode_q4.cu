@@ -230,7 +230,7 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int tok0 = r.unit * a.tile_tokens;
     // the range's tiles, and the end of its keys
-    const int first = r.step0 * 8, end = min((r.step0 + r.nstep) * 8, (seq.sk + 15) >> 4);
+    const int first = r.step0 * 2, end = min((r.step0 + r.nstep) * 2, (seq.sk + 15) >> 4);
     const int limit = min(seq.sk, 16 * end);
 
     // ---- fetching: lane i knows the page of tile i of 32, and the next 32's;
@@ -288,6 +288,8 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
     look_up(first, &page, &row);
     look_up(first + 32, &page2, &row2);
     if (!(a.flags & kFlagSkipLoads)) refill();
+    int first_part = 0, nparts = 1;  // of a cut unit
+    if (r.slot >= 0) who_shares(shape, deal, r, &first_part, &nparts);
 
     // ---- queries: row n of the products is token n / group, head n % group
     uint32_t qf[NT][2 * G::J];
@@ -595,8 +597,6 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
 
     // ---- a cut unit. Results lie in the workspace as the lanes hold them.
     constexpr int V = G::J > 1 ? 2 : 1;  // products whose values a lane moves at once
-    int first_part, nparts;
-    who_shares(shape, deal, r, &first_part, &nparts);
     auto leave = [&](int64_t place) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -692,14 +692,14 @@ __global__ void __launch_bounds__(kWarps * 32, DecGeom<D, NT>::CTAS) decode_q4_k
         *abort_flag = 0u;
         fence_mbar_init();
     }
-    if (a.seqs.b > 32) line_sum_warps<0>(a.seqs, a.line, sums);  // (fewer: find_part does it alone)
+    if (a.seqs.b > 32) line_sum_warps<2>(a.seqs, a.line, sums);  // (fewer: find_part does it alone)
     __syncthreads();
     const WaitGuard g{abort_flag, a.status, kKernFwd};
     const uint32_t ring = sbase + warp * G::RING, landed = sbase + G::OFF_BAR + 8u * (warp * G::DEPTH);
     const int part = blockIdx.x * kWarps + warp;
     LineShape shape = a.line;
     LineDeal deal;
-    PartPlace at = find_part<0, true>(
+    PartPlace at = find_part<2, true>(
         a.seqs, shape, [&] { return line_total(sums, kWarps); }, part, gridDim.x * kWarps, &deal);
     TileRing q;
     walk_part(

@@ -78,10 +78,12 @@ static_assert(sizeof(UnitMsg) == 64, "four 16-byte words");
 
 constexpr int kMsgSlots = 4;
 
-// What each kernel knows of its line: half of the arithmetic's code.
+// What each kernel knows of its line: half of the arithmetic's code. BY_KEY 2: a
+// line over query tokens whose steps are not 128 keys.
 template <int BY_KEY>
 __device__ __forceinline__ void known_shape(LineShape *s) {
-    s->by_key = BY_KEY;
+    s->by_key = BY_KEY == 1;
+    if (BY_KEY == 2) return;
     if (BY_KEY) {
         s->unit_len = 128;
         s->unit_mul = 1u << 31;
@@ -149,7 +151,7 @@ __device__ __forceinline__ PartPlace find_part(const SeqArrays &seqs, LineShape 
         sum.units = __reduce_add_sync(0xffffffffu, shape.heads * n);
         const int longest = !ordered ? kOutOfOrder
                             : n == 0 ? 0
-                            : BY_KEY ? line_before(shape, x.sq, x.sk, 1)
+                            : BY_KEY == 1 ? line_before(shape, x.sq, x.sk, 1)
                                      : per - line_before(shape, x.sq, x.sk, n - 1);
         sum.longest = __reduce_max_sync(0xffffffffu, longest);
     } else {
