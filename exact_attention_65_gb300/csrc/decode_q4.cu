@@ -30,8 +30,9 @@
 // each takes its share of a unit's keys from its first tile to its last, and
 // ranges of a cut unit leave normalised fp32 O_i and LSE_i (log2) in the
 // workspace. The range that finishes last joins them in the order of the keys,
-// so the result does not depend on who that is; where there are more than
-// kJoin, in groups of so many first. (With a CTA's warps sharing every unit, and
+// so the result does not depend on who that is; those of a CTA's warps are joined
+// in shared memory first, and where more than kJoin are left, groups of so many.
+// (With a CTA's warps sharing every unit, and
 // joining in shared memory, 64 requests of 200 to 8192 keys took 83 us: a fifth
 // of it went into waiting for one another.)
 #include "packed.h"
@@ -43,7 +44,7 @@ namespace exattn {
 namespace {
 
 constexpr float kShift = 6.0f;  // P is 2^6 times the softmax's, at most 2^14
-constexpr int kJoin = 16;       // ranges joined at once
+constexpr int kJoin = 10;       // results joined at once
 constexpr int kWarps = kDecodeQ4Warps;
 
 template <int D, int NT>
@@ -62,7 +63,8 @@ struct DecGeom {
     static constexpr int OFF_BAR = kWarps * RING;       // [kWarps, DEPTH] a slot has landed
     static constexpr int OFF_SUM = OFF_BAR + kWarps * DEPTH * 8;
     static constexpr int OFF_MISC = OFF_SUM + kWarps * 12;
-    static constexpr int SMEM_BYTES = OFF_MISC + 16;
+    static constexpr int SMEM_BYTES = OFF_MISC + 16 + kWarps * 4;  // abort, arrivals of the CTA's warps
+    static_assert(RING >= ROWS * (D + 1) * 4, "a ring holds a range's results");
     static_assert(STAGE % 16 == 0 && (SMEM_BYTES + 1024) * CTAS <= 228 * 1024, "shared memory budget");
 };
 
@@ -224,8 +226,8 @@ __device__ __forceinline__ void who_shares(const LineShape &s, const LineDeal &d
 // A range of a unit: its tiles, and its results. False: a wait ran out.
 template <int D, bool BF16, int NT>
 __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &seq, const LineShape &shape,
-                                           const LineDeal &deal, int part, uint32_t ring, uint32_t landed, TileRing &q,
-                                           const PackArgs &a, const WaitGuard &guard) {
+                                           const LineDeal &deal, int part, uint8_t *smem, uint32_t ring,
+                                           uint32_t landed, TileRing &q, const PackArgs &a, const WaitGuard &guard) {
     using G = DecGeom<D, NT>;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int tok0 = r.unit * a.tile_tokens;
@@ -595,14 +597,15 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
         return true;
     }
 
-    // ---- a cut unit. Results lie in the workspace as the lanes hold them.
+    // ---- a cut unit. Results lie in memory as the lanes hold them: O_i [NT, 2,
+    // J, 32 lanes, 2] and LSE_i [ROWS].
     constexpr int V = G::J > 1 ? 2 : 1;  // products whose values a lane moves at once
-    auto leave = [&](int64_t place) {
+    auto leave = [&](float *o_to, float *lse_to) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float *dst = a.o_part + ((place * NT + nt) * 2 + e) * (G::J * 64) + lane * (2 * V);
+                float *dst = o_to + (nt * 2 + e) * (G::J * 64) + lane * (2 * V);
 #pragma unroll
                 for (int j = 0; j < G::J; j += V) {
                     if constexpr (V == 2)
@@ -611,13 +614,13 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
                     else
                         *reinterpret_cast<float2 *>(dst + j * 64) = make_float2(o[nt][j][e], o[nt][j][e + 2]);
                 }
-                if (g == 0) a.lse_part[place * G::ROWS + 8 * nt + 2 * t + e] = lse2[nt][e];
+                if (g == 0) lse_to[8 * nt + 2 * t + e] = lse2[nt][e];
             }
     };
-    // Joins n ranges, every `every`-th of the unit's parts from i0 on: with M the largest LSE_i, l =
-    // sum_i 2^(LSE_i - M), O = sum_i 2^(LSE_i - M) O_i / l, LSE = M + log2 l. Two at a
-    // time: bound by the latency of loads from L2.
-    auto gather = [&](int i0, int every, int n) {
+    // Joins n results, place(i, &o, &lse) says where the i-th lies: with M the
+    // largest LSE_i, l = sum_i 2^(LSE_i - M), O = sum_i 2^(LSE_i - M) O_i / l, LSE =
+    // M + log2 l. Two at a time: bound by the latency of loads from L2.
+    auto gather = [&](int n, auto place, auto load) {
         clear();
 #pragma unroll 1
         for (int i = 0; i < n; i += 2) {
@@ -626,19 +629,20 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
                 float v[2][2][G::J][2], lse[2][2];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const int64_t place = part_place(first_part, i0 + min(i + b, n - 1) * every);
+                    const float *o_from, *lse_from;
+                    place(min(i + b, n - 1), &o_from, &lse_from);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        lse[b][e] = __ldcg(a.lse_part + place * G::ROWS + 8 * nt + 2 * t + e);
-                        const float *src = a.o_part + ((place * NT + nt) * 2 + e) * (G::J * 64) + lane * (2 * V);
+                        lse[b][e] = load(lse_from + 8 * nt + 2 * t + e);
+                        const float *src = o_from + (nt * 2 + e) * (G::J * 64) + lane * (2 * V);
 #pragma unroll
                         for (int j = 0; j < G::J; j += V) {
                             if constexpr (V == 2) {
-                                const float4 y = __ldcg(reinterpret_cast<const float4 *>(src + j * 64));
+                                const float4 y = load(reinterpret_cast<const float4 *>(src + j * 64));
                                 v[b][e][j][0] = y.x, v[b][e][j][1] = y.y;
                                 v[b][e][j + 1][0] = y.z, v[b][e][j + 1][1] = y.w;
                             } else {
-                                const float2 y = __ldcg(reinterpret_cast<const float2 *>(src + j * 64));
+                                const float2 y = load(reinterpret_cast<const float2 *>(src + j * 64));
                                 v[b][e][j][0] = y.x, v[b][e][j][1] = y.y;
                             }
                         }
@@ -665,15 +669,51 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
         }
         finish(1.0f, 0.f);
     };
-    const int mine = part - first_part, group = mine / kJoin * kJoin;
-    leave(part_place(first_part, mine));
-    if (!warp_arrives_last(a.arrivals + part_place(first_part, group), a.call, min(kJoin, nparts - group))) return true;
-    gather(group, 1, min(kJoin, nparts - group));
-    if (nparts > kJoin) {
-        leave(part_place(first_part, group));
-        const int groups = (nparts + kJoin - 1) / kJoin;
+    // The CTA's warps whose shares end inside the unit have no more work: they
+    // leave their results in their rings, and the last one to come joins them.
+    // Entries of the unit's list: one for each CTA so, and its last part.
+    const int cta = part / kWarps, cta0 = first_part / kWarps, last = first_part + nparts - 1;
+    const int entries = (last - 1) / kWarps - cta0 + 2;
+    if (part != last) {
+        const int from = max(first_part, cta * kWarps), to = min(last - 1, cta * kWarps + kWarps - 1);
+        if (from < to) {
+            float *room = reinterpret_cast<float *>(smem + (part % kWarps) * G::RING);
+            leave(room, room + G::ROWS * D);
+            __threadfence_block();
+            __syncwarp();
+            int old = 0;
+            if (lane == 0)
+                old = atomicAdd(reinterpret_cast<int *>(smem + G::OFF_MISC + 16) + from % kWarps, 1);
+            if (__shfl_sync(0xffffffffu, old, 0) != to - from) return true;
+            __threadfence_block();
+            gather(to - from + 1, [&](int i, const float **o_from, const float **lse_from) {
+                *o_from = reinterpret_cast<const float *>(smem + ((from + i) % kWarps) * G::RING);
+                *lse_from = *o_from + G::ROWS * D;
+            }, [](const auto *p) { return *p; });
+        }
+    }
+    // where entry i of the unit lies: at the place of its first part
+    auto place = [&](int i) {
+        return part_place(first_part, i == entries - 1 ? nparts - 1 : max((cta0 + i) * kWarps - first_part, 0));
+    };
+    auto leave_entry = [&](int i) { leave(a.o_part + place(i) * (G::ROWS * D), a.lse_part + place(i) * G::ROWS); };
+    auto gather_entries = [&](int i0, int every, int n) {
+        gather(n, [&](int i, const float **o_from, const float **lse_from) {
+            const int64_t at = place(i0 + i * every);
+            *o_from = a.o_part + at * (G::ROWS * D);
+            *lse_from = a.lse_part + at * G::ROWS;
+        }, [](const auto *p) { return __ldcg(p); });
+    };
+    const int mine = part == last ? entries - 1 : cta - cta0, group = mine / kJoin * kJoin;
+    const int members = min(kJoin, entries - group);
+    leave_entry(mine);
+    if (!warp_arrives_last(a.arrivals + place(group), a.call, members)) return true;
+    gather_entries(group, 1, members);
+    if (entries > kJoin) {
+        leave_entry(group);
+        const int groups = (entries + kJoin - 1) / kJoin;
         if (!warp_arrives_last(a.arrivals + 2 * deal.parts + first_part, a.call, groups)) return true;
-        gather(0, kJoin, groups);
+        gather_entries(0, kJoin, groups);
     }
     write();
     return true;
@@ -690,6 +730,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecGeom<D, NT>::CTAS) decode_q4_k
     if (threadIdx.x == 0) {
         for (int i = 0; i < kWarps * G::DEPTH; ++i) mbar_init(sbase + G::OFF_BAR + 8u * i, G::B);
         *abort_flag = 0u;
+        for (int i = 0; i < kWarps; ++i) reinterpret_cast<int *>(smem + G::OFF_MISC + 16)[i] = 0;
         fence_mbar_init();
     }
     if (a.seqs.b > 32) line_sum_warps<2>(a.seqs, a.line, sums);  // (fewer: find_part does it alone)
@@ -709,7 +750,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecGeom<D, NT>::CTAS) decode_q4_k
             return SeqLen{at.cur.sq, at.cur.sk};
         },
         [&](const UnitRange &r) {
-            return take_range<D, BF16, NT>(r, at.cur, shape, deal, part, ring, landed, q, a, g);
+            return take_range<D, BF16, NT>(r, at.cur, shape, deal, part, smem, ring, landed, q, a, g);
         });
     // Never leave the CTA with a copy still landing (after a wait that ran out)
     WaitGuard drain = g;
