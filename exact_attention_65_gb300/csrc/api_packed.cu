@@ -451,7 +451,6 @@ attn_status_t fill_append(AppendArgs *a, const void *q, const void *k, const voi
     a->q_out_stride = q_out_stride / 8;
     a->h = h;
     a->h_kv = h_kv;
-    a->d = d;
     a->rot = rot;
     a->interleaved = interleaved ? 1 : 0;
     a->page_size = page_size;
@@ -461,12 +460,12 @@ attn_status_t fill_append(AppendArgs *a, const void *q, const void *k, const voi
     return ATTN_OK;
 }
 
-attn_status_t run_append(const AppendArgs &a, int dtype, bool q4, cudaStream_t stream) {
+attn_status_t run_append(const AppendArgs &a, int d, int dtype, bool q4, cudaStream_t stream) {
     int dev = 0, sms = 0;
     uint32_t *status = nullptr;
     const attn_status_t st = device_info(&dev, &status, &sms);
     if (st != ATTN_OK) return st;
-    return launch_append(a, dtype == ATTN_BF16, q4, sms, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    return launch_append(a, d, dtype == ATTN_BF16, q4, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace
@@ -800,7 +799,7 @@ attn_status_t attn_paged_append(const void *q, const void *k, const void *v, con
     const attn_status_t st =
         fill_append(&a, q, k, v, cos_sin, positions, slot_map, q_out, k_pages, v_pages, tokens, max_positions, rot,
                     interleaved, h, h_kv, d, num_pages, page_size, q_stride, k_stride, v_stride, q_out_stride, dtype);
-    return st == ATTN_OK ? run_append(a, dtype, false, stream) : st;
+    return st == ATTN_OK ? run_append(a, d, dtype, false, stream) : st;
 }
 
 attn_status_t attn_paged_append_q4(const void *q, const void *k, const void *v, const float *cos_sin,
@@ -821,7 +820,7 @@ attn_status_t attn_paged_append_q4(const void *q, const void *k, const void *v, 
     a.v_six = 6.0f * v_scale;
     a.block = q4_block_bytes(page_size, d);
     a.codes = static_cast<int64_t>(page_size) * q4_code_bytes(d);
-    return run_append(a, dtype, true, stream);
+    return run_append(a, d, dtype, true, stream);
 }
 
 attn_status_t attn_chunk_paged_q4(const void *q, const void *k_pages, const void *v_pages,
@@ -914,11 +913,10 @@ attn_status_t attn_paged_read_q4(const void *k_pages, const void *v_pages, const
     a.block = q4_block_bytes(page_size, d);
     a.codes = static_cast<int64_t>(page_size) * q4_code_bytes(d);
     a.h_kv = h_kv;
-    a.d = d;
     a.page_size = page_size;
     a.k_scale = k_scale;
     a.v_scale = v_scale;
-    return launch_read_q4(a, dtype == ATTN_BF16, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    return launch_read_q4(a, d, dtype == ATTN_BF16, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // extern "C"

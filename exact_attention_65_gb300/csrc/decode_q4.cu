@@ -57,8 +57,10 @@ struct DecGeom {
     static constexpr int SCALE_BYTES = 16 * q4_scale_bytes(D);
     static constexpr int OFF_KS = CODE_BYTES, OFF_V = OFF_KS + SCALE_BYTES, OFF_VS = OFF_V + CODE_BYTES;
     static constexpr int STAGE = OFF_VS + SCALE_BYTES;  // a tile: 16 keys
-    static constexpr int B = 2;                         // tiles that a warp takes at once
-    static constexpr int DEPTH = D == 128 ? 3 : 4;      // slots of B tiles of a warp's ring
+    // tiles that a warp takes at once, as many as registers allow (64 requests of 8192
+    // keys, h16/4 d64: 55 us with 2, 52 with 4)
+    static constexpr int B = D == 128 ? 2 : 4;
+    static constexpr int DEPTH = D == 128 ? 3 : 2;      // slots of B tiles of a warp's ring
     static constexpr int RING = (DEPTH * B * STAGE + 127) / 128 * 128;  // bytes
     static constexpr int OFF_BAR = kWarps * RING;       // [kWarps, DEPTH] a slot has landed
     static constexpr int OFF_SUM = OFF_BAR + kWarps * DEPTH * 8;
@@ -236,7 +238,7 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
     const int limit = min(seq.sk, 16 * end);
 
     // ---- fetching: lane i knows the page of tile i of 32, and the next 32's;
-    // lanes 0 and 1 fetch a slot's tiles
+    // lanes below B fetch a slot's tiles
     const int32_t *table = a.block_table + static_cast<int64_t>(r.seq) * a.max_pages;
     int page = 0, row = 0, page2 = 0, row2 = 0, issued = first;
     auto look_up = [&](int tile, int *pg, int *rw) {
@@ -255,7 +257,7 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
                 row = row2;
                 look_up(issued + 32, &page2, &row2);
             }
-            const int src = at + (lane & 1);
+            const int src = at + (lane & (G::B - 1));
             const int pg = __shfl_sync(0xffffffffu, page, src), rw = __shfl_sync(0xffffffffu, row, src);
             if (lane < G::B) {
                 const uint32_t bar = landed + 8u * q.put;
@@ -437,7 +439,8 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     top[nt][e] = fmaxf(s[0][nt][e], s[0][nt][e + 2]);
-                    if constexpr (G::B == 2) top[nt][e] = max3f(top[nt][e], s[1][nt][e], s[1][nt][e + 2]);
+#pragma unroll
+                    for (int b = 1; b < G::B; ++b) top[nt][e] = max3f(top[nt][e], s[b][nt][e], s[b][nt][e + 2]);
                     need = need || top[nt][e] > m[nt][e] + 8.0f;
                 }
             // The reference max moves when a tile exceeds it by more than 8 (log2)

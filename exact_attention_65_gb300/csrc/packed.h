@@ -150,14 +150,14 @@ struct AppendArgs {
     const int64_t *positions, *slot_map;  // [tokens]
     void *k_pages, *v_pages;
     int64_t tokens, max_positions, slots, q_stride, k_stride, v_stride, q_out_stride;
-    int h, h_kv, d, rot, interleaved, page_size;
+    int h, h_kv, rot, interleaved, page_size;
     // 4-bit pages: the tensors' scales, six times each, bytes of a page of a head
     // and of its codes
     float k_scale, v_scale, k_six, v_six;
     int64_t block, codes;
-    int lpr_log2, per_token, per_token_log2;  // set by the launch
+    int per_token, per_token_log2;  // set by the launch
 };
-cudaError_t launch_append(const AppendArgs &a, bool bf16, bool q4, int num_sms, cudaStream_t stream);
+cudaError_t launch_append(const AppendArgs &a, int d, bool bf16, bool q4, cudaStream_t stream);
 
 // Rows out of a 4-bit cache (append_paged.cu).
 struct ReadQ4Args {
@@ -165,10 +165,11 @@ struct ReadQ4Args {
     const int64_t *slot_map;  // [tokens]
     uint4 *k, *v;             // rows k_stride, v_stride 16-byte words apart
     int64_t tokens, slots, k_stride, v_stride, block, codes;
-    int h_kv, d, page_size, gpr_log2;
+    int h_kv, page_size;
+    int gpr_log2, wide;  // set by the launch
     float k_scale, v_scale;
 };
-cudaError_t launch_read_q4(const ReadQ4Args &a, bool bf16, cudaStream_t stream);
+cudaError_t launch_read_q4(const ReadQ4Args &a, int d, bool bf16, cudaStream_t stream);
 
 // 16-bit tensor with four dimensions, innermost first; strides in bytes of
 // dimensions 1 to 3.
