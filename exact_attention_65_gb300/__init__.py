@@ -681,25 +681,53 @@ def attn_paged_write(k, v, slot_map, k_pages, v_pages, stream=None):
 def _append_args(q, k, v, cos_sin, positions, slot_map, q_out, stream):
     """Sizes, strides, dtype code and device index of an append's rows, with
     its output. (Kept lean: a decode step's append issues in a few microseconds.)"""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
-        raise ValueError("q must be a CUDA tensor [tokens, h, d] (there is no CPU path)")
-    idx, dt = q.get_device(), q.dtype
-    code = _dtype_code(q)
-    qs, ks, vs = _rows("q", q, idx, dt), _rows("k", k, idx, dt), _rows("v", v, idx, dt)
-    t, h, d = q.shape
-    if k.shape != v.shape or k.shape[0] != t or k.shape[2] != d:
-        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
-    if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be a float32 tensor [max_positions, rot]")
-    _array("cos_sin", cos_sin, tuple(cos_sin.shape), idx, _F32)
-    _array("positions", positions, (t,), idx, _I64)
-    _array("slot_map", slot_map, (t,), idx, _I64)
-    if q_out is None:
-        q_out = _empty((t, h, d), dt, q.device, stream)
-    os = _rows("q_out", q_out, idx, dt)
-    if q_out.shape != q.shape:
-        raise ValueError("q_out must have q's shape")
-    return t, h, k.shape[1], d, qs, ks, vs, os, code, idx, q_out
+    try:
+        idx, dt = q.get_device(), q.dtype
+        t, h, d = q.shape
+        tk, hk, dk = k.shape
+        qs, q1, q2 = q.stride()
+        ks, k1, k2 = k.stride()
+        vs, v1, v2 = v.stride()
+        if q_out is None:
+            q_out = _empty((t, h, d), dt, q.device, stream)
+        os, o1, o2 = q_out.stride()
+        far, rot = cos_sin.shape
+        row, krow = h * d, hk * d
+        fine = (idx >= 0 and k.dtype is dt and v.dtype is dt and q_out.dtype is dt and cos_sin.dtype is _F32
+                and positions.dtype is _I64 and slot_map.dtype is _I64 and k.get_device() == idx
+                and v.get_device() == idx and q_out.get_device() == idx and cos_sin.get_device() == idx
+                and positions.get_device() == idx and slot_map.get_device() == idx and v.shape == k.shape
+                and tk == t and dk == d and q_out.shape == q.shape and positions.shape == (t,)
+                and slot_map.shape == (t,) and q2 == 1 and k2 == 1 and v2 == 1 and o2 == 1 and q1 == d and k1 == d
+                and v1 == d and o1 == d and qs >= row and os >= row and ks >= krow and vs >= krow
+                and (qs | os | ks | vs) % 8 == 0 and cos_sin.is_contiguous() and positions.is_contiguous()
+                and slot_map.is_contiguous())
+    except (AttributeError, ValueError, TypeError):
+        fine = False
+    if not fine:
+        if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
+            raise ValueError("q must be a CUDA tensor [tokens, h, d] (there is no CPU path)")
+        idx, dt = q.get_device(), q.dtype
+        qs, ks, vs = _rows("q", q, idx, dt), _rows("k", k, idx, dt), _rows("v", v, idx, dt)
+        t, h, d = q.shape
+        hk = k.shape[1]
+        if k.shape != v.shape or k.shape[0] != t or k.shape[2] != d:
+            raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
+        if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be a float32 tensor [max_positions, rot]")
+        far, rot = cos_sin.shape
+        _array("cos_sin", cos_sin, (far, rot), idx, _F32)
+        _array("positions", positions, (t,), idx, _I64)
+        _array("slot_map", slot_map, (t,), idx, _I64)
+        if q_out is None:
+            q_out = _empty((t, h, d), dt, q.device, stream)
+        os = _rows("q_out", q_out, idx, dt)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    code = _DTYPE_CODE.get(dt)
+    if code is None:
+        raise TypeError(f"exattn takes float16 or bfloat16 tensors, got {dt}")
+    return t, h, hk, d, far, rot, qs, ks, vs, os, code, idx, q_out
 
 
 def attn_paged_append(q, k, v, cos_sin, positions, slot_map, k_pages, v_pages, q_out=None,
@@ -717,14 +745,15 @@ def attn_paged_append(q, k, v, cos_sin, positions, slot_map, k_pages, v_pages, q
     a pair, instead of i and i + rot / 2. q_out: [tokens, h, d], also a slice
     of wider rows, or q itself. k_pages, v_pages: [num_pages, page_size, h_kv,
     d], written in place; they may not overlap the rows."""
-    t, h, hk, d, qs, ks, vs, os, code, idx, q_out = _append_args(q, k, v, cos_sin, positions, slot_map, q_out, stream)
+    t, h, hk, d, far, rot, qs, ks, vs, os, code, idx, q_out = _append_args(q, k, v, cos_sin, positions, slot_map,
+                                                                         q_out, stream)
     num_pages, page_size, ph, pd = _pools(k_pages, v_pages, idx, q.dtype)
     if ph != hk or pd != d:
         raise ValueError(f"shape mismatch: k {tuple(k.shape)}, pages {tuple(k_pages.shape)}")
     lib = _lib or load_library()
     rc = _call(lib.attn_paged_append, idx, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), cos_sin.data_ptr(),
                positions.data_ptr(), slot_map.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-               t, cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0, h, hk, d, num_pages, page_size, qs,
+               t, far, rot, 1 if interleaved else 0, h, hk, d, num_pages, page_size, qs,
                ks, vs, os, code)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_paged_append")
@@ -764,14 +793,15 @@ def attn_paged_append_q4(q, k, v, cos_sin, positions, slot_map, k_pages, v_pages
     and head, rows of e2m1 codes (two to a byte) and then rows of e4m3 scales,
     one for 16 channels. A value is code * scale * k_scale (v_scale); every
     call on a pool gets the same scales."""
-    t, h, hk, d, qs, ks, vs, os, code, idx, q_out = _append_args(q, k, v, cos_sin, positions, slot_map, q_out, stream)
+    t, h, hk, d, far, rot, qs, ks, vs, os, code, idx, q_out = _append_args(q, k, v, cos_sin, positions, slot_map,
+                                                                         q_out, stream)
     num_pages, ph, page_size = _pools_q4(k_pages, v_pages, d, idx)
     if ph != hk:
         raise ValueError(f"shape mismatch: k {tuple(k.shape)}, pages {tuple(k_pages.shape)}")
     lib = _lib or load_library()
     rc = _call(lib.attn_paged_append_q4, idx, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), cos_sin.data_ptr(),
                positions.data_ptr(), slot_map.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-               t, cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0, h, hk, d, num_pages, page_size, qs,
+               t, far, rot, 1 if interleaved else 0, h, hk, d, num_pages, page_size, qs,
                ks, vs, os, k_scale, v_scale, code)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_paged_append_q4")

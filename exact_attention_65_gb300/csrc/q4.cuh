@@ -78,6 +78,9 @@ __device__ __forceinline__ uint32_t q4_code_byte(float lo, float hi) {
     return r;
 }
 
+// Both halves of a pair of fp32 negated.
+__device__ __forceinline__ uint64_t f2_neg(uint64_t x) { return x ^ 0x8000000080000000ull; }
+
 // 16 bytes at a 16-byte-aligned shared-memory address.
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&r)[4]) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
