@@ -860,20 +860,30 @@ attn_status_t attn_chunk_paged_q4(const void *q, const void *k_pages, const void
     a.block4 = q4_block_bytes(page_size, d);
     a.v_scale4 = v_scale;
     // Few rows: a kernel that widens the codes in registers (64 requests of a
-    // token over up to 8192 keys, h32/8 d128: 92 us, on the two-tile form 199)
+    // token over up to 8192 keys, h32/8 d128: 66 us, on the two-tile form 199).
+    // Where a batch may mix them with chunks, each kernel takes its own sequences
+    // (16 requests with 512 tokens or one over up to 16384 keys: TODO us, all on the
+    // two-tile form 196).
     const int64_t longest = max_seqlen_q > 0 && max_seqlen_q < total_q ? max_seqlen_q : total_q;
-    const int rows = decode_q4_rows(longest * a.group);
+    const int all = decode_q4_rows(longest * a.group);
+    const int rows = all > 0 ? all : b > 1 && b * longest > total_q ? decode_q4_rows(a.group) : 0;
     if (rows > 0 && check_units(b, total_q, rows / a.group, h_kv) == ATTN_OK && h_kv * a.block4 <= 0xffffffffLL) {
-        a.q = q;
-        a.q_stride = q_stride;
-        a.tile_tokens = rows / a.group;
-        a.line = decode_q4_line(h_kv, a.tile_tokens, causal != 0, LineBound{b, total_q, max_k, max_k});
-        a.ctas = sms * decode_q4_ctas(rows);
-        a.page_bytes = static_cast<uint32_t>(h_kv * a.block4);
-        fast_division(page_size / 16, &a.page_mul, &a.page_div);
-        const int warps = a.ctas * kDecodeQ4Warps;
-        return run_with(&a, dev, d, static_cast<size_t>(warps) * 2 * rows, 3 * warps, stream,
-                        [&] { return launch_decode_q4(d, bf16, rows, a, stream); });
+        PackArgs few = a;
+        few.q = q;
+        few.q_stride = q_stride;
+        few.tile_tokens = rows / a.group;
+        few.line = decode_q4_line(h_kv, few.tile_tokens, causal != 0, LineBound{b, total_q, max_k, max_k});
+        few.ctas = sms * decode_q4_ctas(rows);
+        few.page_bytes = static_cast<uint32_t>(h_kv * a.block4);
+        fast_division(page_size / 16, &few.page_mul, &few.page_div);
+        if (all == 0) {
+            few.seqs.most = few.tile_tokens;
+            a.seqs.least = few.tile_tokens + 1;
+        }
+        const int warps = few.ctas * kDecodeQ4Warps;
+        st = run_with(&few, dev, d, static_cast<size_t>(warps) * 2 * rows, 3 * warps, stream,
+                      [&] { return launch_decode_q4(d, bf16, rows, few, stream); });
+        if (all > 0 || st != ATTN_OK) return st;
     }
     CUtensorMap tq;
     if (!encode_rows(&tq, q, bf16, d, h, h_kv, total_q, q_stride, a.tile_tokens)) return ATTN_ERR_CUDA;

@@ -20,6 +20,8 @@ struct SeqArrays {
     const int32_t *seqlens;  // [b] keys of each sequence (paged cache); nullptr for packed K/V
     int b, total_q;
     int max_k;  // key rows (packed), or the most keys a row of the block table holds (paged)
+    // a sequence with fewer or more query rows is another kernel's: no work here
+    int least = 0, most = 0x7fffffff;
 };
 
 // Grouped-head forward over packed or paged K/V (fwd_packed.cuh).

@@ -57,6 +57,7 @@ __device__ __forceinline__ SeqInfo seq_info(const SeqArrays &s, int i, bool *ord
         x.k0 = 0;
         x.sk = min(max(__ldg(s.seqlens + i), 0), s.max_k);
     }
+    if (x.sq < s.least || x.sq > s.most) x.sq = 0;
     if (ordered != nullptr) *ordered = in_order;
     return x;
 }
