@@ -307,13 +307,12 @@ void fill_pack(PackArgs *a, void *o, float *lse, int b, int total_q, int max_seq
     a->page_div = 0;
 }
 
-// Takes the workspace (`rows` rows of partial results, `counters` counters) and
-// launches.
 template <class Launch>
-attn_status_t run_with(PackArgs *a, int dev, int d, size_t rows, int counters, cudaStream_t stream, Launch launch) {
+attn_status_t run_pack(PackArgs *a, int dev, int d, cudaStream_t stream, Launch launch) {
+    const size_t rows = static_cast<size_t>(a->ctas) * 2 * (a->one_tile ? 1 : 2) * 128;
     Workspace w;
     const attn_status_t st =
-        get_workspace(dev, stream, counters, rows * (static_cast<size_t>(d) + 1) * sizeof(float), &w);
+        get_workspace(dev, stream, 2 * a->ctas, rows * (static_cast<size_t>(d) + 1) * sizeof(float), &w);
     if (st != ATTN_OK) return st;
     a->arrivals = w.arrivals;
     a->call = w.call;
@@ -322,12 +321,6 @@ attn_status_t run_with(PackArgs *a, int dev, int d, size_t rows, int counters, c
     const cudaError_t e = launch();
     const cudaError_t ef = w.owned ? cudaFreeAsync(w.owned, stream) : cudaSuccess;
     return (e == cudaSuccess && ef == cudaSuccess) ? ATTN_OK : ATTN_ERR_CUDA;
-}
-
-template <class Launch>
-attn_status_t run_pack(PackArgs *a, int dev, int d, cudaStream_t stream, Launch launch) {
-    const size_t rows = static_cast<size_t>(a->ctas) * 2 * (a->one_tile ? 1 : 2) * 128;
-    return run_with(a, dev, d, rows, 2 * a->ctas, stream, launch);
 }
 
 bool overlap(const void *p, size_t np, const void *q, size_t nq) {
@@ -862,13 +855,18 @@ attn_status_t attn_chunk_paged_q4(const void *q, const void *k_pages, const void
     // Few rows: a kernel that widens the codes in registers (64 requests of a
     // token over up to 8192 keys, h32/8 d128: 66 us, on the two-tile form 199).
     // Where a batch may mix them with chunks, each kernel takes its own sequences
-    // (16 requests with 512 tokens or one over up to 16384 keys: TODO us, all on the
+    // (16 requests with 512 tokens or one over up to 16384 keys: 166 us, all on the
     // two-tile form 196).
     const int64_t longest = max_seqlen_q > 0 && max_seqlen_q < total_q ? max_seqlen_q : total_q;
     const int all = decode_q4_rows(longest * a.group);
-    const int rows = all > 0 ? all : b > 1 && b * longest > total_q ? decode_q4_rows(a.group) : 0;
-    if (rows > 0 && check_units(b, total_q, rows / a.group, h_kv) == ATTN_OK && h_kv * a.block4 <= 0xffffffffLL) {
-        PackArgs few = a;
+    int rows = all > 0 ? all : b > 1 && b * longest > total_q ? decode_q4_rows(a.group) : 0;
+    if (rows > 0 && (check_units(b, total_q, rows / a.group, h_kv) != ATTN_OK || h_kv * a.block4 > 0xffffffffLL))
+        rows = 0;
+    const bool few_only = all > 0 && rows > 0;
+    PackArgs few = a;
+    CUtensorMap tq;
+    int warps = 0;  // of the few-row kernel
+    if (rows > 0) {
         few.q = q;
         few.q_stride = q_stride;
         few.tile_tokens = rows / a.group;
@@ -876,18 +874,31 @@ attn_status_t attn_chunk_paged_q4(const void *q, const void *k_pages, const void
         few.ctas = sms * decode_q4_ctas(rows);
         few.page_bytes = static_cast<uint32_t>(h_kv * a.block4);
         fast_division(page_size / 16, &few.page_mul, &few.page_div);
-        if (all == 0) {
-            few.seqs.most = few.tile_tokens;
-            a.seqs.least = few.tile_tokens + 1;
-        }
-        const int warps = few.ctas * kDecodeQ4Warps;
-        st = run_with(&few, dev, d, static_cast<size_t>(warps) * 2 * rows, 3 * warps, stream,
-                      [&] { return launch_decode_q4(d, bf16, rows, few, stream); });
-        if (all > 0 || st != ATTN_OK) return st;
+        warps = few.ctas * kDecodeQ4Warps;
     }
-    CUtensorMap tq;
-    if (!encode_rows(&tq, q, bf16, d, h, h_kv, total_q, q_stride, a.tile_tokens)) return ATTN_ERR_CUDA;
-    return run_pack(&a, dev, d, stream, [&] { return launch_chunk_q4(d, bf16, tq, a, stream); });
+    if (rows > 0 && !few_only) {
+        few.seqs.most = few.tile_tokens;
+        a.seqs.least = few.tile_tokens + 1;
+    }
+    if (!few_only && !encode_rows(&tq, q, bf16, d, h, h_kv, total_q, q_stride, a.tile_tokens)) return ATTN_ERR_CUDA;
+    // each kernel's part of the workspace: the second starts before the first is done
+    const size_t few_rows = static_cast<size_t>(warps) * 2 * rows;
+    const size_t pack_rows = few_only ? 0 : static_cast<size_t>(a.ctas) * 4 * 128;
+    Workspace w;
+    st = get_workspace(dev, stream, 3 * warps + (few_only ? 0 : 2 * a.ctas),
+                       (few_rows + pack_rows) * (static_cast<size_t>(d) + 1) * sizeof(float), &w);
+    if (st != ATTN_OK) return st;
+    few.arrivals = w.arrivals;
+    a.arrivals = w.arrivals + 3 * warps;
+    few.call = a.call = w.call;
+    few.o_part = reinterpret_cast<float *>(w.part);
+    few.lse_part = few.o_part + few_rows * d;
+    a.o_part = few.lse_part + few_rows;
+    a.lse_part = a.o_part + pack_rows * d;
+    cudaError_t e = rows > 0 ? launch_decode_q4(d, bf16, rows, few, stream) : cudaSuccess;
+    if (e == cudaSuccess && !few_only) e = launch_chunk_q4(d, bf16, tq, a, rows > 0, stream);
+    const cudaError_t ef = w.owned ? cudaFreeAsync(w.owned, stream) : cudaSuccess;
+    return (e == cudaSuccess && ef == cudaSuccess) ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 attn_status_t attn_paged_read_q4(const void *k_pages, const void *v_pages, const int64_t *slot_map, void *k, void *v,

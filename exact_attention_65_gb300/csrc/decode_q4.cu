@@ -730,6 +730,7 @@ __global__ void __launch_bounds__(kWarps * 32, DecGeom<D, NT>::CTAS) decode_q4_k
     const int warp = threadIdx.x >> 5;
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + G::OFF_MISC);
     LineSum *sums = reinterpret_cast<LineSum *>(smem + G::OFF_SUM);
+    griddep_launch_dependents();  // (the chunks' kernel touches nothing of this one's)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kWarps * G::DEPTH; ++i) mbar_init(sbase + G::OFF_BAR + 8u * i, G::B);
         *abort_flag = 0u;

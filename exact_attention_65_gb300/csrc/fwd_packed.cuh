@@ -1137,9 +1137,11 @@ __global__ void __launch_bounds__(PackThreads<Q4>::COUNT, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, G::TMEM_COLS);
+    // (the few-row kernel before it: what comes behind in the stream waits for this one)
+    if (Q4 && threadIdx.x == 0) griddep_wait();
 }
 
-template <int D, bool BF16, bool PAGED, bool ONE, bool Q4 = false>
+template <int D, bool BF16, bool PAGED, bool ONE>
 cudaError_t launch_pack_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const PackArgs &a,
                           cudaStream_t stream) {
     using G = PackGeom<D, ONE>;
@@ -1148,13 +1150,13 @@ cudaError_t launch_pack_t(const CUtensorMap &tq, const CUtensorMap &tk, const CU
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 64 && !attr_set[dev]) {
-        e = cudaFuncSetAttribute(pack_kernel<D, BF16, PAGED, ONE, Q4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(pack_kernel<D, BF16, PAGED, ONE, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  G::SMEM_BYTES);
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    pack_kernel<D, BF16, PAGED, ONE, Q4>
-        <<<a.ctas, PackThreads<Q4>::COUNT, G::SMEM_BYTES, stream>>>(tq, tk, tv, a);
+    pack_kernel<D, BF16, PAGED, ONE, false>
+        <<<a.ctas, PackThreads<false>::COUNT, G::SMEM_BYTES, stream>>>(tq, tk, tv, a);
     return cudaGetLastError();
 }
 

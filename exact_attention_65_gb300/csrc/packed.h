@@ -77,7 +77,9 @@ cudaError_t launch_fwd_packed(int d, bool bf16, const CUtensorMap &tq, const CUt
                               const CUtensorMap &tv, const PackArgs &a, cudaStream_t stream);
 cudaError_t launch_chunk_paged(int d, bool bf16, const CUtensorMap &tq, const CUtensorMap &tk,
                                const CUtensorMap &tv, const PackArgs &a, cudaStream_t stream);
-cudaError_t launch_chunk_q4(int d, bool bf16, const CUtensorMap &tq, const PackArgs &a, cudaStream_t stream);
+// early: may start while launch_decode_q4()'s kernel before it still runs
+cudaError_t launch_chunk_q4(int d, bool bf16, const CUtensorMap &tq, const PackArgs &a, bool early,
+                            cudaStream_t stream);
 // The most rows (tokens times a group's heads) of a unit of launch_decode_q4()
 // with so many rows to a request: 8 or 16, 0 where it has more. Its work is dealt
 // to four warps of each CTA; each leaves up to two ranges' O_i and LSE_i [warps, 2,
