@@ -874,7 +874,7 @@ attn_status_t attn_chunk_paged_q4(const void *q, const void *k_pages, const void
         few.ctas = sms * decode_q4_ctas(rows);
         few.page_bytes = static_cast<uint32_t>(h_kv * a.block4);
         fast_division(page_size / 16, &few.page_mul, &few.page_div);
-        warps = few.ctas * kDecodeQ4Warps;
+        warps = few.ctas * decode_q4_warps(rows);
     }
     if (rows > 0 && !few_only) {
         few.seqs.most = few.tile_tokens;

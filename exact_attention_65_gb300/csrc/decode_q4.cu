@@ -45,13 +45,12 @@ namespace {
 
 constexpr float kShift = 6.0f;  // P is 2^6 times the softmax's, at most 2^14
 constexpr int kJoin = 10;       // results joined at once
-constexpr int kWarps = kDecodeQ4Warps;
 
 template <int D, int NT>
 struct DecGeom {
-    // registers decide: 128 a thread for 16 warps an SM, 168 for 12
-    static constexpr int CTAS = NT == 1 ? 4 : 3;
     static constexpr int ROWS = 8 * NT;
+    // registers decide: 128 a thread for 16 warps an SM, 168 for 12
+    static constexpr int WARPS = decode_q4_warps(ROWS), CTAS = decode_q4_ctas(ROWS);
     static constexpr int J = D / 16;                    // products of 16 channels
     static constexpr int CODE_BYTES = 16 * q4_code_bytes(D);    // of a tile of K or V
     static constexpr int SCALE_BYTES = 16 * q4_scale_bytes(D);
@@ -62,10 +61,10 @@ struct DecGeom {
     static constexpr int B = D == 128 ? 2 : 4;
     static constexpr int DEPTH = D == 128 ? 3 : 2;      // slots of B tiles of a warp's ring
     static constexpr int RING = (DEPTH * B * STAGE + 127) / 128 * 128;  // bytes
-    static constexpr int OFF_BAR = kWarps * RING;       // [kWarps, DEPTH] a slot has landed
-    static constexpr int OFF_SUM = OFF_BAR + kWarps * DEPTH * 8;
-    static constexpr int OFF_MISC = OFF_SUM + kWarps * 12;
-    static constexpr int SMEM_BYTES = OFF_MISC + 16 + kWarps * 4;  // abort, arrivals of the CTA's warps
+    static constexpr int OFF_BAR = WARPS * RING;       // [WARPS, DEPTH] a slot has landed
+    static constexpr int OFF_SUM = OFF_BAR + WARPS * DEPTH * 8;
+    static constexpr int OFF_MISC = OFF_SUM + WARPS * 12;
+    static constexpr int SMEM_BYTES = OFF_MISC + 16 + WARPS * 4;  // abort, arrivals of the CTA's warps
     static_assert(RING >= ROWS * (D + 1) * 4, "a ring holds a range's results");
     static_assert(STAGE % 16 == 0 && (SMEM_BYTES + 1024) * CTAS <= 228 * 1024, "shared memory budget");
 };
@@ -622,16 +621,18 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
     };
     // Joins n results, place(i, &o, &lse) says where the i-th lies: with M the
     // largest LSE_i, l = sum_i 2^(LSE_i - M), O = sum_i 2^(LSE_i - M) O_i / l, LSE =
-    // M + log2 l. Two at a time: bound by the latency of loads from L2.
+    // M + log2 l. P at a time, as registers allow: bound by the latency of loads
+    // from L2.
+    constexpr int P = D == 128 ? 2 : 4;
     auto gather = [&](int n, auto place, auto load) {
         clear();
 #pragma unroll 1
-        for (int i = 0; i < n; i += 2) {
+        for (int i = 0; i < n; i += P) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float v[2][2][G::J][2], lse[2][2];
+                float v[P][2][G::J][2], lse[P][2];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
+                for (int b = 0; b < P; ++b) {
                     const float *o_from, *lse_from;
                     place(min(i + b, n - 1), &o_from, &lse_from);
 #pragma unroll
@@ -652,7 +653,7 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
                     }
                 }
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                for (int b = 0; b < P; ++b)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float x = i + b < n ? lse[b][e] : -INFINITY;
@@ -675,29 +676,29 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
     // The CTA's warps whose shares end inside the unit have no more work: they
     // leave their results in their rings, and the last one to come joins them.
     // Entries of the unit's list: one for each CTA so, and its last part.
-    const int cta = part / kWarps, cta0 = first_part / kWarps, last = first_part + nparts - 1;
-    const int entries = (last - 1) / kWarps - cta0 + 2;
+    const int cta = part / G::WARPS, cta0 = first_part / G::WARPS, last = first_part + nparts - 1;
+    const int entries = (last - 1) / G::WARPS - cta0 + 2;
     if (part != last) {
-        const int from = max(first_part, cta * kWarps), to = min(last - 1, cta * kWarps + kWarps - 1);
+        const int from = max(first_part, cta * G::WARPS), to = min(last - 1, cta * G::WARPS + G::WARPS - 1);
         if (from < to) {
-            float *room = reinterpret_cast<float *>(smem + (part % kWarps) * G::RING);
+            float *room = reinterpret_cast<float *>(smem + (part % G::WARPS) * G::RING);
             leave(room, room + G::ROWS * D);
             __threadfence_block();
             __syncwarp();
             int old = 0;
             if (lane == 0)
-                old = atomicAdd(reinterpret_cast<int *>(smem + G::OFF_MISC + 16) + from % kWarps, 1);
+                old = atomicAdd(reinterpret_cast<int *>(smem + G::OFF_MISC + 16) + from % G::WARPS, 1);
             if (__shfl_sync(0xffffffffu, old, 0) != to - from) return true;
             __threadfence_block();
             gather(to - from + 1, [&](int i, const float **o_from, const float **lse_from) {
-                *o_from = reinterpret_cast<const float *>(smem + ((from + i) % kWarps) * G::RING);
+                *o_from = reinterpret_cast<const float *>(smem + ((from + i) % G::WARPS) * G::RING);
                 *lse_from = *o_from + G::ROWS * D;
             }, [](const auto *p) { return *p; });
         }
     }
     // where entry i of the unit lies: at the place of its first part
     auto place = [&](int i) {
-        return part_place(first_part, i == entries - 1 ? nparts - 1 : max((cta0 + i) * kWarps - first_part, 0));
+        return part_place(first_part, i == entries - 1 ? nparts - 1 : max((cta0 + i) * G::WARPS - first_part, 0));
     };
     auto leave_entry = [&](int i) { leave(a.o_part + place(i) * (G::ROWS * D), a.lse_part + place(i) * G::ROWS); };
     auto gather_entries = [&](int i0, int every, int n) {
@@ -723,7 +724,7 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
 }
 
 template <int D, bool BF16, int NT>
-__global__ void __launch_bounds__(kWarps * 32, DecGeom<D, NT>::CTAS) decode_q4_kernel(const PackArgs a) {
+__global__ void __launch_bounds__(DecGeom<D, NT>::WARPS * 32, DecGeom<D, NT>::CTAS) decode_q4_kernel(const PackArgs a) {
     using G = DecGeom<D, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -732,20 +733,20 @@ __global__ void __launch_bounds__(kWarps * 32, DecGeom<D, NT>::CTAS) decode_q4_k
     LineSum *sums = reinterpret_cast<LineSum *>(smem + G::OFF_SUM);
     griddep_launch_dependents();  // (the chunks' kernel touches nothing of this one's)
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kWarps * G::DEPTH; ++i) mbar_init(sbase + G::OFF_BAR + 8u * i, G::B);
+        for (int i = 0; i < G::WARPS * G::DEPTH; ++i) mbar_init(sbase + G::OFF_BAR + 8u * i, G::B);
         *abort_flag = 0u;
-        for (int i = 0; i < kWarps; ++i) reinterpret_cast<int *>(smem + G::OFF_MISC + 16)[i] = 0;
+        for (int i = 0; i < G::WARPS; ++i) reinterpret_cast<int *>(smem + G::OFF_MISC + 16)[i] = 0;
         fence_mbar_init();
     }
     if (a.seqs.b > 32) line_sum_warps<2>(a.seqs, a.line, sums);  // (fewer: find_part does it alone)
     __syncthreads();
     const WaitGuard g{abort_flag, a.status, kKernFwd};
     const uint32_t ring = sbase + warp * G::RING, landed = sbase + G::OFF_BAR + 8u * (warp * G::DEPTH);
-    const int part = blockIdx.x * kWarps + warp;
+    const int part = blockIdx.x * G::WARPS + warp;
     LineShape shape = a.line;
     LineDeal deal;
     PartPlace at = find_part<2, true>(
-        a.seqs, shape, [&] { return line_total(sums, kWarps); }, part, gridDim.x * kWarps, &deal);
+        a.seqs, shape, [&] { return line_total(sums, G::WARPS); }, part, gridDim.x * G::WARPS, &deal);
     TileRing q;
     walk_part(
         shape, a.seqs.b, at.p, at.e, at.p_len, at.p_units, at.p_x0,
@@ -783,7 +784,7 @@ cudaError_t launch_t(const PackArgs &a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    decode_q4_kernel<D, BF16, NT><<<a.ctas, kWarps * 32, G::SMEM_BYTES, stream>>>(a);
+    decode_q4_kernel<D, BF16, NT><<<a.ctas, G::WARPS * 32, G::SMEM_BYTES, stream>>>(a);
     return cudaGetLastError();
 }
 

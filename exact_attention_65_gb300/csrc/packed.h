@@ -82,11 +82,11 @@ cudaError_t launch_chunk_q4(int d, bool bf16, const CUtensorMap &tq, const PackA
                             cudaStream_t stream);
 // The most rows (tokens times a group's heads) of a unit of launch_decode_q4()
 // with so many rows to a request: 8 or 16, 0 where it has more. Its work is dealt
-// to four warps of each CTA; each leaves up to two ranges' O_i and LSE_i [warps, 2,
-// rows], with three counters.
-inline int decode_q4_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 0; }
-inline int decode_q4_ctas(int rows) { return rows == 8 ? 4 : 3; }
-constexpr int kDecodeQ4Warps = 4;
+// to the warps of two CTAs an SM; each leaves up to two ranges' O_i and LSE_i
+// [warps, 2, rows], with three counters.
+constexpr int decode_q4_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 0; }
+constexpr int decode_q4_warps(int rows) { return rows == 8 ? 8 : 6; }
+constexpr int decode_q4_ctas(int rows) { return 2; }
 LineShape decode_q4_line(int heads, int tokens, bool causal, const LineBound &bound);
 cudaError_t launch_decode_q4(int d, bool bf16, int rows, const PackArgs &a, cudaStream_t stream);
 
