@@ -103,6 +103,8 @@ def load_library() -> ctypes.CDLL:
         lib.attn_q4_page_bytes.argtypes = [i32] * 2
         lib.attn_debug_packed_plan.restype = i32
         lib.attn_debug_packed_plan.argtypes = [vp, vp] + [i32] * 8 + [vp]
+        lib.attn_debug_few_plan.restype = i32
+        lib.attn_debug_few_plan.argtypes = [vp, vp] + [i32] * 7 + [vp]
         lib.attn_debug_packed_starts.restype = i32
         lib.attn_debug_packed_starts.argtypes = [vp, vp] + [i32] * 10 + [vp]
         lib.attn_debug_packed_shares.restype = i32

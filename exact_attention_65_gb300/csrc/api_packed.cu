@@ -344,7 +344,9 @@ namespace {
 
 // The plan of the line of these sequences for ctas CTAs, as the kernels make
 // it: rows of 9 ints (attn_debug_packed_plan). in_order: what the starts say.
-int plan_on_host(LineShape s, const std::vector<SeqLen> &seqs, bool in_order, int ctas, int max_ranges, int *out) {
+// few: as the few-row kernel over a 4-bit cache looks for who shares a unit.
+int plan_on_host(LineShape s, const std::vector<SeqLen> &seqs, bool in_order, int ctas, int max_ranges, int *out,
+                 bool few = false) {
     const int b = static_cast<int>(seqs.size());
     LineSum sum{0, 0, 0};
     for (const SeqLen &x : seqs) line_add(&sum, s, x.sq, x.sk, in_order);
@@ -368,8 +370,9 @@ int plan_on_host(LineShape s, const std::vector<SeqLen> &seqs, bool in_order, in
                   [&](int i) { return seqs[i]; },
                   [&](const UnitRange &r) {
                       if (n >= max_ranges) return false;
-                      int first = c, cuts = 0;
-                      for (int o = 0; r.slot >= 0 && o < d.parts; ++o)
+                      int first = c, cuts = 0, lo = 0, hi = d.parts - 1;
+                      if (few && r.slot >= 0) parts_inside(d, r.x0, r.cost, &lo, &hi);
+                      for (int o = lo; r.slot >= 0 && o <= hi; ++o)
                           if (part_cuts(s, d, o, r.x0, r.cost, r.steps) && cuts++ == 0) first = o - 1;
                       const int row[9] = {c, r.seq, r.head, r.unit, r.step0, r.nstep, r.slot, first, cuts + 1};
                       for (int i = 0; i < 9; ++i) out[9 * n + i] = row[i];
@@ -480,6 +483,27 @@ int attn_debug_packed_plan(const int *seqlens_q, const int *seqlens_k, int b, in
     const LineBound bound{b, static_cast<int>(all_q), all_k, all_k};
     return plan_on_host(plan_shape(h, h_kv, one_tile, causal, by_key, bound), seqs, true, ctas, max_ranges, out);
 } catch (...) {  // no exception leaves the library
+    return -1;
+}
+
+int attn_debug_few_plan(const int *seqlens_q, const int *seqlens_k, int b, int h, int h_kv, int rows, int causal,
+                        int warps, int max_ranges, int *out) try {
+    if (!plan_args_ok(seqlens_q, seqlens_k, out, b, h, h_kv, warps, max_ranges) || (rows != 8 && rows != 16) ||
+        h / h_kv > rows)
+        return -1;
+    int64_t all_q = 0, max_k = 0;
+    std::vector<SeqLen> seqs(b);
+    for (int i = 0; i < b; ++i) {
+        if (seqlens_q[i] < 0 || seqlens_k[i] < 0 || seqlens_k[i] > kMaxRows) return -1;
+        seqs[i] = SeqLen{seqlens_q[i], seqlens_k[i]};
+        all_q += seqlens_q[i];
+        if (seqlens_k[i] > max_k) max_k = seqlens_k[i];
+    }
+    if (all_q > kMaxRows) return -1;
+    const LineBound bound{b, static_cast<int>(all_q), max_k, max_k};
+    return plan_on_host(decode_q4_line(h_kv, rows / (h / h_kv), causal != 0, bound), seqs, true, warps, max_ranges, out,
+                        true);
+} catch (...) {
     return -1;
 }
 
@@ -859,8 +883,9 @@ attn_status_t attn_chunk_paged_q4(const void *q, const void *k_pages, const void
     // two-tile form 196).
     const int64_t longest = max_seqlen_q > 0 && max_seqlen_q < total_q ? max_seqlen_q : total_q;
     const int all = decode_q4_rows(longest * a.group);
-    int rows = all > 0 ? all : b > 1 && b * longest > total_q ? decode_q4_rows(a.group) : 0;
-    if (rows > 0 && (check_units(b, total_q, rows / a.group, h_kv) != ATTN_OK || h_kv * a.block4 > 0xffffffffLL))
+    // (equal lengths, all of them the longest, are no mix)
+    int rows = all > 0 ? all : b > 1 && b * longest != total_q ? decode_q4_rows(a.group) : 0;
+    if (rows > 0 && (check_units(b, total_q, rows / a.group, h_kv) != ATTN_OK || h_kv * a.block4 > 0x7fffffffLL))
         rows = 0;
     const bool few_only = all > 0 && rows > 0;
     PackArgs few = a;

@@ -102,10 +102,6 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
     return r;
 }
 
-__device__ __forceinline__ void sts8(uint32_t a) {
-    asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(0u) : "memory");
-}
-
 // c += a b: a 16 x 16 (rows), b 16 x 8 (columns), fp16, fp32 accumulators.
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -201,11 +197,8 @@ __device__ __forceinline__ int64_t part_place(int first, int i) {
 __device__ __forceinline__ void who_shares(const LineShape &s, const LineDeal &d, const UnitRange &r, int *first,
                                            int *nparts) {
     const int lane = threadIdx.x & 31;
-    // part c begins at floor(length c / parts): the first one behind x0, the last
-    // one before x0 + cost; those near the unit's ends cut nothing
-    const uint64_t p = static_cast<uint64_t>(d.parts), len = static_cast<uint64_t>(d.length);
-    const int lo = static_cast<int>((p * (r.x0 + 1) + len - 1) / len);
-    const int hi = static_cast<int>((p * (r.x0 + r.cost) + len - 1) / len) - 1;
+    int lo, hi;
+    parts_inside(d, r.x0, r.cost, &lo, &hi);
     int a = lo, z = hi;
     uint32_t in = 0;
 #pragma unroll 1
@@ -261,7 +254,7 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
             if (lane < G::B) {
                 const uint32_t bar = landed + 8u * q.put;
                 if (issued + lane < end) {
-                    // (a page of all heads is less than 2^32 bytes)
+                    // (a page of all heads is less than 2^31 bytes)
                     const uint8_t *kp = a.k4 + r.head * a.block4 +
                                         static_cast<uint64_t>(static_cast<uint32_t>(min(max(pg, 0), a.num_pages - 1))) *
                                             a.page_bytes;
@@ -405,7 +398,7 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
         };
         // P of the tiles from `tile` on, whose S is given, with the running max and sum
         uint32_t p[G::B][NT][2];
-        auto softmax = [&](int tile, uint32_t stage, float(&s)[G::B][NT][4]) {
+        auto softmax = [&](int tile, float(&s)[G::B][NT][4]) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -420,16 +413,6 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
                         for (int i = 0; i < 2 * G::B; ++i)
                             if (16 * (i >> 1) + 8 * (i & 1) >= sees) s[i >> 1][nt][2 * (i & 1) + e] = -INFINITY;
                     }
-                // P is 0 there, but a stale scale of V may be NaN: zeros in their place
-#pragma unroll
-                for (int b = 0; b < G::B; ++b) {
-                    const int left = max(limit - 16 * (tile + b), 0);  // keys of the tile
-#pragma unroll 1
-                    for (int i = left * q4_scale_bytes(D) + lane; i < G::SCALE_BYTES; i += 32)
-                        sts8(stage + b * G::STAGE + G::OFF_VS + i);
-                }
-                fence_proxy_async_smem();  // (before the slot's next copy)
-                __syncwarp();
             }
             float top[NT][2];
             bool need = false;
@@ -480,7 +463,11 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
             }
         };
         // O^T += V^T P^T of the tiles in a slot
-        auto values = [&](uint32_t stage) {
+        auto values = [&](int tile, uint32_t stage) {
+            // Scales are not negative, and a NaN (a key whose value is no number, or
+            // what lies behind the sequence) counts as 0 here: its product with a P
+            // of 0 would be NaN
+            uint32_t bad = 0;
 #pragma unroll
             for (int b = 0; b < G::B; ++b) {
                 const uint32_t at = stage + b * G::STAGE + G::OFF_V;
@@ -491,8 +478,10 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
                     const int k0 = key_of(2 * t) + 8 * half, k1 = key_of(2 * t + 1) + 8 * half;
                     load_v<D>(at, k0, g, w0);
                     load_v<D>(at, k1, g, w1);
-                    sv[half] = q4_scales_f16(load_vs<D>(at + G::CODE_BYTES, k0, g) |
-                                             load_vs<D>(at + G::CODE_BYTES, k1, g) << 8);
+                    const uint32_t read = q4_scales_f16(load_vs<D>(at + G::CODE_BYTES, k0, g) |
+                                                        load_vs<D>(at + G::CODE_BYTES, k1, g) << 8);
+                    sv[half] = h2_max0(read);
+                    bad |= read ^ sv[half];
 #pragma unroll
                     for (int i = 0; i < (D + 63) / 64; ++i) {
                         lo[half][i] = (w0[i] & 0x0f0f0f0fu) | ((w1[i] << 4) & 0xf0f0f0f0u);
@@ -518,6 +507,24 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
                     }
                 }
             }
+            if (__any_sync(0xffffffffu, bad != 0)) {
+                // the rows that see such a key come out as NaN
+#pragma unroll 1
+                for (int b = 0; b < G::B; ++b) {
+                    int lowest = 16;  // the first one of the tile
+#pragma unroll 1
+                    for (int i = lane; i < G::SCALE_BYTES; i += 32)
+                        if ((lds8(stage + b * G::STAGE + G::OFF_VS + i) & 0x7fu) == 0x7fu)
+                            lowest = min(lowest, i / q4_scale_bytes(D));
+                    lowest = __reduce_min_sync(0xffffffffu, lowest) + 16 * (tile + b);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (lowest < min(row_sees(8 * nt + 2 * t + e), 16 * (tile + b) + 16))
+                                l[nt][e] = __int_as_float(0x7fffffff);
+                }
+            }
         };
 #pragma unroll 1
         for (int tile = first; tile < end; tile += G::B) {
@@ -528,8 +535,8 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
             const uint32_t stage = ring + q.get * (G::B * G::STAGE);
             float s[G::B][NT][4];
             scores(stage, s);
-            softmax(tile, stage, s);
-            values(stage);
+            softmax(tile, s);
+            values(tile, stage);
             __syncwarp();
             if (++q.get == G::DEPTH) {
                 q.get = 0;

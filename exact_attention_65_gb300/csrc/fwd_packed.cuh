@@ -344,7 +344,9 @@ struct Q4Row {
 // Four warps widen K and V: thread r takes key r of each step, from the pages
 // through registers (both rows a step ahead) into row r of the ring's tile,
 // swizzled as TMA would leave it. Values are exact in either type; K takes Q's
-// type, V is fp16. Rows past the sequence's end are zeros.
+// type, V is fp16. Rows past the sequence's end are zeros. A key with a NaN in V
+// gets NaN as its K, which the rows that see it come to feel, and zeros in V, whose
+// product with a P of 0 would be NaN in the others.
 template <int D, bool BF16>
 __device__ __forceinline__ void pack_widen(uint32_t sbase, const UnitMsg *msgs, const PackArgs &a,
                                            const WaitGuard &g) {
@@ -386,10 +388,15 @@ __device__ __forceinline__ void pack_widen(uint32_t sbase, const UnitMsg *msgs, 
                 ok = ok && await(bar(G::BAR_KVE + ring.slot), ring.phase, g, 2);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 const uint32_t dst = sbase + G::OFF_KV + ring.slot * G::TILE_BYTES + row;
+                uint32_t bad = 0;
+#pragma unroll
+                for (int i = 0; i < (D + 63) / 64; ++i) bad |= q4_scales_nan(buf[1].scale[i]);
+                const uint32_t keep = bad == 0 ? 0xffffffffu : 0u;
 #pragma unroll
                 for (int i = 0; i < Q4Row<D>::WORDS; ++i) {
                     const uint32_t pair = q4_scales_f16(buf[kv].scale[i / 8] >> (16 * (i / 4 % 2)));
-                    const uint32_t s2 = __byte_perm(pair, 0, i / 2 % 2 ? 0x3232 : 0x1010);
+                    uint32_t s2 = __byte_perm(pair, 0, i / 2 % 2 ? 0x3232 : 0x1010);
+                    s2 = kv == 0 ? s2 | (~keep & 0x7fff7fffu) : s2 & keep;
                     uint32_t w[4];
                     q4_codes_f16(buf[kv].code[i], w);
 #pragma unroll

@@ -257,6 +257,15 @@ EXATTN_HD bool part_cuts(const LineShape &s, const LineDeal &d, int c, int x0, i
     return t > 0 && t < n;
 }
 
+// The parts [lo, hi] that begin inside a unit that begins at x0 and costs
+// `cost`: part c begins at floor(length c / parts). Of them, those near the
+// unit's ends may cut nothing (part_cuts()).
+EXATTN_HD void parts_inside(const LineDeal &d, int x0, int cost, int *lo, int *hi) {
+    const uint64_t p = static_cast<uint64_t>(d.parts), len = static_cast<uint64_t>(d.length);
+    *lo = static_cast<int>((p * (static_cast<uint64_t>(x0) + 1) + len - 1) / len);
+    *hi = static_cast<int>((p * (static_cast<uint64_t>(x0) + cost) + len - 1) / len) - 1;
+}
+
 // A sequence of the line: its query rows and keys.
 struct SeqLen {
     int sq, sk;

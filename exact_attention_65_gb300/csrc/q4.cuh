@@ -5,6 +5,7 @@
 // times the tensor's own fp32 scale. A code has 2 significant bits and s has 4:
 // code * s has at most 6 and lies within 2^-10 .. 2688, so it is exact in fp16
 // and in bf16 and a product with it loses nothing that a 16-bit cache keeps.
+// Scales are not negative; NaN stands for a group that held no number.
 //
 // A pool is [num_pages, h_kv, page_size * 9 d / 16] bytes. The block of a page
 // and head is contiguous: page_size rows of d / 2 bytes of codes (channel 2 i in
@@ -49,6 +50,16 @@ __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+
+// Both halves at least 0; NaN becomes 0.
+__device__ __forceinline__ uint32_t h2_max0(uint32_t a) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0u));
+    return r;
+}
+
+// Four scale bytes: not 0 if one of them is NaN.
+__device__ __forceinline__ uint32_t q4_scales_nan(uint32_t s) { return ((s & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
 // Both halves of a pair of fp16 as fp32.
 __device__ __forceinline__ float2 h2_float2(uint32_t x) {

@@ -425,7 +425,8 @@ attn_status_t attn_paged_append(const void *q, const void *k, const void *v, con
  * page of a head holds page_size rows of d / 2 bytes of codes (channel 2 i of
  * the row in the low half of byte i), then page_size rows of d / 16 scales.
  *   code   e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6, and 8 more with the sign
- *   scale  e4m3, one for 16 neighbouring channels of a row
+ *   scale  e4m3, not negative, one for 16 neighbouring channels of a row; NaN
+ *          stands for a group that held no number
  *   value  code * scale * (the tensor's scale, k_scale or v_scale)
  * page_size is a multiple of 16 (ATTN_ERR_UNSUPPORTED otherwise), k_scale and
  * v_scale lie within 2^-64 .. 2^64 (ATTN_ERR_INVALID_ARG otherwise), and every
@@ -461,8 +462,13 @@ attn_status_t attn_paged_append_q4(const void *q, const void *k, const void *v, 
  * attention over the cache's values.
  *   k_pages, v_pages  4-bit pools [num_pages, h_kv, page_bytes]; k_scale, v_scale
  *                     as attn_paged_append_q4 got them; scale * k_scale finite
- * Rows of a page past a request's end may hold anything. Other arguments,
- * results, workspace and errors as attn_chunk_paged.
+ *   max_seqlen_q      as in attn_fwd_packed; requests whose tokens make at most 16
+ *                     rows (tokens times h / h_kv) to a K/V head run on a
+ *                     kernel of their own, which is worth most where all do and
+ *                     this says so
+ * Rows of a page past a request's end may hold anything. A key with a scale of
+ * NaN in K or V makes the rows that see it NaN, O and LSE, and no others. Other
+ * arguments, results, workspace (at most 120 MB) and errors as attn_chunk_paged.
  */
 attn_status_t attn_chunk_paged_q4(const void *q, const void *k_pages, const void *v_pages,
                                   const int32_t *block_table, const int32_t *cu_seqlens_q,
@@ -620,6 +626,14 @@ int attn_debug_packed_plan(const int *seqlens_q, const int *seqlens_k, int b, in
                            int one_tile, int causal, int by_key, int ctas, int max_ranges, int *out);
 
 /*
+ * Test hook, host-side only: how attn_chunk_paged_q4 would deal requests with
+ * few rows to warps: units of floor(rows / (h / h_kv)) tokens (rows 8 or 16),
+ * steps of 32 keys. Otherwise as attn_debug_packed_plan, with warps for CTAs.
+ */
+int attn_debug_few_plan(const int *seqlens_q, const int *seqlens_k, int b, int h, int h_kv, int rows, int causal,
+                        int warps, int max_ranges, int *out);
+
+/*
  * Test hook, host-side only: attn_debug_packed_plan from starts as the kernels
  * read them (int32 [b + 1], whatever they hold) in tensors of total_q and
  * total_k rows: clamped, and nothing dealt out (0) where they are out of order.
@@ -637,7 +651,7 @@ int attn_debug_packed_starts(const int *cu_seqlens_q, const int *cu_seqlens_k, i
 int attn_debug_packed_shares(const int *seqlens_q, const int *seqlens_k, int b, int h, int h_kv,
                              int causal, int ctas, int *out);
 
-/* Library ABI version (major * 100 + minor): 104. */
+/* Library ABI version (major * 100 + minor): 105. */
 int attn_version(void);
 
 #ifdef __cplusplus
