@@ -902,8 +902,8 @@ attn_status_t attn_chunk_paged_q4(const void *q, const void *k_pages, const void
         warps = few.ctas * decode_q4_warps(rows);
     }
     if (rows > 0 && !few_only) {
-        few.seqs.most = few.tile_tokens;
-        a.seqs.least = few.tile_tokens + 1;
+        few.filter.most = few.tile_tokens;
+        a.filter.least = few.tile_tokens + 1;
     }
     if (!few_only && !encode_rows(&tq, q, bf16, d, h, h_kv, total_q, q_stride, a.tile_tokens)) return ATTN_ERR_CUDA;
     // each kernel's part of the workspace: the second starts before the first is done

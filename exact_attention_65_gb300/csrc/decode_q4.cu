@@ -745,20 +745,20 @@ __global__ void __launch_bounds__(DecGeom<D, NT>::WARPS * 32, DecGeom<D, NT>::CT
         for (int i = 0; i < G::WARPS; ++i) reinterpret_cast<int *>(smem + G::OFF_MISC + 16)[i] = 0;
         fence_mbar_init();
     }
-    if (a.seqs.b > 32) line_sum_warps<2>(a.seqs, a.line, sums);  // (fewer: find_part does it alone)
+    if (a.seqs.b > 32) line_sum_warps<2, true>(a.seqs, a.line, sums, a.filter);  // (fewer: find_part does it alone)
     __syncthreads();
     const WaitGuard g{abort_flag, a.status, kKernFwd};
     const uint32_t ring = sbase + warp * G::RING, landed = sbase + G::OFF_BAR + 8u * (warp * G::DEPTH);
     const int part = blockIdx.x * G::WARPS + warp;
     LineShape shape = a.line;
     LineDeal deal;
-    PartPlace at = find_part<2, true>(
-        a.seqs, shape, [&] { return line_total(sums, G::WARPS); }, part, gridDim.x * G::WARPS, &deal);
+    PartPlace at = find_part<2, true, true>(
+        a.seqs, shape, [&] { return line_total(sums, G::WARPS); }, part, gridDim.x * G::WARPS, &deal, a.filter);
     TileRing q;
     walk_part(
         shape, a.seqs.b, at.p, at.e, at.p_len, at.p_units, at.p_x0,
         [&](int i) {
-            at.cur = seq_info(a.seqs, i);
+            at.cur = seq_info<true>(a.seqs, i, nullptr, a.filter);
             return SeqLen{at.cur.sq, at.cur.sk};
         },
         [&](const UnitRange &r) {

@@ -863,7 +863,7 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
                             mx[i & 3] = max3f(mx[i & 3], s[2 * i], s[2 * i + 1]);
                     }
                     step(fmaxf(max3f(mx[0], mx[1], mx[2]), mx[3]));
-                    const float neg_m = P_SHIFT - m_ref;
+                    const float neg_m = Q4 ? P_SHIFT - m_ref : -m_ref;
                     const uint64_t c2 = f2_make(c, c), nm2 = f2_make(neg_m, neg_m);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
@@ -897,7 +897,7 @@ __device__ __forceinline__ void pack_softmax(uint8_t *smem, uint32_t sbase, uint
                             if (c0 + i < valid) mx[i & 1] = fmaxf(mx[i & 1], __uint_as_float(sr[i]));
                     }
                     step(fmaxf(mx[0], mx[1]));
-                    const float neg_m = P_SHIFT - m_ref;
+                    const float neg_m = Q4 ? P_SHIFT - m_ref : -m_ref;
                     const uint64_t c2 = f2_make(c, c), nm2 = f2_make(neg_m, neg_m);
 #pragma unroll 1
                     for (int c0 = 0; c0 < G::BN; c0 += 32) {
@@ -1099,7 +1099,7 @@ __global__ void __launch_bounds__(PackThreads<Q4>::COUNT, 1)
         tmem_alloc(smem_u32(tmem_slot), G::TMEM_COLS);
         tmem_relinquish();
     }
-    if (a.seqs.b > 32) line_sum_warps<0>(a.seqs, a.line, sums);  // (fewer: post_units does it alone)
+    if (a.seqs.b > 32) line_sum_warps<0, Q4>(a.seqs, a.line, sums, a.filter);  // (fewer: post_units does it alone)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1124,9 +1124,9 @@ __global__ void __launch_bounds__(PackThreads<Q4>::COUNT, 1)
                         pack_producer<D, PAGED, ONE, 1>(&tq, &tk, &tv, sbase, msgs, a, g);
             }
         } else {
-            post_units<0>(
+            post_units<0, Q4>(
                 a.seqs, a.line, [&] { return line_total(sums, T::COUNT / 32); }, msgs, bar(G::BAR_MF),
-                bar(G::BAR_ME), bar(G::BAR_MS), g, 18, blockIdx.x, gridDim.x);
+                bar(G::BAR_ME), bar(G::BAR_MS), g, 18, blockIdx.x, gridDim.x, a.filter);
         }
     } else if (Q4 && warp >= 12) {
         reg_dealloc<T::REGS_WIDEN>();

@@ -20,7 +20,10 @@ struct SeqArrays {
     const int32_t *seqlens;  // [b] keys of each sequence (paged cache); nullptr for packed K/V
     int b, total_q;
     int max_k;  // key rows (packed), or the most keys a row of the block table holds (paged)
-    // a sequence with fewer or more query rows is another kernel's: no work here
+};
+// A sequence with fewer or more query rows than this is another kernel's: no work
+// here.
+struct SeqFilter {
     int least = 0, most = 0x7fffffff;
 };
 
@@ -60,6 +63,7 @@ struct PackArgs {
     uint32_t page_bytes;
     uint32_t page_mul;
     int page_div;
+    SeqFilter filter;  // (over a 4-bit cache)
 };
 // Query tokens of a 128-row tile, and where work is cut.
 inline int pack_tile_tokens(int group) { return 128 / group; }

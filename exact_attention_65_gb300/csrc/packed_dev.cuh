@@ -48,7 +48,10 @@ struct SeqInfo {
     int q0, sq, k0, sk;
 };
 
-__device__ __forceinline__ SeqInfo seq_info(const SeqArrays &s, int i, bool *ordered = nullptr) {
+// SOME: only sequences that the filter lets pass have query rows here.
+template <bool SOME = false>
+__device__ __forceinline__ SeqInfo seq_info(const SeqArrays &s, int i, bool *ordered = nullptr,
+                                            SeqFilter filter = SeqFilter{}) {
     SeqInfo x;
     bool in_order = clamp_rows(__ldg(s.cu_q + i), __ldg(s.cu_q + i + 1), s.total_q, &x.q0, &x.sq);
     if (s.cu_k != nullptr) {
@@ -57,7 +60,7 @@ __device__ __forceinline__ SeqInfo seq_info(const SeqArrays &s, int i, bool *ord
         x.k0 = 0;
         x.sk = min(max(__ldg(s.seqlens + i), 0), s.max_k);
     }
-    if (x.sq < s.least || x.sq > s.most) x.sq = 0;
+    if (SOME && (x.sq < filter.least || x.sq > filter.most)) x.sq = 0;
     if (ordered != nullptr) *ordered = in_order;
     return x;
 }
@@ -98,14 +101,15 @@ __device__ __forceinline__ void known_shape(LineShape *s) {
 
 // The line's sums: every thread of the block adds some sequences, warp sums go
 // to `sums` (one LineSum per warp) for line_total() after a barrier.
-template <int BY_KEY>
-__device__ __forceinline__ void line_sum_warps(const SeqArrays &s, LineShape shape, LineSum *sums) {
+template <int BY_KEY, bool SOME = false>
+__device__ __forceinline__ void line_sum_warps(const SeqArrays &s, LineShape shape, LineSum *sums,
+                                               SeqFilter filter = SeqFilter{}) {
     known_shape<BY_KEY>(&shape);
     LineSum t{0, 0, 0};
 #pragma unroll 1
     for (int i = threadIdx.x; i < s.b; i += blockDim.x) {
         bool ordered;
-        const SeqInfo x = seq_info(s, i, &ordered);
+        const SeqInfo x = seq_info<SOME>(s, i, &ordered, filter);
         line_add(&t, shape, x.sq, x.sk, ordered);
     }
     t.cost = __reduce_add_sync(0xffffffffu, t.cost);
@@ -136,14 +140,14 @@ struct PartPlace {
 // Run by one warp: finds part `part` of the line dealt to `ctas` CTAs (or warps:
 // MANY, more than 512). total(): the line's sums where there are more than 32
 // sequences. Fits `shape` to the deal.
-template <int BY_KEY, bool MANY, class Total>
+template <int BY_KEY, bool MANY, bool SOME, class Total>
 __device__ __forceinline__ PartPlace find_part(const SeqArrays &seqs, LineShape &shape, Total total, int part, int ctas,
-                                               LineDeal *dealt) {
+                                               LineDeal *dealt, SeqFilter filter) {
     const int lane = threadIdx.x & 31;
     known_shape<BY_KEY>(&shape);
     SeqInfo x{0, 0, 0, 0};
     bool ordered = true;
-    if (lane < seqs.b) x = seq_info(seqs, lane, &ordered);
+    if (lane < seqs.b) x = seq_info<SOME>(seqs, lane, &ordered, filter);
     int n = line_units(shape, x.sq, x.sk);         // units of a head
     int per = line_before(shape, x.sq, x.sk, n);   // and their cost
     LineSum sum;
@@ -240,7 +244,7 @@ __device__ __forceinline__ PartPlace find_part(const SeqArrays &seqs, LineShape 
             i0 += 32;
             if (i0 >= seqs.b || before > want1) break;
             x = SeqInfo{0, 0, 0, 0};
-            if (i0 + lane < seqs.b) x = seq_info(seqs, i0 + lane);
+            if (i0 + lane < seqs.b) x = seq_info<SOME>(seqs, i0 + lane, nullptr, filter);
             n = line_units(shape, x.sq, x.sk);
             per = line_before(shape, x.sq, x.sk, n);
         }
@@ -252,13 +256,13 @@ __device__ __forceinline__ PartPlace find_part(const SeqArrays &seqs, LineShape 
 // posts its units. total(): the line's sums where there are more than 32
 // sequences. `full` / `empty` / `shared`: kMsgSlots barriers each; `site`:
 // where a timeout of the wait for a free message slot is recorded.
-template <int BY_KEY, class Total>
+template <int BY_KEY, bool SOME = false, class Total>
 __device__ __forceinline__ void post_units(const SeqArrays &seqs, LineShape shape, Total total, UnitMsg *msgs,
                                            uint32_t full, uint32_t empty, uint32_t shared, const WaitGuard &g,
-                                           uint32_t site, int part, int ctas) {
+                                           uint32_t site, int part, int ctas, SeqFilter filter = SeqFilter{}) {
     const int lane = threadIdx.x & 31;
     LineDeal deal;
-    PartPlace at = find_part<BY_KEY, false>(seqs, shape, total, part, ctas, &deal);
+    PartPlace at = find_part<BY_KEY, false, SOME>(seqs, shape, total, part, ctas, &deal, filter);
     SeqInfo &cur = at.cur;
 
     int posted = 0;
@@ -280,7 +284,7 @@ __device__ __forceinline__ void post_units(const SeqArrays &seqs, LineShape shap
     walk_part(
         shape, seqs.b, at.p, at.e, at.p_len, at.p_units, at.p_x0,
         [&](int i) {
-            cur = seq_info(seqs, i);
+            cur = seq_info<SOME>(seqs, i, nullptr, filter);
             return SeqLen{cur.sq, cur.sk};
         },
         [&](const UnitRange &r) {
