@@ -59,9 +59,14 @@ LineShape pack_line(int heads, int group, bool one_tile, bool causal, const Line
 }
 
 // Few rows over a 4-bit cache: units of `tokens` tokens in steps of two tiles of
-// 16 keys, dealt to warps and cut wherever a warp's share ends. (Steps of 128 keys
-// left shares of 3 or 4 for one long sequence: TODO us against TODO.) A unit's fixed cost
-// counts as two steps; a share is four steps at least, for the join's sake.
+// 16 keys, dealt to warps and cut wherever a warp's share ends. (With steps of
+// 128 keys shares are uneven: 64 requests of a token over up to 8192 keys took 70 us
+// so, 66 with 32.) A unit's fixed cost counts as two steps (one, three, four:
+// 67.7, 66.2, 66.5 us, and 300 requests of 200 keys 26, 35, 35). A share is four
+// steps at least, two where there are few units to spread (in a graph, h32/8 d128:
+// one token over 900 keys 16.4 us with 4, 15.0 with 2; four over 1500 17.4 and 15.4;
+// 300 requests of 200 keys 26 and 35, as units of up to twice that are not cut
+// where every one has a warp).
 LineShape decode_q4_line(int heads, int tokens, bool causal, const LineBound &bound) {
     LineShape s;
     s.heads = heads;
@@ -73,7 +78,7 @@ LineShape decode_q4_line(int heads, int tokens, bool causal, const LineBound &bo
     s.shift = 5;
     s.unit_cost = 2;
     s.min_steps = 1;
-    s.min_part = 4;
+    s.min_part = static_cast<int64_t>(bound.b) * heads <= 128 ? 2 : 4;
     fit_line(&s, bound);
     return s;
 }
