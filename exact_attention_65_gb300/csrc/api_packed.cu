@@ -881,6 +881,7 @@ attn_status_t attn_chunk_paged_q4(const void *q, const void *k_pages, const void
     a.v4 = static_cast<const uint8_t *>(v_pages);
     a.block4 = q4_block_bytes(page_size, d);
     a.v_scale4 = v_scale;
+    fast_division(page_size / 16, &a.page_mul, &a.page_div);
     // Few rows: a kernel that widens the codes in registers (64 requests of a
     // token over up to 8192 keys, h32/8 d128: 66 us, on the two-tile form 199).
     // Where a batch may mix them with chunks, each kernel takes its own sequences
@@ -903,7 +904,6 @@ attn_status_t attn_chunk_paged_q4(const void *q, const void *k_pages, const void
         few.line = decode_q4_line(h_kv, few.tile_tokens, causal != 0, LineBound{b, total_q, max_k, max_k});
         few.ctas = sms * decode_q4_ctas(rows);
         few.page_bytes = static_cast<uint32_t>(h_kv * a.block4);
-        fast_division(page_size / 16, &few.page_mul, &few.page_div);
         warps = few.ctas * decode_q4_warps(rows);
     }
     if (rows > 0 && !few_only) {

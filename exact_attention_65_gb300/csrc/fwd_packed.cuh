@@ -363,26 +363,37 @@ __device__ __forceinline__ void pack_widen(uint32_t sbase, const UnitMsg *msgs, 
 #pragma unroll 1
     for (int n = 0; ok && take_unit<true>(&x, n, msgs, bar(G::BAR_MF), bar(G::BAR_ME), g, 17); ++n) {
         const int32_t *table = a.block_table + static_cast<int64_t>(x.seq) * a.max_pages;
+        const int end = x.step0 + x.nstep;
         Q4Row<D> buf[2];
-        // this thread's row of K and V of step j
-        auto fetch = [&](int j, int kv) {
+        // The page and the row in it (-1: none) of this thread's key in the step
+        // that is fetched next, looked up a step before
+        int page = 0, at = -1;
+        auto look_up = [&](int j) {
             const int key = j * G::BN + r;
+            at = -1;
+            if (j < end && key < x.sk) {
+                const int p = divided(static_cast<uint32_t>(key) >> 4, a.page_mul, a.page_div);
+                at = key - p * a.page_size;
+                page = __ldg(table + p);
+            }
+        };
+        auto fetch = [&](int kv) {
             buf[kv].clear();
-            if (j < x.step0 + x.nstep && key < x.sk) {
-                const int p = static_cast<int>(static_cast<uint32_t>(key) / static_cast<uint32_t>(a.page_size));
-                const int page = min(max(__ldg(table + p), 0), a.num_pages - 1);
-                const int at = key - p * a.page_size;
+            if (at >= 0) {
                 const uint8_t *block =
-                    (kv ? a.v4 : a.k4) + (static_cast<int64_t>(page) * (a.h / a.group) + x.head) * a.block4;
+                    (kv ? a.v4 : a.k4) +
+                    (static_cast<int64_t>(min(max(page, 0), a.num_pages - 1)) * a.line.heads + x.head) * a.block4;
                 buf[kv].load(block + static_cast<int64_t>(at) * q4_code_bytes(D),
                              block + static_cast<int64_t>(a.page_size) * q4_code_bytes(D) +
                                  static_cast<int64_t>(at) * q4_scale_bytes(D));
             }
         };
-        fetch(x.step0, 0);
-        fetch(x.step0, 1);
+        look_up(x.step0);
+        fetch(0);
+        fetch(1);
+        look_up(x.step0 + 1);
 #pragma unroll 1
-        for (int j = x.step0; ok && j < x.step0 + x.nstep; ++j) {
+        for (int j = x.step0; ok && j < end; ++j) {
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
                 ok = ok && await(bar(G::BAR_KVE + ring.slot), ring.phase, g, 2);
@@ -413,8 +424,9 @@ __device__ __forceinline__ void pack_widen(uint32_t sbase, const UnitMsg *msgs, 
                 __syncwarp();
                 if ((threadIdx.x & 31) == 0) mbar_arrive(bar(G::BAR_KVF + ring.slot));
                 ring.next();
-                fetch(j + 1, kv);
+                fetch(kv);
             }
+            look_up(j + 2);
         }
     }
 }

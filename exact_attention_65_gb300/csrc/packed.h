@@ -56,13 +56,13 @@ struct PackArgs {
     const uint8_t *k4, *v4;
     int64_t block4;
     float v_scale4;
-    // few rows over a 4-bit cache (decode_q4.cu): q itself, bytes of a page of all
-    // heads, and tile / (tiles of 16 keys in a page) = tile * page_mul >> page_div
+    // ... and tile / (tiles of 16 keys in a page) = tile * page_mul >> page_div
+    uint32_t page_mul;
+    int page_div;
+    // few rows over it (decode_q4.cu): q itself, bytes of a page of all heads
     const void *q;
     int64_t q_stride;
     uint32_t page_bytes;
-    uint32_t page_mul;
-    int page_div;
     SeqFilter filter;  // (over a 4-bit cache)
 };
 // Query tokens of a 128-row tile, and where work is cut.
