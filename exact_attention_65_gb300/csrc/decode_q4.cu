@@ -32,9 +32,17 @@
 // workspace. The range that finishes last joins them in the order of the keys,
 // so the result does not depend on who that is; those of a CTA's warps are joined
 // in shared memory first, and where more than kJoin are left, groups of so many.
-// (With a CTA's warps sharing every unit, and
-// joining in shared memory, 64 requests of 200 to 8192 keys took 83 us: a fifth
-// of it went into waiting for one another.)
+// (With a CTA's warps sharing every unit and meeting at its end, 64 requests of 200
+// to 8192 keys took 83 us, a fifth of it waiting for one another; so 66.)
+//
+// Measured, h32/8 d128 with 16-key pages: 64 requests of 4096 keys 73 us, of 8192
+// 126, by the difference 5.7 TB/s, 86% of the copy bandwidth; the start takes 8 us
+// (to the first tiles of every warp) and uneven ends with the joins some 10. A warp
+// executes 316 instructions for 16 keys, 128 of them for widening, with the ALU pipe,
+// half of which they need, at 50%: what is left is the latency of their chains, which
+// 16 warps do not hide. Tried: 18 and 20 warps with fewer registers and a tile at a
+// time (4.0 TB/s), S of one slot beside O of the last (4.7), the softmax's scale
+// folded into one multiplication (the same).
 #include "packed.h"
 #include "packed_dev.cuh"
 #include "ptx.cuh"

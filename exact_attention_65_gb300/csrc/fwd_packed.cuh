@@ -29,6 +29,11 @@
 // still while it waited and counted (b1 s8192 h32 d128, no mask: 888 us with one,
 // 754 with two when they came in).
 //
+// Over a cache held in 4 bits (Q4, two tiles; chunk_q4.cu) four more warps, 12-15,
+// take the K and V producer's part: they widen rows from the pages into the ring.
+// A step takes 2.05 us there (two requests with 512 tokens over 16384 keys: 246 us,
+// over 16-bit pages 262).
+//
 // V rows of a unit's last tile that lie past the sequence belong to the next
 // sequence or are stale; P is 0 there, and 0 * NaN is NaN: the issuers zero
 // those below the next multiple of 16, where the P V product stops.
@@ -366,7 +371,8 @@ __device__ __forceinline__ void pack_widen(uint32_t sbase, const UnitMsg *msgs, 
         const int end = x.step0 + x.nstep;
         Q4Row<D> buf[2];
         // The page and the row in it (-1: none) of this thread's key in the step
-        // that is fetched next, looked up a step before
+        // that is fetched next, looked up a step before (five prompts of 1900
+        // tokens: 192 us, 200 with both loads one behind the other)
         int page = 0, at = -1;
         auto look_up = [&](int j) {
             const int key = j * G::BN + r;
