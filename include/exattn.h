@@ -442,9 +442,10 @@ int64_t attn_q4_page_bytes(int page_size, int d);
  * values: a group of 16 channels with largest magnitude m gets the scale s =
  * e4m3(m / (6 k_scale)), a channel x the code e2m1(x / (s k_scale)), each
  * rounded to the nearest with ties to even and limited to the largest value; s =
- * 0 has codes 0. A group that holds an infinity or a NaN gets the scale NaN, so
- * that what reads it gets NaN. The same slot twice leaves codes and scales of
- * both rows side by side. Other arguments and errors as attn_paged_append.
+ * 0 has codes of 0 with either sign. A group that holds an infinity or a NaN
+ * gets the scale NaN, so that what reads it gets NaN. The same slot twice leaves
+ * codes and scales of both rows side by side. Other arguments and errors as
+ * attn_paged_append.
  */
 attn_status_t attn_paged_append_q4(const void *q, const void *k, const void *v, const float *cos_sin,
                                    const int64_t *positions, const int64_t *slot_map, void *q_out,
