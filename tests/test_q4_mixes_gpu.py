@@ -125,6 +125,30 @@ def test_values_of_nan_reach_their_own_rows_only(gpu, oracle_mod, page):
         assert torch.equal(o[keep], clean[0][keep])
 
 
+@pytest.mark.parametrize("d,dtype", [(128, torch.bfloat16), (64, torch.float16), (16, torch.bfloat16)])
+@pytest.mark.parametrize("key", [1, 255, 256, 399, 499])
+def test_values_of_nan_in_a_chunk(gpu, oracle_mod, d, dtype, key):
+    """The same of a chunk's rows, from the first that sees the key on, with a token of another request beside it."""
+    lens, new, h, h_kv, page = [500, 90], [400, 1], 6, 2, 48
+    kp, vp, table, k, v = make_cache(oracle_mod, lens, h_kv, d, page, 1.0, 1.0, 12)
+    q = torch.randn((401, h, d), generator=torch.Generator().manual_seed(5)).to(dtype).cuda()
+    args = (table.cuda(), ints(starts(new)), ints(lens))
+    for hint in (400, 0):
+        clean = gpu.attn_chunk_paged_q4(q, kp.cuda(), vp.cuda(), *args, hint, causal=True)
+        slot = int(table[0, key // page]) * page + key % page
+        for pool in (kp, vp):
+            bad = pool.clone()
+            bad[slot // page, 1, page * d // 2 + slot % page * (d // 16) + d // 16 - 1] = 127
+            o, lse = gpu.attn_chunk_paged_q4(q, *(bad.cuda() if x is pool else x.cuda() for x in (kp, vp)), *args,
+                                             hint, causal=True)
+            assert gpu.attn_get_device_status() == gpu.ATTN_OK
+            want = torch.zeros((401, h), dtype=torch.bool, device="cuda")
+            want[max(key - 100, 0):400, 3:] = True  # row i of the chunk is token 100 + i
+            assert torch.equal(torch.isnan(o.float()).any(-1), want)
+            assert torch.equal(torch.isnan(lse).T, want)
+            assert torch.equal(o[~want], clean[0][~want]) and torch.equal(lse.T[~want], clean[1].T[~want])
+
+
 def test_another_device_index_and_wrong_shapes(gpu):
     """The binding's own refusals."""
     q = torch.zeros((2, 4, 64), dtype=torch.float16, device="cuda")
