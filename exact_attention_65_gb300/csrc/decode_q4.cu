@@ -129,15 +129,34 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 // The key in its tile that row r of the products stands for.
 __device__ __forceinline__ int key_of(int r) { return r ^ (r >> 2 & 1); }
 
-// As arrive_last(), by a warp whose results are written.
+// As arrive_last(), by a warp whose results are written. Lane 0 counts for all
+// of them: the barriers order the other lanes' stores before its fence, and its
+// second fence before their loads (a shuffle alone orders no memory).
 __device__ __forceinline__ bool warp_arrives_last(uint32_t *counter, uint32_t call, int n) {
-    __threadfence();
     __syncwarp();
     int last = 0;
-    if ((threadIdx.x & 31) == 0) last = arrive_last(counter, call, n);
+    if ((threadIdx.x & 31) == 0) {
+        __threadfence();
+        last = arrive_last(counter, call, n);
+        __threadfence();
+    }
     last = __shfl_sync(0xffffffffu, last, 0);
-    if (last) __threadfence();
+    __syncwarp();
     return last != 0;
+}
+
+// The same among a CTA's warps, for results in shared memory.
+__device__ __forceinline__ bool warp_arrives_last_in_cta(int *counter, int n) {
+    __syncwarp();
+    int old = 0;
+    if ((threadIdx.x & 31) == 0) {
+        __threadfence_block();
+        old = atomicAdd(counter, 1);
+        __threadfence_block();
+    }
+    old = __shfl_sync(0xffffffffu, old, 0);
+    __syncwarp();
+    return old == n - 1;
 }
 
 // A lane's codes of one key for S: D / 4 channels, a word for 8.
@@ -698,13 +717,9 @@ __device__ __forceinline__ bool take_range(const UnitRange &r, const SeqInfo &se
         if (from < to) {
             float *room = reinterpret_cast<float *>(smem + (part % G::WARPS) * G::RING);
             leave(room, room + G::ROWS * D);
-            __threadfence_block();
-            __syncwarp();
-            int old = 0;
-            if (lane == 0)
-                old = atomicAdd(reinterpret_cast<int *>(smem + G::OFF_MISC + 16) + from % G::WARPS, 1);
-            if (__shfl_sync(0xffffffffu, old, 0) != to - from) return true;
-            __threadfence_block();
+            if (!warp_arrives_last_in_cta(reinterpret_cast<int *>(smem + G::OFF_MISC + 16) + from % G::WARPS,
+                                          to - from + 1))
+                return true;
             gather(to - from + 1, [&](int i, const float **o_from, const float **lse_from) {
                 *o_from = reinterpret_cast<const float *>(smem + ((from + i) % G::WARPS) * G::RING);
                 *lse_from = *o_from + G::ROWS * D;
