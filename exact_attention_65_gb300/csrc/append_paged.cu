@@ -232,8 +232,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
                 const uint32_t sb = m[n] == INFINITY ? 0x7fu : q4_scale_byte(__fdiv_rn(m[n], six));
                 const float unit = h2_float2(q4_scales_f16(sb)).x * scale;
                 // x / unit, corrected once: exact where x is a border between two codes,
-                // so that ties go to the even one. (At most 6 times 17 / 16 unless
-                // the scale is at its largest.)
+                // so that ties go to the even one. Its magnitude is at most 6 times 17 / 16
+                // where the scale is a normal number, and below 9 where it is not (m / six
+                // just below 1.5 2^-9 rounds to 2^-9): the conversion to codes saturates.
+                // The largest scale bounds nothing, and there x is limited first.
                 const float inv = unit > 0.f ? __frcp_rn(unit) : 0.f;
                 if (sb == 0x7eu) {
 #pragma unroll
