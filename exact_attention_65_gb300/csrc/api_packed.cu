@@ -66,7 +66,9 @@ LineShape pack_line(int heads, int group, bool one_tile, bool causal, const Line
 // steps at least, two where there are few units to spread (in a graph, h32/8 d128:
 // one token over 900 keys 16.4 us with 4, 15.0 with 2; four over 1500 17.4 and 15.4;
 // 300 requests of 200 keys 26 and 35, as units of up to twice that are not cut
-// where every one has a warp).
+// where every one has a warp). The 128 units that separate the two lie between the
+// 8 and the 2400 of these cases; nothing was measured near them, and the requests of
+// a mixed batch that the other kernel takes count as well.
 LineShape decode_q4_line(int heads, int tokens, bool causal, const LineBound &bound) {
     LineShape s;
     s.heads = heads;
@@ -886,7 +888,9 @@ attn_status_t attn_chunk_paged_q4(const void *q, const void *k_pages, const void
     // token over up to 8192 keys, h32/8 d128: 66 us, on the two-tile form 199).
     // Where a batch may mix them with chunks, each kernel takes its own sequences
     // (16 requests with 512 tokens or one over up to 16384 keys: 166 us, all on the
-    // two-tile form 196).
+    // two-tile form 196). Its units are for a token there, so that requests with more
+    // than 8 rows (16 in groups above 8) count as chunks: 16 requests of which two bring
+    // 512 tokens take 124 us where the others bring one, 180 where they bring four.
     const int64_t longest = max_seqlen_q > 0 && max_seqlen_q < total_q ? max_seqlen_q : total_q;
     const int all = decode_q4_rows(longest * a.group);
     // (equal lengths, all of them the longest, are no mix)

@@ -1,5 +1,6 @@
 // A few new rows of each request over a cache held in 4 bits
-// (attn_chunk_paged_q4 where no request has more than 16 rows to a K/V head).
+// (attn_chunk_paged_q4: all requests where none is said to have more than 16 rows to
+// a K/V head; in other batches those with up to 8, or a token of up to 16).
 //
 // The mathematics is the forward's: S = scale Q K^T, an online softmax, O = P V,
 // and per key 1.125 bytes of K and V a channel are read once. What bounds it is
@@ -57,7 +58,9 @@ constexpr int kJoin = 10;       // results joined at once
 template <int D, int NT>
 struct DecGeom {
     static constexpr int ROWS = 8 * NT;
-    // registers decide: 128 a thread for 16 warps an SM, 168 for 12
+    // registers decide: 128 a thread for 16 warps an SM, 168 for 12 (D = 128 spills 40
+    // to 52 bytes with 8 rows, in the joins only; with 16 rows 224, 196 without the
+    // joins, and D = 64 52 to 76, 40 without)
     static constexpr int WARPS = decode_q4_warps(ROWS), CTAS = decode_q4_ctas(ROWS);
     static constexpr int J = D / 16;                    // products of 16 channels
     static constexpr int CODE_BYTES = 16 * q4_code_bytes(D);    // of a tile of K or V

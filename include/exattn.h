@@ -463,10 +463,14 @@ attn_status_t attn_paged_append_q4(const void *q, const void *k, const void *v, 
  * attention over the cache's values.
  *   k_pages, v_pages  4-bit pools [num_pages, h_kv, page_bytes]; k_scale, v_scale
  *                     as attn_paged_append_q4 got them; scale * k_scale finite
- *   max_seqlen_q      as in attn_fwd_packed; requests whose tokens make at most 16
- *                     rows (tokens times h / h_kv) to a K/V head run on a
- *                     kernel of their own, which is worth most where all do and
- *                     this says so
+ *   max_seqlen_q      as in attn_fwd_packed. Requests with few rows to a K/V head
+ *                     (tokens times h / h_kv) run on a kernel of their own, the
+ *                     others on one for chunks. Where this says that no request
+ *                     has more than 16 rows, all of them do; in other batches of
+ *                     several requests those with at most floor(8 / (h / h_kv))
+ *                     tokens, or with one token where h / h_kv is 9 to 16. So give
+ *                     it: 64 requests with four tokens each over up to 8192 keys,
+ *                     h32 on 8, take 95 us with it and 199 without.
  * Rows of a page past a request's end may hold anything. A key with a scale of
  * NaN in K or V makes the rows that see it NaN, O and LSE, and no others. Other
  * arguments, results, workspace (at most 120 MB) and errors as attn_chunk_paged.
@@ -479,10 +483,11 @@ attn_status_t attn_chunk_paged_q4(const void *q, const void *k_pages, const void
                                   float v_scale, int causal, attn_dtype_t dtype, cudaStream_t stream);
 
 /*
- * Rows of a 4-bit cache back in 16 bits: row slot_map[t] of the pools, rounded
- * once, to row t of k and v [tokens, h_kv, d] (token strides as above); zeros
- * where the slot is outside the pools. A slot may come up several times. Errors
- * as attn_fwd.
+ * Rows of a 4-bit cache back in 16 bits: row slot_map[t] of the pools to row t
+ * of k and v [tokens, h_kv, d] (token strides as above); zeros where the slot is
+ * outside the pools. A value is rounded once where the tensor's scale is a power of
+ * two; with another one the product with it is rounded to fp32 before. A slot
+ * may come up several times. Errors as attn_fwd.
  */
 attn_status_t attn_paged_read_q4(const void *k_pages, const void *v_pages, const int64_t *slot_map,
                                  void *k, void *v, int64_t tokens, int h_kv, int d, int num_pages,
