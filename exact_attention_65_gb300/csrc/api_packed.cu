@@ -889,8 +889,8 @@ attn_status_t attn_chunk_paged_q4(const void *q, const void *k_pages, const void
     // Where a batch may mix them with chunks, each kernel takes its own sequences
     // (16 requests with 512 tokens or one over up to 16384 keys: 166 us, all on the
     // two-tile form 196). Its units are for a token there, so that requests with more
-    // than 8 rows (16 in groups above 8) count as chunks: 16 requests of which two bring
-    // 512 tokens take 124 us where the others bring one, 180 where they bring four.
+    // than 8 rows (16 in groups above 8) count as chunks: 16 requests over 108529 keys, of
+    // which two bring 512 tokens, take 124 us where the others bring one, 180 where four.
     const int64_t longest = max_seqlen_q > 0 && max_seqlen_q < total_q ? max_seqlen_q : total_q;
     const int all = decode_q4_rows(longest * a.group);
     // (equal lengths, all of them the longest, are no mix)
